@@ -32,7 +32,11 @@ EXPORTED = ("gdr_validate", "gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd_debug
             "gdr_chunk_bwd_workspace_size", "gdr_chunk_bwd",
             "gdr_status_string", "gdr_last_error_message",
             "gdr_peak_copy", "gdr_peak_mfma", "gdr_peak_mfma_flops",
-            "gdr_chunk_fwd_noalloc", "gdr_chunk_fwd_noalloc_max_workspace")
+            "gdr_chunk_fwd_noalloc", "gdr_chunk_fwd_noalloc_max_workspace",
+            "gdr_conv_fwd", "gdr_conv_step", "gdr_conv_bwd", "gdr_conv_bwd_workspace_size",
+            "gdr_scan_fwd", "gdr_scan_fwd_workspace_size", "gdr_scan_step", "gdr_scan_bwd",
+            "gdr_scan_bwd_workspace_size", "gdr_layer_norm_fwd", "gdr_layer_norm_bwd",
+            "gdr_layer_norm_bwd_workspace_size")
 
 
 class Problem(ctypes.Structure):
@@ -49,6 +53,29 @@ class Intermediates(ctypes.Structure):
                 ("U", ctypes.c_void_p), ("KT", ctypes.c_void_p), ("H", ctypes.c_void_p),
                 ("VN", ctypes.c_void_p), ("T", ctypes.c_void_p), ("P", ctypes.c_void_p),
                 ("R", ctypes.c_void_p), ("num_chunks", ctypes.c_int64)]
+
+
+class ConvProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seq_len", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int32), ("channels", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("dy_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class ScanProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seq_len", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("c_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("state_dim", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("cols", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class GdrError(RuntimeError):
@@ -101,6 +128,17 @@ def load_library():
     lib.gdr_peak_mfma.restype = ctypes.c_int
     lib.gdr_peak_mfma_flops.argtypes = [ctypes.c_int32, ctypes.c_int32]
     lib.gdr_peak_mfma_flops.restype = ctypes.c_double
+    CP, SP, NP = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(NormProblem)
+    Z, PZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    for name, types in (("gdr_conv_fwd", [CP] + [P] * 9), ("gdr_conv_step", [CP] + [P] * 6),
+                        ("gdr_conv_bwd", [CP] + [P] * 13 + [Z, P]), ("gdr_conv_bwd_workspace_size", [CP, PZ]),
+                        ("gdr_scan_fwd", [SP] + [P] * 14 + [Z, P]), ("gdr_scan_fwd_workspace_size", [SP, PZ]),
+                        ("gdr_scan_step", [SP] + [P] * 11), ("gdr_scan_bwd", [SP] + [P] * 23 + [Z, P]),
+                        ("gdr_scan_bwd_workspace_size", [SP, PZ]), ("gdr_layer_norm_fwd", [NP] + [P] * 7),
+                        ("gdr_layer_norm_bwd", [NP] + [P] * 9 + [Z, P]),
+                        ("gdr_layer_norm_bwd_workspace_size", [NP, PZ])):
+        getattr(lib, name).argtypes = types
+        getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libgdr.so")
 SOURCES = ["gdr_api.hip", "gdr_kernels.hip", "gdr_fp16.hip", "gdr_recurrent.hip", "gdr_backward.hip",
-           "gdr_peaks.hip"]
+           "gdr_peaks.hip", "gdr_mixer_api.hip", "gdr_conv.hip", "gdr_norm.hip", "gdr_scan.hip", "gdr_scan_bwd.hip"]
 # per-file options: the matrix-core loops of these files keep their accumulators
 # in VGPRs (without it the compiler moves loop-carried accumulators between
 # AGPRs and VGPRs on every iteration)

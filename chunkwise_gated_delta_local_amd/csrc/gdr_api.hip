@@ -9,12 +9,16 @@
 #include "gdr.h"
 #include "gdr_fp16.hpp"
 #include "gdr_launch.hpp"
+#include "gdr_mixer.hpp"
 
 namespace {
 
 thread_local char g_err[512] = "";
 
-gdr_status_t fail(gdr_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+// The layer operators (gdr_mixer_api.hip) report through the same message.
+namespace gdr {
 gdr_status_t fail(gdr_status_t st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -22,6 +26,12 @@ gdr_status_t fail(gdr_status_t st, const char* fmt, ...) {
     va_end(ap);
     return st;
 }
+void clear_error() { g_err[0] = '\0'; }
+}  // namespace gdr
+
+namespace {
+
+using gdr::fail;
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 

@@ -1,0 +1,273 @@
+// Selective state space scan with a diagonal transition per channel
+// (include/gdr_mixer.h): forward over packed sequences, and one token per
+// sequence.
+//
+//   h_t[d][n] = exp(delta_t[d] A[d][n]) h_{t-1}[d][n] + delta_t[d] B_t[n] x_t[d]
+//   y_t[d]    = (sum_n C_t[n] h_t[d][n] + D[d] x_t[d]) silu(z_t[d])
+//
+// The exponentials bound the forward pass: v_exp_f32 takes 8 cycles of a SIMD
+// for a wavefront and every other operation 4, so a (token, channel, state)
+// costs at least 24 (two products, exp, two fused multiply-adds) against 1 to 2
+// bytes of x, dt, z and y at 16 states. The recurrence is serial in t, and few
+// channels would leave the card idle; therefore the wavefronts of a workgroup
+// take consecutive pieces of the same channels' time axis: h at the end of a
+// piece is P h_in + h_loc with P = exp(A sum(delta)), so each runs its piece
+// from a zero state (one more fused multiply-add an element; exp and
+// delta B x stay in registers), publishes P and h_loc, and repeats the
+// recurrence from the state its predecessors give.
+//
+// Layout: a wavefront holds 16 channels (lane & 15) by 4 state groups
+// (lane >> 4) of SPL states: B and C are then LDS broadcasts, and the sum over
+// states ends with three swaps and adds for four tokens, each lane left with
+// one token's sum, which it finishes.
+#include "gdr_scan.hpp"
+
+namespace gdr {
+
+namespace {
+
+// Tokens a wavefront takes at a time: SPL * piece exponentials and as many
+// products stay in registers.
+template <int SPL> constexpr int kPiece = SPL <= 4 ? 16 : 64 / SPL;
+
+template <int SPL> constexpr int kFwdWaveFloats = kPiece<SPL> * (kCh * 2 + 8 * SPL);       // delta, delta x; B, C
+template <int SPL> constexpr int kFwdPubFloats = 64 * 2 * SPL;                             // P and h_loc of a wavefront
+template <int SPL> constexpr size_t fwd_lds(int nw) {
+    return 4 * ((size_t)nw * (kFwdWaveFloats<SPL> + 2 * kFwdPubFloats<SPL>) + 2 * 64 * SPL);
+}
+
+template <typename T, int SPL>
+__global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, int cbg) {
+    constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    int n, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int c = lane & 15, q = lane >> 4;
+    const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
+    const bool act = cb * kCh + c < Dg;
+    const int ch = g * Dg + (act ? cb * kCh + c : Dg - 1);
+    float* sd = lds + wave * kFwdWaveFloats<SPL>;           // [L][16][2]
+    float* sB = sd + L * kCh * 2;                           // [L][SP]
+    float* sC = sB + L * SP;
+    float* pub = lds + nw * kFwdWaveFloats<SPL>;            // [2][nw][2][64][SPL]
+    float* carry = pub + 2 * nw * kFwdPubFloats<SPL>;       // [2][64][SPL]
+
+    int64_t s, e;
+    seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    float A2[SPL], h0[SPL];
+    const int64_t st0 = ((int64_t)n * a.p.channels + ch) * S + q * SPL;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+        const bool in = act && q * SPL + i < S;
+        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        h0[i] = in && a.S0 ? a.S0[st0 + i] : 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
+    const int o32 = a.p.out_dtype == GDR_F32;
+
+    const T zero = to_t<T>(0.f);
+    T rx[K], rdt[K], rz[K];
+    StateRows<T, SPL, L> rB, rC;
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t t = t0 + 4 * k + q;
+            rx[k] = rdt[k] = rz[k] = zero;
+            if (act && t < e) {
+                rx[k] = ((const T*)a.x)[t * a.p.x_stride + ch];
+                rdt[k] = ((const T*)a.dt)[t * a.p.dt_stride + ch];
+                if (a.z) rz[k] = ((const T*)a.z)[t * a.p.z_stride + ch];
+            }
+        }
+        rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
+        rC.load(a.C, a.p.c_stride, (int64_t)g * S, S, t0, e);
+    };
+    fetch(s + wave * L);
+    int buf = 0;
+    for (int64_t tb = s; tb < e; tb += (int64_t)nw * L, buf ^= 1) {
+        const int64_t t0 = tb + wave * L;
+        wave_lds_fence();
+        float x[K], z[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k] = to_f(rx[k]);
+            z[k] = to_f(rz[k]);
+            float d = to_f(rdt[k]) + bias;
+            if (a.p.dt_softplus) d = softplus(d);
+            d = t0 + 4 * k + q < e ? d : 0.f;               // past the end: the state stays as it is
+            *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x[k]};
+        }
+        rB.put(sB);
+        rC.put(sC);
+        wave_lds_fence();
+        fetch(t0 + (int64_t)nw * L);
+
+        float ea[L][SPL], b[L][SPL], P[SPL], hl[SPL], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) hl[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
+            float Bv[SPL];
+            lds_read(sB + j * SP + q * SPL, Bv);
+            sum += d[0];
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) {
+                ea[j][i] = __builtin_amdgcn_exp2f(A2[i] * d[0]);
+                b[j][i] = d[1] * Bv[i];
+                hl[i] = __builtin_fmaf(ea[j][i], hl[i], b[j][i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
+        float* my = pub + (size_t)(buf * nw + wave) * kFwdPubFloats<SPL> + lane * SPL;
+        lds_write(my, P);
+        lds_write(my + 64 * SPL, hl);
+        lds_barrier();
+        if (tb != s) lds_read(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
+        for (int w = 0; w < wave; ++w) {
+            const float* p = pub + (size_t)(buf * nw + w) * kFwdPubFloats<SPL> + lane * SPL;
+            float Pw[SPL], hw[SPL];
+            lds_read(p, Pw);
+            lds_read(p + 64 * SPL, hw);
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(Pw[i], h0[i], hw[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float y[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int j = 4 * k + m;
+                float Cv[SPL];
+                lds_read(sC + j * SP + q * SPL, Cv);
+                y[m] = 0.f;
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    h0[i] = __builtin_fmaf(ea[j][i], h0[i], b[j][i]);
+                    y[m] = __builtin_fmaf(Cv[i], h0[i], y[m]);
+                }
+            }
+            float v = __builtin_fmaf(skip, x[k], rows_sum4(y));
+            if (a.z) v *= silu(z[k]);
+            const int64_t t = t0 + 4 * k + q;
+            if (act && t < e) store_as<T>(a.y, t * a.p.channels + ch, v, o32);
+        }
+        if (wave == nw - 1) lds_write(carry + buf * 64 * SPL + lane * SPL, h0);
+    }
+    if (a.ST && act && wave == nw - 1) {
+#pragma unroll
+        for (int i = 0; i < SPL; ++i)
+            if (q * SPL + i < S) a.ST[st0 + i] = h0[i];
+    }
+}
+
+// One token of every sequence: the state's bytes bound it, so it moves once, 16
+// bytes a lane. LC lanes hold the states of a channel, 4 each.
+template <typename T, int LC, bool WIDE>
+__global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int64_t nch) {
+    const int l = threadIdx.x % LC;
+    const int64_t i = (int64_t)blockIdx.x * (256 / LC) + threadIdx.x / LC;     // (sequence, channel)
+    if (i >= nch) return;                                  // whole groups of LC lanes
+    const int D = a.p.channels, S = a.p.state_dim, Dg = D / a.p.groups;
+    const int64_t n = i / D;
+    const int ch = (int)(i % D), g = ch / Dg, s0 = l * 4;
+    float* st = a.state + i * S + s0;
+    const float* Ap = a.A + (int64_t)ch * S + s0;
+    const T* Bp = (const T*)a.B + n * a.p.b_stride + (int64_t)g * S + s0;
+    const T* Cp = (const T*)a.C + n * a.p.c_stride + (int64_t)g * S + s0;
+    float h[4] = {}, A2[4] = {}, B[4] = {}, C[4] = {};
+    if (WIDE) {
+        if (s0 < S) {
+            load_vec_as<float, 4>(st, 0, 0, h);
+            load_vec_as<float, 4>(Ap, 0, 0, A2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                B[j] = to_f(Bp[j]);
+                C[j] = to_f(Cp[j]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (s0 + j < S) {
+                h[j] = st[j];
+                A2[j] = Ap[j];
+                B[j] = to_f(Bp[j]);
+                C[j] = to_f(Cp[j]);
+            }
+    }
+    const float x = to_f(((const T*)a.x)[n * a.p.x_stride + ch]);
+    float d = to_f(((const T*)a.dt)[n * a.p.dt_stride + ch]) + (a.dt_bias ? a.dt_bias[ch] : 0.f);
+    if (a.p.dt_softplus) d = softplus(d);
+    const float dx = d * x;
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        h[j] = __builtin_fmaf(exp_fast(A2[j] * d), h[j], dx * B[j]);
+        y = __builtin_fmaf(C[j], h[j], y);
+    }
+    if (WIDE) {
+        if (s0 < S) store_vec<float, 4>(st, h);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (s0 + j < S) st[j] = h[j];
+    }
+#pragma unroll
+    for (int m = 1; m < LC; m <<= 1) y += __shfl_xor(y, m, 64);
+    if (l == 0) {
+        y = __builtin_fmaf(a.D ? a.D[ch] : 0.f, x, y);
+        if (a.z) y *= silu(to_f(((const T*)a.z)[n * a.p.z_stride + ch]));
+        store_as<T>(a.y, i, y, a.p.out_dtype == GDR_F32);
+    }
+}
+
+template <typename T, int SPL>
+hipError_t fwd(const ScanArgs& a) {
+    const int Dg = a.p.channels / a.p.groups, cbg = (Dg + kCh - 1) / kCh;
+    const int64_t units = (int64_t)a.p.num_seqs * a.p.groups * cbg;
+    constexpr int most = SPL == 16 ? 4 : 8;
+    static_assert(fwd_lds<SPL>(most) <= 160 * 1024, "LDS of a compute unit");
+    const int nw = waves_for(a.max_len, kPiece<SPL>, most);
+    if (!grid_fits(units + 8, 64 * nw)) return hipErrorInvalidConfiguration;
+    k_scan_fwd<T, SPL><<<dim3((unsigned)((units + 7) / 8 * 8)), 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, units, cbg);
+    return hipGetLastError();
+}
+
+template <typename T, bool WIDE>
+hipError_t step(const ScanArgs& a) {
+    const int64_t nch = (int64_t)a.p.num_seqs * a.p.channels;
+    auto go = [&](auto lanes) {
+        constexpr int LC = decltype(lanes)::value;
+        const int64_t blocks = (nch + 256 / LC - 1) / (256 / LC);
+        if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+        if (blocks == 0) return hipSuccess;
+        k_scan_step<T, LC, WIDE><<<dim3((unsigned)blocks), 256, 0, a.stream>>>(a, nch);
+        return hipGetLastError();
+    };
+    const int need = (a.p.state_dim + 3) / 4;
+    if (need <= 1) return go(std::integral_constant<int, 1>{});
+    if (need <= 2) return go(std::integral_constant<int, 2>{});
+    if (need <= 4) return go(std::integral_constant<int, 4>{});
+    if (need <= 8) return go(std::integral_constant<int, 8>{});
+    return go(std::integral_constant<int, 16>{});
+}
+
+}  // namespace
+
+size_t scan_fwd_workspace(const gdr_scan_problem_t&) { return 0; }
+
+hipError_t launch_scan_fwd(const ScanArgs& a) {
+    if (a.p.num_seqs == 0) return hipSuccess;
+    return by_states(a, [&](auto type, auto spl) { return fwd<decltype(type), decltype(spl)::value>(a); });
+}
+
+hipError_t launch_scan_step(const ScanArgs& a) {
+    const bool wide = a.p.state_dim % 4 == 0 && ((uintptr_t)a.state & 15) == 0 && ((uintptr_t)a.A & 15) == 0;
+    if (a.p.io_dtype == GDR_BF16) return wide ? step<bf16, true>(a) : step<bf16, false>(a);
+    return wide ? step<float, true>(a) : step<float, false>(a);
+}
+
+}  // namespace gdr

@@ -1,0 +1,119 @@
+// What the scan's forward and backward kernels share.
+#pragma once
+
+#include <type_traits>
+
+#include "gdr_mixer.hpp"
+
+namespace gdr {
+
+constexpr int kCh = 16;                                    // channels of a wavefront
+
+__device__ __forceinline__ void swap32(float& a, float& b) {   // a = {a.lo, b.lo}, b = {a.hi, b.hi} (halves of 32 lanes)
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap16(float& a, float& b) {   // the same with odd and even rows of 16 lanes
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+// v[i] summed over the four rows of 16 lanes; row i keeps the sum of v[i]
+__device__ __forceinline__ float rows_sum4(float (&v)[4]) {
+    swap32(v[0], v[2]);
+    swap32(v[1], v[3]);
+    float a = v[0] + v[2], b = v[1] + v[3];
+    swap16(a, b);
+    return a + b;
+}
+
+// LDS written by some lanes of a wavefront is read by others of the same one:
+// its LDS operations complete in order; this keeps the compiler from moving them.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Workgroup -> (sequence, group, channel block): consecutive blocks of channels
+// on the same XCD (workgroups are dealt to the eight XCDs in turn), so that the
+// 32-byte pieces of a 128-byte line meet in one L2.
+__device__ __forceinline__ bool unit_of(int64_t units, int cbg, int groups, int* n, int* g, int* cb) {
+    const int64_t per = (units + 7) / 8, u = (blockIdx.x % 8) * per + blockIdx.x / 8;
+    if (u >= units || blockIdx.x / 8 >= per) return false;
+    *cb = (int)(u % cbg);
+    *g = (int)(u / cbg % groups);
+    *n = (int)(u / ((int64_t)cbg * groups));
+    return true;
+}
+
+// The rows of B (or C) of L tokens from t0 into LDS as [token][4 SPL] fp32,
+// zero past the sequence and past state_dim.
+template <typename T, int SPL, int L>
+struct StateRows {
+    static constexpr int SP = 4 * SPL, PER = L * SP / 64;
+    T r[PER];
+    __device__ __forceinline__ void load(const void* base, int64_t stride, int64_t first, int S, int64_t t0, int64_t e) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = i * 64 + lane, n = idx % SP;
+            const int64_t t = t0 + idx / SP;
+            r[i] = to_t<T>(0.f);
+            if (t < e && n < S) r[i] = ((const T*)base)[t * stride + first + n];
+        }
+    }
+    __device__ __forceinline__ void put(float* lds) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) lds[i * 64 + lane] = to_f(r[i]);
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void lds_read(const float* p, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i + j] = w[j];
+        }
+    } else {
+        static_assert(N == 2, "state group");
+        const f32x2 w = *reinterpret_cast<const f32x2*>(p);
+        v[0] = w[0];
+        v[1] = w[1];
+    }
+}
+template <int N>
+__device__ __forceinline__ void lds_write(float* p, const float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+        *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]};
+    }
+}
+
+// ---------------------------------------------------------------- host
+// Wavefronts of a workgroup: enough pieces for the longest sequence, a power of two up to `most`.
+inline int waves_for(int64_t max_len, int piece, int most) {
+    int nw = 1;
+    while (nw < most && (int64_t)nw * piece < max_len) nw *= 2;
+    return nw;
+}
+
+template <typename F>
+hipError_t by_states(const ScanArgs& a, F f) {
+    auto pick = [&](auto type) {
+        const int S = a.p.state_dim;
+        if (S <= 8) return f(type, std::integral_constant<int, 2>{});
+        if (S <= 16) return f(type, std::integral_constant<int, 4>{});
+        if (S <= 32) return f(type, std::integral_constant<int, 8>{});
+        return f(type, std::integral_constant<int, 16>{});
+    };
+    return a.p.io_dtype == GDR_BF16 ? pick(bf16{}) : pick(float{});
+}
+
+}  // namespace gdr

@@ -1,0 +1,524 @@
+// Backward pass of the selective state space scan (include/gdr_mixer.h).
+//
+// With ds = d_y silu(z) and g_t the gradient of h_t,
+//   g_t = ds_t C_t + G_t,   G_{t-1} = exp(delta_t A) g_t   (G behind the last token: d_final_state)
+//   dC_t = sum_d ds h,  dB_t = sum_d g delta x,  dx = delta sum_n g B + D ds,
+//   d delta = x sum_n g B + sum_n g p A,  dA = sum_t g p delta,  p_t = exp(delta_t A) h_{t-1}.
+//
+// k_scan_states runs the recurrence once and stores the state before every tile
+// of tokens. k_scan_bwd takes the tiles of 16 J channels from the last to the
+// first; within a tile the wavefronts take consecutive pieces of L tokens, whose
+// exponentials and states stay in registers. Forward, a piece's entering state
+// comes from the tile's state and its predecessors' (P, h_loc); in reverse, its
+// incoming G from the later tile's and its successors' (P, G_loc): G at the
+// start of a piece is P G_in + G_loc.
+//
+// Layout: channel on lane bits 0, 1, 4, 5 (and J of them in a lane), state group
+// on bits 2, 3. The sums over channels (dB and dC, 2 SPL values a token) then
+// take swaps and adds over bits 5 and 4, each halving the values, and quad
+// permutes; the sums over states take row rotations by 4 and 8.
+//
+// dB and dC of a token sum over all channels of a group: every workgroup stores
+// its channels' sums and k_sum_partials joins them in a fixed order.
+#include "gdr_scan.hpp"
+
+namespace gdr {
+
+namespace {
+
+// Variants by states a lane: J channels a lane, L tokens a piece, at most NW wavefronts
+template <int SPL> struct Bwd {
+    static constexpr int J = SPL <= 4 ? 2 : 1, L = SPL <= 8 ? 8 : 4, NW = SPL <= 8 ? 8 : 4;
+    static constexpr int EPT = SPL * J, SP = 4 * SPL, CHB = kCh * J;
+    static constexpr int kWaveFloats = L * CHB * 4 + 2 * L * SP;      // (delta, delta x, ds, -); B, C
+    static constexpr int kPubFloats = 3 * 64 * EPT;                   // P, h_loc, G_loc
+    static constexpr size_t lds(int nw) { return 4 * ((size_t)nw * (kWaveFloats + 2 * kPubFloats) + 2 * 64 * EPT); }
+};
+
+struct ScanBwdWs {
+    float* states;             // [Ttot / tile + N][D][4 SPL] states before the tiles
+    float* bc;                 // [channel blocks of a group][2][Ttot][groups][S]: dB, dC
+    float* dA;                 // [N][D][S]
+    float* dch;                // [N][2][D]: dD, ddt_bias
+};
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+    return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum_quad(float x) { return add_dpp<0xb1>(add_dpp<0x4e>(x)); }      // over lane bits 0, 1
+__device__ __forceinline__ float sum_states(float x) { return add_dpp<0x128>(add_dpp<0x124>(x)); }  // over bits 2, 3
+
+// Slot of a sequence's first tile: floor(s / tile) + n leaves room for the
+// partial tiles of the sequences before it.
+__device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) { return s / tile + n; }
+
+template <typename T, int SPL>
+__global__ __launch_bounds__(512, 2) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg) {
+    constexpr int L = Bwd<SPL>::L, K = (L + 3) / 4, SP = 4 * SPL;
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    int n, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int c = lane & 15, q = lane >> 4;
+    const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
+    const bool act = cb * kCh + c < Dg;
+    const int ch = g * Dg + (act ? cb * kCh + c : Dg - 1);
+    float* sd = lds + wave * (L * kCh * 2 + L * SP);
+    float* sB = sd + L * kCh * 2;
+    float* pub = lds + nw * (L * kCh * 2 + L * SP);         // [2][nw][2][64][SPL]
+    int64_t s, e;
+    seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    float A2[SPL], h0[SPL];
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+        const bool in = act && q * SPL + i < S;
+        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        h0[i] = in && a.S0 ? a.S0[((int64_t)n * a.p.channels + ch) * S + q * SPL + i] : 0.f;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
+    const T zero = to_t<T>(0.f);
+    T rx[K], rdt[K];
+    StateRows<T, SPL, L> rB;
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t t = t0 + 4 * k + q;
+            rx[k] = rdt[k] = zero;
+            if (act && t < e) {
+                rx[k] = ((const T*)a.x)[t * a.p.x_stride + ch];
+                rdt[k] = ((const T*)a.dt)[t * a.p.dt_stride + ch];
+            }
+        }
+        rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
+    };
+    fetch(s + wave * L);
+    int64_t slot = first_slot(s, nw * L, n);
+    int buf = 0;
+    for (int64_t tb = s; tb < e; tb += (int64_t)nw * L, buf ^= 1, ++slot) {
+        const int64_t t0 = tb + wave * L;
+        wave_lds_fence();
+        if (wave == 0 && act) lds_write(states + (slot * a.p.channels + ch) * SP + q * SPL, h0);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float x = to_f(rx[k]);
+            float d = to_f(rdt[k]) + bias;
+            if (a.p.dt_softplus) d = softplus(d);
+            d = t0 + 4 * k + q < e ? d : 0.f;
+            *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x};
+        }
+        rB.put(sB);
+        wave_lds_fence();
+        fetch(t0 + (int64_t)nw * L);
+        float P[SPL], hl[SPL], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) hl[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
+            float Bv[SPL];
+            lds_read(sB + j * SP + q * SPL, Bv);
+            sum += d[0];
+#pragma unroll
+            for (int i = 0; i < SPL; ++i)
+                hl[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * d[0]), hl[i], d[1] * Bv[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
+        float* my = pub + (size_t)(buf * nw + wave) * 128 * SPL + lane * SPL;
+        lds_write(my, P);
+        lds_write(my + 64 * SPL, hl);
+        lds_barrier();
+        for (int w = 0; w < nw; ++w) {
+            const float* p = pub + (size_t)(buf * nw + w) * 128 * SPL + lane * SPL;
+            float Pw[SPL], hw[SPL];
+            lds_read(p, Pw);
+            lds_read(p + 64 * SPL, hw);
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(Pw[i], h0[i], hw[i]);
+        }
+    }
+}
+
+template <typename T, int SPL>
+__global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+    typedef Bwd<SPL> V;
+    constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, H2 = SPL / 2;
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    int n, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int c = (lane & 3) | ((lane >> 4) << 2), q = (lane >> 2) & 3, l3 = lane & 3;
+    const int D = a.p.channels, Dg = D / a.p.groups, S = a.p.state_dim;
+    float* sd = lds + wave * V::kWaveFloats;                // [L][CHB][4]
+    float* sB = sd + L * CHB * 4;                           // [L][SP]
+    float* sC = sB + L * SP;
+    float* pub = lds + nw * V::kWaveFloats;                 // [2][nw][3][64][EPT]
+    float* carry = pub + 2 * nw * V::kPubFloats;            // [2][64][EPT]
+    int64_t s, e;
+    seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+
+    bool act[J];
+    int ch[J];
+    float bias[J], skip[J], A2[EPT], dA[EPT], G[EPT], sumD[J], sumT[J];
+    int64_t st0[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int cl = cb * CHB + c + kCh * j;
+        act[j] = cl < Dg;
+        ch[j] = g * Dg + (act[j] ? cl : Dg - 1);
+        bias[j] = a.dt_bias ? a.dt_bias[ch[j]] : 0.f;
+        skip[j] = a.D ? a.D[ch[j]] : 0.f;
+        sumD[j] = sumT[j] = 0.f;
+        st0[j] = ((int64_t)n * D + ch[j]) * S + q * SPL;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) {
+            const bool in = act[j] && q * SPL + i < S;
+            A2[j * SPL + i] = in ? a.A[(int64_t)ch[j] * S + q * SPL + i] * kLog2e : 0.f;
+            G[j * SPL + i] = in && a.dST ? a.dST[st0[j] + i] : 0.f;
+            dA[j * SPL + i] = 0.f;
+        }
+    }
+    const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
+    const int tile = nw * L;
+    const int64_t ntiles = (e - s + tile - 1) / tile;
+    float* part = ws.bc + (int64_t)cb * 2 * a.Ttot * a.p.groups * S;
+    const T zero = to_t<T>(0.f);
+    T rx[K][J], rdt[K][J], rz[K][J];
+    float rdy[K][J];
+    StateRows<T, SPL, L> rB, rC;
+    auto fetch = [&](int64_t t0) {                          // t0 < s: nothing left
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int64_t t = t0 + 4 * k + q;
+                rx[k][j] = rdt[k][j] = rz[k][j] = zero;
+                rdy[k][j] = 0.f;
+                if (act[j] && t < e && t >= s) {
+                    rx[k][j] = ((const T*)a.x)[t * a.p.x_stride + ch[j]];
+                    rdt[k][j] = ((const T*)a.dt)[t * a.p.dt_stride + ch[j]];
+                    if (a.z) rz[k][j] = ((const T*)a.z)[t * a.p.z_stride + ch[j]];
+                    rdy[k][j] = load_as<T>(a.d_y, t * D + ch[j], dy32);
+                }
+            }
+        if (t0 >= s) {
+            rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
+            rC.load(a.C, a.p.c_stride, (int64_t)g * S, S, t0, e);
+        }
+    };
+    fetch(s + (ntiles - 1) * tile + wave * L);
+    int buf = 0;
+    for (int64_t it = ntiles - 1; it >= 0; --it, buf ^= 1) {
+        const int64_t t0 = s + it * tile + wave * L;
+        float h[L + 1][EPT], ea[L][EPT];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float v[SPL];
+            lds_read(ws.states + ((first_slot(s, tile, n) + it) * D + ch[j]) * SP + q * SPL, v);
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h[0][j * SPL + i] = act[j] ? v[i] : 0.f;
+        }
+        wave_lds_fence();
+        float x[K][J], pre[K][J], z[K][J], dy[K][J];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                x[k][j] = to_f(rx[k][j]);
+                z[k][j] = to_f(rz[k][j]);
+                dy[k][j] = rdy[k][j];
+                pre[k][j] = to_f(rdt[k][j]) + bias[j];
+                float d = a.p.dt_softplus ? softplus(pre[k][j]) : pre[k][j];
+                d = act[j] && t0 + 4 * k + q < e ? d : 0.f;
+                const float ds = a.z ? dy[k][j] * silu(z[k][j]) : dy[k][j];
+                *reinterpret_cast<f32x4*>(sd + ((4 * k + q) * CHB + c + kCh * j) * 4) = f32x4{d, d * x[k][j], ds, 0.f};
+            }
+        rB.put(sB);
+        rC.put(sC);
+        wave_lds_fence();
+        fetch(t0 - tile);
+
+        // the piece from a zero state, and its G from zero behind it
+        float P[EPT], hl[EPT], Gl[EPT], sum[J];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) hl[i] = Gl[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum[j] = 0.f;
+#pragma unroll
+        for (int m = 0; m < L; ++m) {
+            float Bv[SPL];
+            lds_read(sB + m * SP + q * SPL, Bv);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
+                sum[j] += d[0];
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    const int o = j * SPL + i;
+                    ea[m][o] = __builtin_amdgcn_exp2f(A2[o] * d[0]);
+                    hl[o] = __builtin_fmaf(ea[m][o], hl[o], d[1] * Bv[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = L - 1; m >= 0; --m) {
+            float Cv[SPL];
+            lds_read(sC + m * SP + q * SPL, Cv);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float ds = sd[(m * CHB + c + kCh * j) * 4 + 2];
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    const int o = j * SPL + i;
+                    Gl[o] = ea[m][o] * __builtin_fmaf(ds, Cv[i], Gl[o]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) P[j * SPL + i] = __builtin_amdgcn_exp2f(A2[j * SPL + i] * sum[j]);
+        float* my = pub + (size_t)(buf * nw + wave) * V::kPubFloats + lane * EPT;
+        lds_write(my, P);
+        lds_write(my + 64 * EPT, hl);
+        lds_write(my + 128 * EPT, Gl);
+        lds_barrier();
+        if (it != ntiles - 1) lds_read(carry + (buf ^ 1) * 64 * EPT + lane * EPT, G);
+        for (int w = 0; w < wave; ++w) {
+            const float* p = pub + (size_t)(buf * nw + w) * V::kPubFloats + lane * EPT;
+            float u[EPT], v[EPT];
+            lds_read(p, u);
+            lds_read(p + 64 * EPT, v);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) h[0][i] = __builtin_fmaf(u[i], h[0][i], v[i]);
+        }
+        for (int w = nw - 1; w > wave; --w) {
+            const float* p = pub + (size_t)(buf * nw + w) * V::kPubFloats + lane * EPT;
+            float u[EPT], v[EPT];
+            lds_read(p, u);
+            lds_read(p + 128 * EPT, v);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) G[i] = __builtin_fmaf(u[i], G[i], v[i]);
+        }
+#pragma unroll
+        for (int m = 0; m < L; ++m) {
+            float Bv[SPL];
+            lds_read(sB + m * SP + q * SPL, Bv);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float dx = sd[(m * CHB + c + kCh * j) * 4 + 1];
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    const int o = j * SPL + i;
+                    h[m + 1][o] = __builtin_fmaf(ea[m][o], h[m][o], dx * Bv[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            float gB[J], gA[J], yC[J], u[H2];
+#pragma unroll
+            for (int j = 0; j < J; ++j) gB[j] = gA[j] = yC[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < H2; ++i) u[i] = 0.f;
+#pragma unroll
+            for (int m4 = 3; m4 >= 0; --m4) {
+                const int m = 4 * k + m4;
+                float Bv[SPL], Cv[SPL], dBv[SPL], dCv[SPL];
+                lds_read(sB + m * SP + q * SPL, Bv);
+                lds_read(sC + m * SP + q * SPL, Cv);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
+                    float tB = 0.f, tA = 0.f, tC = 0.f;
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i) {
+                        const int o = j * SPL + i;
+                        const float gr = __builtin_fmaf(d[2], Cv[i], G[o]);
+                        const float gp = gr * (ea[m][o] * h[m][o]);
+                        tB = __builtin_fmaf(gr, Bv[i], tB);
+                        tA = __builtin_fmaf(gp, A2[o], tA);
+                        tC = __builtin_fmaf(Cv[i], h[m + 1][o], tC);
+                        dA[o] = __builtin_fmaf(gp, d[0], dA[o]);
+                        dBv[i] = j ? __builtin_fmaf(gr, d[1], dBv[i]) : gr * d[1];
+                        dCv[i] = j ? __builtin_fmaf(d[2], h[m + 1][o], dCv[i]) : d[2] * h[m + 1][o];
+                        G[o] = ea[m][o] * gr;
+                    }
+                    tB = sum_states(tB);
+                    tA = sum_states(tA);
+                    if (a.z) tC = sum_states(tC);
+                    gB[j] = q == m4 ? tB : gB[j];
+                    gA[j] = q == m4 ? tA : gA[j];
+                    yC[j] = q == m4 ? tC : yC[j];
+                }
+                // over the channels: lanes below 32 keep dB, the others dC; rows then halve the states
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    swap32(dBv[i], dCv[i]);
+                    dBv[i] += dCv[i];
+                }
+#pragma unroll
+                for (int i = 0; i < H2; ++i) {
+                    swap16(dBv[i], dBv[i + H2]);
+                    const float t = sum_quad(dBv[i] + dBv[i + H2]);
+                    u[i] = l3 == m4 ? t : u[i];
+                }
+            }
+            const int64_t tk = t0 + 4 * k;
+            if (tk + l3 < e) {
+                const int64_t at = (((int64_t)(lane >> 5) * a.Ttot + tk + l3) * a.p.groups + g) * S;
+                const int n0 = q * SPL + ((lane >> 4) & 1) * H2;
+#pragma unroll
+                for (int i = 0; i < H2; ++i)
+                    if (n0 + i < S) part[at + n0 + i] = u[i];
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float dy_ = dy[k][j], x_ = x[k][j];
+                float delta = a.p.dt_softplus ? softplus(pre[k][j]) : pre[k][j];
+                const float ds = a.z ? dy_ * silu(z[k][j]) : dy_;
+                const float ddelta = __builtin_fmaf(gA[j], kLn2, x_ * gB[j]);
+                const float ddt = a.p.dt_softplus ? ddelta * sigmoid(pre[k][j]) : ddelta;
+                if (act[j] && tk + q < e) {
+                    const int64_t at = (tk + q) * D + ch[j];
+                    store_as<T>(a.dx, at, __builtin_fmaf(skip[j], ds, delta * gB[j]), g32);
+                    store_as<T>(a.ddt, at, ddt, g32);
+                    if (a.z) store_as<T>(a.dz, at, dy_ * __builtin_fmaf(skip[j], x_, yC[j]) * silu_grad(z[k][j]), g32);
+                    sumD[j] = __builtin_fmaf(ds, x_, sumD[j]);
+                    sumT[j] += ddt;
+                }
+            }
+        }
+        if (wave == 0) lds_write(carry + buf * 64 * EPT + lane * EPT, G);
+    }
+    if (a.dS0 && wave == 0) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < SPL; ++i)
+                if (act[j] && q * SPL + i < S) a.dS0[st0[j] + i] = G[j * SPL + i];
+    }
+    // the wavefronts' sums over their tokens, joined in order
+    lds_barrier();
+    float* all = lds;                                       // [nw][64][EPT + 2 J]
+    constexpr int R = EPT + 2 * J;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) all[(wave * R + i) * 64 + lane] = dA[i];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        all[(wave * R + EPT + j) * 64 + lane] = sum_states(sumD[j]);
+        all[(wave * R + EPT + J + j) * 64 + lane] = sum_states(sumT[j]);
+    }
+    lds_barrier();
+    if (wave != 0) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float v = 0.f;
+        for (int w = 0; w < nw; ++w) v += all[(w * R + i) * 64 + lane];
+        const int j = i < EPT ? i / SPL : (i - EPT) % J;
+        if (!act[j]) continue;
+        if (i < EPT) {
+            if (q * SPL + i % SPL < S) ws.dA[st0[j] + i % SPL] = v;
+        } else if (q == 0) {
+            ws.dch[((int64_t)n * 2 + (i - EPT) / J) * D + ch[j]] = v;
+        }
+    }
+}
+
+template <typename T> struct StateGradOut {                 // dB, dC in grad_dtype
+    void *dB, *dC;
+    int64_t half;
+    int f32;
+    __device__ void operator()(int64_t i, float v) const {
+        if (i < half) store_as<T>(dB, i, v, f32);
+        else store_as<T>(dC, i - half, v, f32);
+    }
+};
+struct PlainOut {
+    float* p;
+    __device__ void operator()(int64_t i, float v) const { p[i] = v; }
+};
+struct ChannelOut {
+    float *dD, *ddt_bias;
+    int64_t D;
+    __device__ void operator()(int64_t i, float v) const {
+        if (i < D) {
+            if (dD) dD[i] = v;
+        } else if (ddt_bias) {
+            ddt_bias[i - D] = v;
+        }
+    }
+};
+
+// Workspace regions. States kept: one a tile of nw L tokens, and one more a
+// sequence. With fewer than NW wavefronts no sequence is longer than a tile,
+// so that T / tile <= N; otherwise the tile has NW L tokens.
+struct BwdPlan {
+    size_t states, bc, dA, dch, end;
+};
+template <int SPL>
+BwdPlan plan(const gdr_scan_problem_t& p) {
+    typedef Bwd<SPL> V;
+    const size_t D = p.channels, S = p.state_dim, N = p.num_seqs, T = (size_t)(p.batch * p.seq_len);
+    const size_t cbg = (D / p.groups + V::CHB - 1) / V::CHB;
+    BwdPlan b;
+    size_t off = 0;
+    auto take = [&](size_t floats) { size_t o = off; off = (off + floats * 4 + 255) & ~(size_t)255; return o; };
+    const size_t most = N < T ? N : T, tiles = T / (V::NW * V::L);
+    b.states = take(((tiles > most ? tiles : most) + N) * D * V::SP);
+    b.bc = take(cbg * 2 * T * p.groups * S);
+    b.dA = take(N * D * S);
+    b.dch = take(N * 2 * D);
+    b.end = off;
+    return b;
+}
+
+template <typename T, int SPL>
+hipError_t bwd(const ScanArgs& a) {
+    typedef Bwd<SPL> V;
+    static_assert(V::lds(V::NW) <= 160 * 1024, "LDS of a compute unit");
+    const int nw = waves_for(a.max_len, V::L, V::NW);
+    const BwdPlan pl = plan<SPL>(a.p);
+    auto f = [&](size_t off) { return reinterpret_cast<float*>(a.ws + off); };
+    const ScanBwdWs ws = {f(pl.states), f(pl.bc), f(pl.dA), f(pl.dch)};
+    const int Dg = a.p.channels / a.p.groups;
+    const int64_t NG = (int64_t)a.p.num_seqs * a.p.groups;
+    const int cbs = (Dg + kCh - 1) / kCh, cbg = (Dg + V::CHB - 1) / V::CHB;
+    auto grid = [](int64_t units) { return dim3((unsigned)((units + 7) / 8 * 8)); };
+    hipError_t e = hipSuccess;
+    if (!grid_fits(NG * cbs + 8, 64 * nw)) return hipErrorInvalidConfiguration;
+    if (NG > 0) {
+        const size_t lds = 4 * (size_t)nw * (V::L * kCh * 2 + V::L * V::SP + 2 * 128 * SPL);
+        k_scan_states<T, SPL><<<grid(NG * cbs), 64 * nw, lds, a.stream>>>(a, ws.states, NG * cbs, cbs);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        k_scan_bwd<T, SPL><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, NG * cbg, cbg);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const int64_t D = a.p.channels, S = a.p.state_dim, half = a.Ttot * a.p.groups * S;
+    e = sum_partials(ws.bc, cbg, 2 * half, StateGradOut<T>{a.dB, a.dC, half, a.p.grad_dtype == GDR_F32}, a.stream);
+    if (e == hipSuccess) e = sum_partials(ws.dA, a.p.num_seqs, D * S, PlainOut{a.dA}, a.stream);
+    if (e == hipSuccess && (a.dD || a.ddt_bias))
+        e = sum_partials(ws.dch, a.p.num_seqs, 2 * D, ChannelOut{a.dD, a.ddt_bias, D}, a.stream);
+    return e;
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace(const gdr_scan_problem_t& p) {
+    const int S = p.state_dim;
+    auto need = [&](auto spl) {
+        constexpr int SPL = decltype(spl)::value;
+        return plan<SPL>(p).end;
+    };
+    if (S <= 8) return need(std::integral_constant<int, 2>{});
+    if (S <= 16) return need(std::integral_constant<int, 4>{});
+    if (S <= 32) return need(std::integral_constant<int, 8>{});
+    return need(std::integral_constant<int, 16>{});
+}
+
+hipError_t launch_scan_bwd(const ScanArgs& a) {
+    return by_states(a, [&](auto type, auto spl) { return bwd<decltype(type), decltype(spl)::value>(a); });
+}
+
+}  // namespace gdr

@@ -20,6 +20,11 @@ and k that the token-by-token forward can apply first.
 in reverse token order: dq, dk, dv, dbeta, dg and the initial state's
 gradient for given output and final-state gradients.
 
+``mixer`` (NumPy) holds the operators that stand next to the delta rule in a
+layer (short causal convolution, selective state space scan, layer norm) and
+their gradients, pinned by ``tests/test_oracle_mixer.py`` against differences
+and independent forms.
+
 All are pinned by the CPU tests in ``tests/test_oracle_*.py`` against closed
 forms, identities and brute-force products fixed by the pages and by algebra.
 Every function is pinned; none is "parity unpinned".
@@ -28,3 +33,4 @@ from .recurrence import recurrence, build  # noqa: F401
 from .chunked import chunked_forward  # noqa: F401
 from .normalize import l2_normalize  # noqa: F401
 from .backward import recurrence_backward  # noqa: F401
+from . import mixer  # noqa: F401
