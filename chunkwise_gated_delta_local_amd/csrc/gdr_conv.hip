@@ -39,11 +39,15 @@ struct Taps {
     __device__ __forceinline__ void load(const ConvArgs& a, int ch) {
         const int f32 = a.p.param_dtype == GDR_F32;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int i = 0; i < W; ++i) {                    // V W consecutive elements, V at a time
+            float part[V];
+            load_vec_as<T, V>(a.weight, (int64_t)ch * W + i * V, f32, part);
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i][v] = load_as<T>(a.weight, (int64_t)(ch + v) * W + i, f32);
-            b[v] = a.bias ? load_as<T>(a.bias, ch + v, f32) : 0.f;
+            for (int v = 0; v < V; ++v) w[(i * V + v) % W][(i * V + v) / W] = part[v];
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v) b[v] = 0.f;
+        if (a.bias) load_vec_as<T, V>(a.bias, ch, f32, b);
     }
     // p of the token whose row is `x`, after the rows hist[0..W-2] (oldest first)
     __device__ __forceinline__ float at(const float (&hist)[W - 1][V], const float (&x)[V], int v) const {

@@ -108,6 +108,12 @@ gdr_status_t check_conv(const gdr_conv_problem_t* p) {
     return check_stride("x_stride", p->x_stride, p->channels);
 }
 
+// 16 bytes of the io type divide the rows and their strides
+bool wide_rows(int32_t io_dtype, int64_t cols, int64_t stride) {
+    const int64_t v = io_dtype == GDR_BF16 ? 8 : 4;
+    return cols % v == 0 && stride % v == 0;
+}
+
 gdr::ConvArgs conv_args(const gdr_conv_problem_t* p, const void* x, const void* weight, const void* bias,
                         const void* S0, const int32_t* cu, void* stream) {
     gdr::ConvArgs a{};
@@ -115,12 +121,9 @@ gdr::ConvArgs conv_args(const gdr_conv_problem_t* p, const void* x, const void* 
     a.Ttot = p->batch * p->seq_len;
     a.x = x; a.weight = weight; a.bias = bias; a.S0 = S0; a.cu = cu;
     a.stream = static_cast<hipStream_t>(stream);
+    a.wide = wide_rows(p->io_dtype, p->channels, p->x_stride) && aligned(x, 16) && aligned(weight, 16) &&
+             aligned(bias, 16) && aligned(S0, 16);
     return a;
-}
-// 16 bytes of the io type divide the rows and their strides
-bool wide_rows(int32_t io_dtype, int64_t cols, int64_t stride) {
-    const int64_t v = io_dtype == GDR_BF16 ? 8 : 4;
-    return cols % v == 0 && stride % v == 0;
 }
 
 size_t conv_bwd_bytes(const gdr_conv_problem_t* p) {
@@ -195,8 +198,7 @@ gdr_status_t gdr_conv_fwd(const gdr_conv_problem_t* p, const void* x, const void
     gdr::ConvArgs a = conv_args(p, x, weight, bias, initial_state, cu_dev, stream);
     a.y = y;
     a.ST = final_state;
-    a.wide = wide_rows(p->io_dtype, p->channels, p->x_stride) && aligned(x, 16) && aligned(initial_state, 16) &&
-             aligned(y, 16) && aligned(final_state, 16);
+    a.wide = a.wide && aligned(y, 16) && aligned(final_state, 16);
     return done(gdr::launch_conv_fwd(a));
 }
 
@@ -212,7 +214,7 @@ gdr_status_t gdr_conv_step(const gdr_conv_problem_t* p, const void* x, const voi
     gdr::ConvArgs a = conv_args(p, x, weight, bias, nullptr, nullptr, stream);
     a.y = y;
     a.ST = state;
-    a.wide = wide_rows(p->io_dtype, p->channels, p->x_stride) && aligned(x, 16) && aligned(state, 16) && aligned(y, 16);
+    a.wide = a.wide && aligned(state, 16) && aligned(y, 16);
     return done(gdr::launch_conv_step(a));
 }
 
@@ -243,8 +245,7 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* p, const void* x, const void
     a.d_y = d_y; a.dST = d_final_state; a.dx = dx; a.dS0 = d_initial_state;
     a.dweight = dweight; a.dbias = dbias;
     a.partial = static_cast<float*>(workspace);
-    a.wide = wide_rows(p->io_dtype, p->channels, p->x_stride) && aligned(x, 16) && aligned(initial_state, 16) &&
-             aligned(d_y, 16) && aligned(d_final_state, 16) && aligned(dx, 16) && aligned(d_initial_state, 16);
+    a.wide = a.wide && aligned(d_y, 16) && aligned(d_final_state, 16) && aligned(dx, 16) && aligned(d_initial_state, 16);
     return done(gdr::launch_conv_bwd(a));
 }
 

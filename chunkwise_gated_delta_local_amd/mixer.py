@@ -30,44 +30,58 @@ def _device(t):
 
 def _launch(fn, dev, *args):
     """Call a library entry point on the current stream of `dev`, with `dev` current."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)      # current_stream(dev).cuda_stream without its object
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-    _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            return _check(fn(*args, stream))
+    _check(fn(*args, stream))
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _refuse(t, name, shape, dtypes):
+    raise ValueError("%s must be %s in %s, on the inputs' device%s" % (
+        name, list(shape), " or ".join(str(d) for d in dtypes),
+        "" if t is None else " (got %s in %s on %s)" % (list(t.shape), t.dtype, t.device)))
+
+
 def _dense(t, name, shape, dtypes, dev):
     """A contiguous tensor of this shape and one of these dtypes (None passes)."""
     if t is None:
         return
-    if t.shape != shape or t.dtype not in dtypes:
-        raise ValueError("%s must be %s in %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be contiguous and on the inputs' device" % name)
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev:
+        _refuse(t, name, shape, dtypes)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
 
 
-def _tokens(t, name, shape, dtype, dev):
-    """The token stride (in elements) of an input [B, T, ...]."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError("%s must be %s in %s" % (name, list(shape), dtype))
-    if t.device != dev:
-        raise ValueError("%s must be on the inputs' device" % name)
-    width = 1
-    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if n > 1 and st != width:
+def _tokens(t, name, shape, width, dtype, dev):
+    """The token stride (in elements) of an input [B, T, ...] or [N, ...] whose
+    tokens hold `width` elements each."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _refuse(t, name, shape, (dtype,))
+    return width if t.is_contiguous() else _token_stride(t, name, width)
+
+
+def _token_stride(t, name, width):
+    sizes, strides = list(t.shape), list(t.stride())
+    inner = 1
+    while inner < width:                        # the axes of a token
+        n, st = sizes.pop(), strides.pop()
+        if n > 1 and st != inner:
             raise ValueError("the elements of a token of %s must be contiguous" % name)
-        width *= n
-    B, T = t.shape[:2]
-    if B * T <= 1:
-        return width
-    ld = t.stride(1) if T > 1 else t.stride(0)
-    if (B > 1 and T > 1 and t.stride(0) != T * ld) or ld < width:
-        raise ValueError("the tokens of %s must be evenly strided" % name)
-    return ld
+        inner *= n
+    ld = rows = 0
+    for n, st in zip(reversed(sizes), reversed(strides)):
+        if n > 1 and ld and st != ld * rows:
+            raise ValueError("the tokens of %s must be evenly strided" % name)
+        if n > 1:
+            ld, rows = (ld, rows * n) if ld else (st, n)
+    if ld and ld < width:
+        raise ValueError("the tokens of %s must not overlap" % name)
+    return ld or width
 
 
 def _seqs(B, cu_seqlens, cu_seqlens_cpu, dev):
@@ -123,7 +137,7 @@ def conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, output
     dev = _device(x)
     if x.dim() != 3:
         raise ValueError("expected x [B,T,D]")
-    stride = _tokens(x, "x", x.shape, x.dtype, dev)
+    stride = _tokens(x, "x", x.shape, x.shape[2], x.dtype, dev)
     N, cu, host = _seqs(x.shape[0], cu_seqlens, cu_seqlens_cpu, dev)
     prob = _conv(x, weight, bias, activation, N, stride)
     state = (N, weight.shape[1] - 1, x.shape[2])
@@ -142,10 +156,12 @@ def conv_step(x, state, weight, bias=None, activation="silu"):
     if x.dim() != 2:
         raise ValueError("expected x [N,D]")
     N, D = x.shape
-    stride = _tokens(x[None], "x", (1, N, D), x.dtype, dev)
+    stride = _tokens(x, "x", x.shape, D, x.dtype, dev)
     prob = _conv(x, weight, bias, activation, N, stride)
+    if state is None:
+        raise ValueError("state is required")
     _dense(state, "state", (N, weight.shape[1] - 1, D), (x.dtype,), dev)
-    y = torch.empty((N, D), dtype=x.dtype, device=dev)
+    y = x.new_empty((N, D))
     _launch(load_library().gdr_conv_step, dev, ctypes.byref(prob), _p(x), _p(weight), _p(bias), _p(state), _p(y))
     return y
 
@@ -159,7 +175,7 @@ def conv_bwd(x, weight, d_y, bias=None, activation="silu", initial_state=None, d
     if x.dim() != 3:
         raise ValueError("expected x [B,T,D]")
     io, grad = x.dtype, _grad_dtype(grad_dtype, x.dtype)
-    stride = _tokens(x, "x", x.shape, io, dev)
+    stride = _tokens(x, "x", x.shape, x.shape[2], io, dev)
     N, cu, host = _seqs(x.shape[0], cu_seqlens, cu_seqlens_cpu, dev)
     _dense(d_y, "d_y", x.shape, (io, torch.float32), dev)
     prob = _conv(x, weight, bias, activation, N, stride, grad, d_y)
@@ -179,29 +195,29 @@ def conv_bwd(x, weight, d_y, bias=None, activation="silu", initial_state=None, d
 
 
 # ---------------------------------------------------------------- selective state space scan
-def _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead, N, out=None, grad=torch.float32, d_y=None):
-    """Checks what the scan's entry points share; `lead` is (batch, tokens a row)."""
-    dev, io = x.device, x.dtype
-    ch = x.shape[-1]
-    rows = lead + (ch,)
-    if A.dim() != 2 or A.shape[0] != ch:
+def _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, N, out=None, grad=torch.float32, d_y=None):
+    """Checks what the scan's entry points share; x is [B, T, D] or [N, D]."""
+    dev, io, shape = x.device, x.dtype, x.shape
+    ch, lead = shape[-1], shape[:-1]
+    if A.dim() != 2:
         raise ValueError("A must be [channels, state] float32")
-    if B.dim() != len(x.shape) + 1:
+    if B.dim() != len(shape) + 1:
         raise ValueError("B and C must be [..., groups, state]")
     G, S = B.shape[-2:]
     f32 = (torch.float32,)
     _dense(A, "A", (ch, S), f32, dev)
     _dense(D, "D", (ch,), f32, dev)
     _dense(dt_bias, "dt_bias", (ch,), f32, dev)
-    two = (lambda t: t[None]) if x.dim() == 2 else (lambda t: t)
-    xs = _tokens(two(x), "x", rows, io, dev)
-    dts = _tokens(two(dt), "dt", rows, io, dev)
-    zs = 0 if z is None else _tokens(two(z), "z", rows, io, dev)
-    bs = _tokens(two(B), "B", lead + (G, S), io, dev)
-    cs = _tokens(two(C), "C", lead + (G, S), io, dev)
-    b, t = (N, 1) if x.dim() == 2 else lead
-    return ScanProblem(b, t, xs, dts, zs, bs, cs, N, ch, G, S, 1 if dt_softplus else 0, _DTYPES[io],
-                       _DTYPES[io if out is None else out], _DTYPES[io if d_y is None else d_y.dtype], _DTYPES[grad], 0)
+    xs = _tokens(x, "x", shape, ch, io, dev)
+    dts = _tokens(dt, "dt", shape, ch, io, dev)
+    zs = 0 if z is None else _tokens(z, "z", shape, ch, io, dev)
+    bs = _tokens(B, "B", lead + (G, S), G * S, io, dev)
+    cs = _tokens(C, "C", lead + (G, S), G * S, io, dev)
+    b, t = lead if len(lead) == 2 else (N, 1)
+    t_io = _DTYPES[io]
+    return ScanProblem(b, t, xs, dts, zs, bs, cs, N, ch, G, S, 1 if dt_softplus else 0, t_io,
+                       t_io if out is None else _DTYPES[out], t_io if d_y is None else _DTYPES[d_y.dtype],
+                       _DTYPES[grad], 0)
 
 
 def _out_dtype(out_dtype, io):
@@ -230,7 +246,7 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False, in
         raise ValueError("expected x [B,T,D]")
     out = _out_dtype(out_dtype, x.dtype)
     N, cu, host = _seqs(x.shape[0], cu_seqlens, cu_seqlens_cpu, dev)
-    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, tuple(x.shape[:2]), N, out)
+    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, N, out)
     state = (N, x.shape[2], B.shape[-1])
     _dense(initial_state, "initial_state", state, (torch.float32,), dev)
     y = torch.empty(x.shape, dtype=out, device=dev)
@@ -250,11 +266,11 @@ def scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=F
         raise ValueError("expected x [N,D]")
     out = _out_dtype(out_dtype, x.dtype)
     N = x.shape[0]
-    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, (1, N), N, out)
-    _dense(state, "state", (N, x.shape[1], B.shape[-1]), (torch.float32,), dev)
+    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, N, out)
     if state is None:
         raise ValueError("state is required")
-    y = torch.empty(x.shape, dtype=out, device=dev)
+    _dense(state, "state", (N, x.shape[1], B.shape[-1]), (torch.float32,), dev)
+    y = x.new_empty(x.shape, dtype=out)
     _launch(load_library().gdr_scan_step, dev, ctypes.byref(prob), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(z),
             _p(dt_bias), _p(state), _p(y))
     return y
@@ -272,7 +288,7 @@ def scan_bwd(x, dt, A, B, C, d_y, D=None, z=None, dt_bias=None, dt_softplus=Fals
     io, grad = x.dtype, _grad_dtype(grad_dtype, x.dtype)
     _dense(d_y, "d_y", x.shape, (io, torch.float32), dev)
     N, cu, host = _seqs(x.shape[0], cu_seqlens, cu_seqlens_cpu, dev)
-    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, tuple(x.shape[:2]), N, None, grad, d_y)
+    prob = _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, N, None, grad, d_y)
     state = (N, x.shape[2], B.shape[-1])
     _dense(initial_state, "initial_state", state, (torch.float32,), dev)
     _dense(d_final_state, "d_final_state", state, (torch.float32,), dev)
@@ -296,24 +312,14 @@ def _norm(x, weight, bias, eps, out, grad=torch.float32, d_y=None):
     if x.dim() < 1:
         raise ValueError("expected x [..., C]")
     C = x.shape[-1]
-    if x.is_contiguous():
-        ld = C
-    else:                                       # rows evenly strided
-        ld = 0
-        if C > 1 and x.stride(-1) != 1:
-            raise ValueError("the elements of a row of x must be contiguous")
-        for n, st in zip(reversed(x.shape[:-1]), reversed(x.stride()[:-1])):
-            if n > 1 and ld and st != ld * rows:
-                raise ValueError("the rows of x must be evenly strided")
-            if n > 1:
-                ld, rows = (ld, rows * n) if ld else (st, n)
-        if ld < C:
-            raise ValueError("the rows of x must not overlap")
+    if C < 1:
+        raise ValueError("the last axis of x is empty")
+    ld = C if x.is_contiguous() else _token_stride(x, "x", C)
     kinds = (io, torch.float32)
     _dense(weight, "weight", (C,), kinds, dev)
     _dense(bias, "bias", (C,), kinds if weight is None else (weight.dtype,), dev)
     param = io if weight is None and bias is None else (bias if weight is None else weight).dtype
-    return NormProblem(x.numel() // C if C else 0, ld, C, eps, _DTYPES[io], _DTYPES[param], _DTYPES[out],
+    return NormProblem(x.numel() // C, ld, C, eps, _DTYPES[io], _DTYPES[param], _DTYPES[out],
                        _DTYPES[io if d_y is None else d_y.dtype], _DTYPES[grad], 0)
 
 
@@ -326,9 +332,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None):
     dev = _device(x)
     out = _out_dtype(out_dtype, x.dtype)
     prob = _norm(x, weight, bias, eps, out)
-    y = torch.empty(x.shape, dtype=out, device=dev)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    y = x.new_empty(x.shape, dtype=out)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _launch(load_library().gdr_layer_norm_fwd, dev, ctypes.byref(prob), _p(x), _p(weight), _p(bias), _p(y), _p(mean),
             _p(rstd))
     return y, mean, rstd
