@@ -5,9 +5,10 @@
 //   p_t = bias + sum_w weight[w] u_{t-(W-1)+w},  u = (initial rows | x),  y = p or p sigmoid(p)
 //
 // 2 W + 5 operations on 4 to 8 bytes: HBM bounds every form. So each element
-// moves once, 16 bytes a lane (a wavefront reads 1 KB of a token's row), and a
-// lane walks kRun tokens of its channels with the last W - 1 rows in registers;
-// only the W - 1 rows before a run are read again.
+// moves once, 8 or 16 bytes a lane, and a wavefront walks a run of tokens with
+// the last W - 1 rows of its channels in registers; only the W - 1 rows before
+// a run (and, backward, behind it) are read again. 65,536 tokens of 8,192 bf16
+// channels: 412 us, 5.2 TB/s, the rate of a copy.
 #include <type_traits>
 
 #include "gdr_mixer.hpp"
@@ -16,9 +17,22 @@ namespace gdr {
 
 namespace {
 
-constexpr int kRun = 32;       // tokens a wavefront walks
-constexpr int kWaves = 4;      // wavefronts of a workgroup: consecutive runs of the same channels
-constexpr int kGroup = 8;      // rows loaded together, ahead of their use
+constexpr int kWaves = 4;      // wavefronts of a workgroup
+constexpr int kGroup = 4;      // rows loaded together (8: 431 us instead of 412; 2: 426)
+// Elements of a bf16 row a lane moves at once. Forward 8 (4: 575 us instead of
+// 422). Backward 4: with 8 the registers of taps, their sums and two histories
+// leave one wavefront on a SIMD (208 us instead of 165 on 16,384 tokens of 6,144
+// channels).
+constexpr int kFwdV = 8, kBwdV = 4;
+
+// Tokens a wavefront walks: the longest run, up to `most`, that still makes 2048
+// wavefronts (two a SIMD); 16 where there is too little work for that. Longest:
+// forward 64 (32: 422 us, 128: 422, 64: 412), backward 128 (64: 143 us, 128: 140).
+int run_length(int64_t Ttot, int wavefronts, int most) {
+    int run = most;
+    while (run > 16 && (Ttot + run - 1) / run * wavefronts < 2048) run /= 2;
+    return run;
+}
 
 // One row of a sequence's u at token t (t may lie before its start s)
 template <typename T, int V>
@@ -69,7 +83,7 @@ __device__ __forceinline__ void push(float (&hist)[W - 1][V], const float (&x)[V
 }
 
 template <typename T, int V, int W>
-__global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a, int ncb, int64_t ntiles) {
+__global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a, int ncb, int64_t ntiles, int run) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int cb = blockIdx.x % ncb;
     const int64_t tile = blockIdx.x / ncb;
@@ -88,9 +102,9 @@ __global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a, int ncb, int64_t n
         }
         return;
     }
-    const int64_t t0 = (tile * kWaves + wave) * kRun;
+    const int64_t t0 = (tile * kWaves + wave) * run;
     if (t0 >= a.Ttot) return;
-    const int64_t t1 = t0 + kRun < a.Ttot ? t0 + kRun : a.Ttot;
+    const int64_t t1 = t0 + run < a.Ttot ? t0 + run : a.Ttot;
     Taps<T, V, W> taps;
     taps.load(a, ch);
     const bool silu_on = a.p.activation == GDR_ACT_SILU;
@@ -168,18 +182,18 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, int ncb) {
 // dp_t it can finish position r = t - (W - 1). At the end of a sequence it feeds
 // W - 1 zeros. A position is stored by the run that holds its token; an initial
 // row by the run that holds the sequence's first token.
-template <typename T, int V, int W>
-__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t ntiles) {
-    __shared__ float red[kWaves][W + 1][64 * V];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int cb = blockIdx.x % ncb;
+// DT: the type of d_y and d_final_state; GT: that of dx and d_initial_state.
+template <typename T, typename DT, typename GT, int V, int W, bool SILU>
+__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t ntiles, int run) {
     const int64_t tile = blockIdx.x / ncb;
-    const int D = a.p.channels, ch = (cb * 64 + lane) * V;
-    const bool active = ch < D;
-    const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
+    const int D = a.p.channels, ch = ((int)(blockIdx.x % ncb) * (int)blockDim.x + (int)threadIdx.x) * V;
+    if (ch >= D) return;
+    GT* dxp = (GT*)a.dx;
+    GT* dS0 = (GT*)a.dS0;
+    const DT* dyp = (const DT*)a.d_y;
+    const DT* dST = (const DT*)a.dST;
     if (tile >= ntiles) {                                // empty sequences: d_initial_state = d_final_state
-        const int64_t q = (tile - ntiles) * kWaves + wave;
-        if (!active || q >= a.p.num_seqs) return;
+        const int64_t q = tile - ntiles;
         int64_t s, e;
         seq_range(a.cu, (int)q, a.p.seq_len, a.Ttot, &s, &e);
         if (e > s) return;
@@ -187,18 +201,17 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t n
         for (int j = 0; j < W - 1; ++j) {
             const int64_t at = (q * (W - 1) + j) * D + ch;
             float f[V] = {};
-            if (a.dST) load_vec_as<T, V>(a.dST, at, dy32, f);
-            store_vec_as<T, V>(a.dS0, at, f, g32);
+            if (dST) unpack<DT, V>(load_raw<DT, V>(dST + at), f);
+            store_vec<GT, V>(dS0 + at, f);
         }
         return;
     }
-    const int64_t t0 = (tile * kWaves + wave) * kRun;
+    const int64_t t0 = tile * run;
     float dw[W][V] = {}, db[V] = {};
-    if (active && t0 < a.Ttot) {
-        const int64_t t1 = t0 + kRun < a.Ttot ? t0 + kRun : a.Ttot;
+    {
+        const int64_t t1 = t0 + run < a.Ttot ? t0 + run : a.Ttot;
         Taps<T, V, W> taps;
         taps.load(a, ch);
-        const bool silu_on = a.p.activation == GDR_ACT_SILU;
         int q = seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t0);
         int64_t s, e;
         seq_range(a.cu, q, a.p.seq_len, a.Ttot, &s, &e);
@@ -209,33 +222,56 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t n
 #pragma unroll
             for (int v = 0; v < V; ++v) dph[i][v] = 0.f;
         }
-        // finishes position r with the newest dp
-        auto emit = [&](int64_t r, const float (&dp)[V]) {
-            const bool mine = r >= s ? (r >= t0 && r < t1) : (s >= t0 && s < t1 && a.dS0 != nullptr);
-            if (!mine) return;
-            float f[V];
+        // du of the position W - 1 before the newest dp
+        auto gather = [&](const float (&dp)[V], float (&f)[V]) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 f[v] = taps.w[0][v] * dp[v];
 #pragma unroll
                 for (int w = 1; w < W; ++w) f[v] = __builtin_fmaf(taps.w[w][v], dph[W - 1 - w][v], f[v]);
             }
-            if (a.dST && r >= e - (W - 1)) {
+        };
+        auto finish = [&](int64_t r, const float (&dp)[V]) {
+            const bool mine = r >= s ? (r >= t0 && r < t1) : (s >= t0 && s < t1 && dS0 != nullptr);
+            if (!mine) return;
+            float f[V];
+            gather(dp, f);
+            if (dST && r >= e - (W - 1)) {
                 float g[V];
-                load_vec_as<T, V>(a.dST, ((int64_t)q * (W - 1) + (r - (e - (W - 1)))) * D + ch, dy32, g);
+                unpack<DT, V>(load_raw<DT, V>(dST + ((int64_t)q * (W - 1) + (r - (e - (W - 1)))) * D + ch), g);
 #pragma unroll
                 for (int v = 0; v < V; ++v) f[v] += g[v];
             }
-            if (r >= s) store_vec_as<T, V>(a.dx, r * D + ch, f, g32);
-            else store_vec_as<T, V>(a.dS0, ((int64_t)q * (W - 1) + (r - s + W - 1)) * D + ch, f, g32);
+            if (r >= s) store_vec<GT, V>(dxp + r * D + ch, f);
+            else store_vec<GT, V>(dS0 + ((int64_t)q * (W - 1) + (r - s + W - 1)) * D + ch, f);
         };
+        auto token = [&](const typename Raw<T, V>::type& rx, const typename Raw<DT, V>::type& rdy, bool own,
+                         auto done) {
+            float x[V], dp[V];
+            unpack<T, V>(rx, x);
+            unpack<DT, V>(rdy, dp);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (SILU) dp[v] *= silu_grad(taps.at(hist, x, v));
+                if (own) {
+#pragma unroll
+                    for (int w = 0; w < W - 1; ++w) dw[w][v] = __builtin_fmaf(dp[v], hist[w][v], dw[w][v]);
+                    dw[W - 1][v] = __builtin_fmaf(dp[v], x[v], dw[W - 1][v]);
+                    db[v] += dp[v];
+                }
+            }
+            done(dp);
+            push<W, V>(hist, x);
+            push<W, V>(dph, dp);
+        };
+        const T* xp = (const T*)a.x + ch;
         int64_t t = t0;
         while (true) {
             if (t >= e) {                                // the sequence has ended: its last W - 1 positions
                 float zero[V] = {};
 #pragma unroll
                 for (int i = 0; i < W - 1; ++i) {
-                    emit(e - (W - 1) + i, zero);
+                    finish(e - (W - 1) + i, zero);
                     push<W, V>(dph, zero);
                 }
                 while (t >= e && q + 1 < a.p.num_seqs) {
@@ -249,52 +285,63 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t n
             // up to W - 1 tokens behind the run while it has positions to finish
             const int64_t stop = e < t1 + (W - 1) ? e : t1 + (W - 1);
             if (t >= stop) break;
-            const int m = (int)(stop - t < kGroup ? stop - t : kGroup);
             typename Raw<T, V>::type rx[kGroup];
-            float dy[kGroup][V];
+            typename Raw<DT, V>::type rdy[kGroup];
+            // away from the ends of the run and of its sequence no token needs a decision, and a group's rows are
+            // loaded while the group before it is worked on
+            auto inside = [&](int64_t t) {
+                return t - (W - 1) >= (s > t0 ? s : t0) && t + kGroup <= (e < t1 ? e : t1);
+            };
+            if (inside(t)) {
+                auto load = [&](int64_t t) {
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) {
+                        rx[j] = load_raw<T, V>(xp + (t + j) * a.p.x_stride);
+                        rdy[j] = load_raw<DT, V>(dyp + (t + j) * D + ch);
+                    }
+                };
+                load(t);
+                bool more;
+                do {
+                    typename Raw<T, V>::type cx[kGroup];
+                    typename Raw<DT, V>::type cdy[kGroup];
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) {
+                        cx[j] = rx[j];
+                        cdy[j] = rdy[j];
+                    }
+                    more = inside(t + kGroup);
+                    if (more) load(t + kGroup);
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        token(cx[j], cdy[j], true, [&](const float (&dp)[V]) {
+                            float f[V];
+                            gather(dp, f);
+                            store_vec<GT, V>(dxp + (t + j - (W - 1)) * D + ch, f);
+                        });
+                    t += kGroup;
+                } while (more);
+                continue;
+            }
+            const int m = (int)(stop - t < kGroup ? stop - t : kGroup);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
                 if (j < m) {
-                    rx[j] = load_raw<T, V>((const T*)a.x + (t + j) * a.p.x_stride + ch);
-                    load_vec_as<T, V>(a.d_y, (t + j) * D + ch, dy32, dy[j]);
+                    rx[j] = load_raw<T, V>(xp + (t + j) * a.p.x_stride);
+                    rdy[j] = load_raw<DT, V>(dyp + (t + j) * D + ch);
                 }
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
                 if (j >= m) break;
-                float x[V], dp[V];
-                unpack<T, V>(rx[j], x);
-                const bool own = t + j < t1;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    dp[v] = silu_on ? dy[j][v] * silu_grad(taps.at(hist, x, v)) : dy[j][v];
-                    if (own) {
-#pragma unroll
-                        for (int w = 0; w < W - 1; ++w) dw[w][v] = __builtin_fmaf(dp[v], hist[w][v], dw[w][v]);
-                        dw[W - 1][v] = __builtin_fmaf(dp[v], x[v], dw[W - 1][v]);
-                        db[v] += dp[v];
-                    }
-                }
-                emit(t + j - (W - 1), dp);
-                push<W, V>(hist, x);
-                push<W, V>(dph, dp);
+                token(rx[j], rdy[j], t + j < t1, [&](const float (&dp)[V]) { finish(t + j - (W - 1), dp); });
             }
             t += m;
         }
     }
+    float* part = a.partial + tile * (W + 1) * D + ch;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) red[wave][w][lane * V + v] = dw[w][v];
-        red[wave][W][lane * V + v] = db[v];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 256) {
-        const int w = i / (64 * V), c = i % (64 * V), d = cb * 64 * V + c;
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) v += red[k][w][c];
-        if (d < D) a.partial[(tile * (W + 1) + w) * D + d] = v;
-    }
+    for (int w = 0; w < W; ++w) store_vec<float, V>(part + (int64_t)w * D, dw[w]);
+    store_vec<float, V>(part + (int64_t)W * D, db);
 }
 
 struct ConvGradOut {
@@ -307,7 +354,8 @@ struct ConvGradOut {
     }
 };
 
-template <typename F>
+// f(io type, elements a lane moves at once, taps); V16 of them for bf16
+template <int V16, typename F>
 hipError_t by_type(const ConvArgs& a, F f) {
     auto by_width = [&](auto type, auto vec) {
         switch (a.p.width) {
@@ -318,32 +366,35 @@ hipError_t by_type(const ConvArgs& a, F f) {
         return hipErrorInvalidValue;
     };
     if (a.p.io_dtype == GDR_BF16)
-        return a.wide ? by_width(bf16{}, std::integral_constant<int, 8>{}) : by_width(bf16{}, std::integral_constant<int, 1>{});
+        return a.wide ? by_width(bf16{}, std::integral_constant<int, V16>{}) : by_width(bf16{}, std::integral_constant<int, 1>{});
     return a.wide ? by_width(float{}, std::integral_constant<int, 4>{}) : by_width(float{}, std::integral_constant<int, 1>{});
 }
 
 int channel_blocks(const ConvArgs& a, int V) { return (a.p.channels + 64 * V - 1) / (64 * V); }
-int64_t run_tiles(int64_t Ttot) { return (Ttot + kRun * kWaves - 1) / (kRun * kWaves); }
 int64_t seq_tiles(const ConvArgs& a) { return ((int64_t)a.p.num_seqs + kWaves - 1) / kWaves; }
+int bwd_run(int64_t Ttot, int32_t channels) { return run_length(Ttot, (channels + 64 * kBwdV - 1) / (64 * kBwdV), 128); }
 
 }  // namespace
 
-int64_t conv_bwd_tiles(int64_t Ttot, int32_t) { return run_tiles(Ttot); }
+int64_t conv_bwd_tiles(int64_t Ttot, int32_t channels) {
+    const int run = bwd_run(Ttot, channels);
+    return (Ttot + run - 1) / run;
+}
 
 hipError_t launch_conv_fwd(const ConvArgs& a) {
-    return by_type(a, [&](auto type, auto vec, auto width) {
+    return by_type<kFwdV>(a, [&](auto type, auto vec, auto width) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, W = decltype(width)::value;
-        const int ncb = channel_blocks(a, V);
-        const int64_t ntiles = run_tiles(a.Ttot), all = ntiles + (a.ST ? seq_tiles(a) : 0);
+        const int ncb = channel_blocks(a, V), run = run_length(a.Ttot, ncb, 64);
+        const int64_t ntiles = (a.Ttot + run * kWaves - 1) / (run * kWaves), all = ntiles + (a.ST ? seq_tiles(a) : 0);
         if (!grid_fits(all * ncb, 256)) return hipErrorInvalidConfiguration;
-        if (all > 0) k_conv_fwd<T, V, W><<<dim3((unsigned)(all * ncb)), 256, 0, a.stream>>>(a, ncb, ntiles);
+        if (all > 0) k_conv_fwd<T, V, W><<<dim3((unsigned)(all * ncb)), 256, 0, a.stream>>>(a, ncb, ntiles, run);
         return hipGetLastError();
     });
 }
 
 hipError_t launch_conv_step(const ConvArgs& a) {
-    return by_type(a, [&](auto type, auto vec, auto width) {
+    return by_type<kFwdV>(a, [&](auto type, auto vec, auto width) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, W = decltype(width)::value;
         const int ncb = channel_blocks(a, V);
@@ -354,14 +405,27 @@ hipError_t launch_conv_step(const ConvArgs& a) {
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a) {
-    const int64_t ntiles = run_tiles(a.Ttot);
-    hipError_t e = by_type(a, [&](auto type, auto vec, auto width) {
+    const int64_t ntiles = conv_bwd_tiles(a.Ttot, a.p.channels);
+    const int run = bwd_run(a.Ttot, a.p.channels);
+    hipError_t e = by_type<kBwdV>(a, [&](auto type, auto vec, auto width) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, W = decltype(width)::value;
-        const int ncb = channel_blocks(a, V);
-        const int64_t all = ntiles + (a.dS0 ? seq_tiles(a) : 0);
+        const int cbs = channel_blocks(a, V), nw = cbs < kWaves ? cbs : kWaves, ncb = (cbs + nw - 1) / nw;
+        const int64_t all = ntiles + (a.dS0 ? a.p.num_seqs : 0);
         if (!grid_fits(all * ncb, 256)) return hipErrorInvalidConfiguration;
-        if (all > 0) k_conv_bwd<T, V, W><<<dim3((unsigned)(all * ncb)), 256, 0, a.stream>>>(a, ncb, ntiles);
+        if (all == 0) return hipSuccess;
+        const dim3 grid((unsigned)(all * ncb));
+        auto go = [&](auto dtype, auto gtype, auto silu_on) {
+            typedef decltype(dtype) DT;
+            typedef decltype(gtype) GT;
+            k_conv_bwd<T, DT, GT, V, W, decltype(silu_on)::value><<<grid, 64 * nw, 0, a.stream>>>(a, ncb, ntiles, run);
+        };
+        auto by_dy = [&](auto gtype, auto silu_on) {
+            a.p.dy_dtype == GDR_F32 ? go(float{}, gtype, silu_on) : go(T{}, gtype, silu_on);
+        };
+        auto by_grad = [&](auto silu_on) { a.p.grad_dtype == GDR_F32 ? by_dy(float{}, silu_on) : by_dy(T{}, silu_on); };
+        if (a.p.activation == GDR_ACT_SILU) by_grad(std::true_type{});
+        else by_grad(std::false_type{});
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
