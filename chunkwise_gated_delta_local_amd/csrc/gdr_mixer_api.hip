@@ -341,7 +341,6 @@ gdr_status_t gdr_layer_norm_fwd(const gdr_norm_problem_t* p, const void* x, cons
     a.p = *p;
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
     a.stream = static_cast<hipStream_t>(stream);
-    a.wide = wide_rows(p->io_dtype, p->cols, p->x_stride) && aligned(x, 16) && aligned(y, 16);
     return done(gdr::launch_norm_fwd(a));
 }
 
@@ -368,7 +367,6 @@ gdr_status_t gdr_layer_norm_bwd(const gdr_norm_problem_t* p, const void* x, cons
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.partial = static_cast<float*>(workspace);
     a.stream = static_cast<hipStream_t>(stream);
-    a.wide = wide_rows(p->io_dtype, p->cols, p->x_stride) && aligned(x, 16) && aligned(d_y, 16) && aligned(dx, 16);
     return done(gdr::launch_norm_bwd(a));
 }
 
