@@ -65,10 +65,10 @@ gdr_status_t check_seqs(int64_t batch, int64_t seq_len, int32_t num_seqs, const 
     return GDR_OK;
 }
 
-gdr_status_t check_stride(const char* name, int64_t stride, int64_t row) {
-    if (stride < row || stride > ((int64_t)1 << 40))
-        return fail(GDR_ERR_SHAPE, "%s (%lld) must be at least the row's %lld elements", name, (long long)stride,
-                    (long long)row);
+gdr_status_t check_stride(const char* name, int64_t stride, int64_t row, int64_t most = (int64_t)1 << 40) {
+    if (stride < row || stride > most)
+        return fail(GDR_ERR_SHAPE, "%s (%lld) must be at least the row's %lld elements and at most %lld", name,
+                    (long long)stride, (long long)row, (long long)most);
     return GDR_OK;
 }
 
@@ -145,11 +145,14 @@ gdr_status_t check_scan(const gdr_scan_problem_t* p, bool has_z) {
     if (p->dt_softplus != 0 && p->dt_softplus != 1)
         return fail(GDR_ERR_UNSUPPORTED, "dt_softplus must be 0 or 1 (got %d)", p->dt_softplus);
     const int64_t rows = (int64_t)p->groups * p->state_dim;
-    GDR_TRY(check_stride("x_stride", p->x_stride, p->channels));
-    GDR_TRY(check_stride("dt_stride", p->dt_stride, p->channels));
-    if (has_z) GDR_TRY(check_stride("z_stride", p->z_stride, p->channels));
-    GDR_TRY(check_stride("b_stride", p->b_stride, rows));
-    return check_stride("c_stride", p->c_stride, rows);
+    // a tile of 128 tokens lies within the 2^31 bytes of a buffer's offsets
+    const int64_t most = ((int64_t)1 << 22) - 1;
+    if (p->channels > most) return fail(GDR_ERR_SHAPE, "channels must be at most %lld", (long long)most);
+    GDR_TRY(check_stride("x_stride", p->x_stride, p->channels, most));
+    GDR_TRY(check_stride("dt_stride", p->dt_stride, p->channels, most));
+    if (has_z) GDR_TRY(check_stride("z_stride", p->z_stride, p->channels, most));
+    GDR_TRY(check_stride("b_stride", p->b_stride, rows, most));
+    return check_stride("c_stride", p->c_stride, rows, most);
 }
 
 gdr::ScanArgs scan_args(const gdr_scan_problem_t* p, const void* x, const void* dt, const float* A, const void* B,

@@ -36,13 +36,14 @@ template <int SPL> constexpr size_t fwd_lds(int nw) {
     return 4 * ((size_t)nw * (kFwdWaveFloats<SPL> + 2 * kFwdPubFloats<SPL>) + 2 * 64 * SPL);
 }
 
-template <typename T, int SPL>
+// OT: type of y; GATE: z is there; SOFT: softplus of dt
+template <typename T, typename OT, int SPL, bool GATE, bool SOFT>
 __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, int cbg) {
     constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, g, cb;
     if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
     const bool act = cb * kCh + c < Dg;
@@ -64,44 +65,57 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
         h0[i] = in && a.S0 ? a.S0[st0 + i] : 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
-    const int o32 = a.p.out_dtype == GDR_F32;
 
-    const T zero = to_t<T>(0.f);
+    // this lane's tokens in a tile are wave L + 4 k + q
+    const int row = wave * L, tile = nw * L;
+    int ox[K], odt[K], oz[K], oy[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t r = row + 4 * k + q;
+        ox[k] = act ? (int)((r * a.p.x_stride + ch) * (int)sizeof(T)) : kNowhere;
+        odt[k] = act ? (int)((r * a.p.dt_stride + ch) * (int)sizeof(T)) : kNowhere;
+        oz[k] = act ? (int)((r * a.p.z_stride + ch) * (int)sizeof(T)) : kNowhere;
+        oy[k] = act ? (int)((r * a.p.channels + ch) * (int)sizeof(OT)) : kNowhere;
+    }
     T rx[K], rdt[K], rz[K];
     StateRows<T, SPL, L> rB, rC;
-    auto fetch = [&](int64_t t0) {
+    rB.init(a.p.b_stride, g * S, S, row);
+    rC.init(a.p.c_stride, g * S, S, row);
+    auto fetch = [&](int64_t tb) {
+        const int64_t rows = e - tb < tile ? (e - tb > 0 ? e - tb : 0) : tile;
+        const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t t = t0 + 4 * k + q;
-            rx[k] = rdt[k] = rz[k] = zero;
-            if (act && t < e) {
-                rx[k] = ((const T*)a.x)[t * a.p.x_stride + ch];
-                rdt[k] = ((const T*)a.dt)[t * a.p.dt_stride + ch];
-                if (a.z) rz[k] = ((const T*)a.z)[t * a.p.z_stride + ch];
-            }
+            rx[k] = buf_load<T>(bx, ox[k]);
+            rdt[k] = buf_load<T>(bdt, odt[k]);
         }
-        rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
-        rC.load(a.C, a.p.c_stride, (int64_t)g * S, S, t0, e);
+        if (GATE) {
+            const auto bz = token_rows<T>(a.z, tb, a.p.z_stride, rows);
+#pragma unroll
+            for (int k = 0; k < K; ++k) rz[k] = buf_load<T>(bz, oz[k]);
+        }
+        rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
+        rC.load(token_rows<T>(a.C, tb, a.p.c_stride, rows));
     };
-    fetch(s + wave * L);
+    fetch(s);
     int buf = 0;
-    for (int64_t tb = s; tb < e; tb += (int64_t)nw * L, buf ^= 1) {
-        const int64_t t0 = tb + wave * L;
+    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1) {
+        const int left = (int)(e - tb < tile ? e - tb : tile);
         wave_lds_fence();
         float x[K], z[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             x[k] = to_f(rx[k]);
-            z[k] = to_f(rz[k]);
+            if (GATE) z[k] = to_f(rz[k]);
             float d = to_f(rdt[k]) + bias;
-            if (a.p.dt_softplus) d = softplus(d);
-            d = t0 + 4 * k + q < e ? d : 0.f;               // past the end: the state stays as it is
+            if (SOFT) d = softplus(d);
+            d = row + 4 * k + q < left ? d : 0.f;           // past the end: the state stays as it is
             *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x[k]};
         }
         rB.put(sB);
         rC.put(sC);
         wave_lds_fence();
-        fetch(t0 + (int64_t)nw * L);
+        fetch(tb + tile);
 
         float ea[L][SPL], b[L][SPL], P[SPL], hl[SPL], sum = 0.f;
 #pragma unroll
@@ -121,19 +135,13 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
         }
 #pragma unroll
         for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
-        float* my = pub + (size_t)(buf * nw + wave) * kFwdPubFloats<SPL> + lane * SPL;
-        lds_write(my, P);
-        lds_write(my + 64 * SPL, hl);
+        float* all = pub + buf * nw * kFwdPubFloats<SPL> + lane * SPL;
+        lds_write(all + wave * kFwdPubFloats<SPL>, P);
+        lds_write(all + wave * kFwdPubFloats<SPL> + 64 * SPL, hl);
         lds_barrier();
         if (tb != s) lds_read(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
-        for (int w = 0; w < wave; ++w) {
-            const float* p = pub + (size_t)(buf * nw + w) * kFwdPubFloats<SPL> + lane * SPL;
-            float Pw[SPL], hw[SPL];
-            lds_read(p, Pw);
-            lds_read(p + 64 * SPL, hw);
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(Pw[i], h0[i], hw[i]);
-        }
+        join_pieces<SPL, true>(all, kFwdPubFloats<SPL>, 64 * SPL, 0, wave, h0);
+        const auto by = token_rows<OT>(a.y, tb, a.p.channels, left);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float y[4];
@@ -150,9 +158,8 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
                 }
             }
             float v = __builtin_fmaf(skip, x[k], rows_sum4(y));
-            if (a.z) v *= silu(z[k]);
-            const int64_t t = t0 + 4 * k + q;
-            if (act && t < e) store_as<T>(a.y, t * a.p.channels + ch, v, o32);
+            if (GATE) v *= silu(z[k]);
+            buf_store<OT>(by, oy[k], v);
         }
         if (wave == nw - 1) lds_write(carry + buf * 64 * SPL + lane * SPL, h0);
     }
@@ -232,7 +239,15 @@ hipError_t fwd(const ScanArgs& a) {
     static_assert(fwd_lds<SPL>(most) <= 160 * 1024, "LDS of a compute unit");
     const int nw = waves_for(a.max_len, kPiece<SPL>, most);
     if (!grid_fits(units + 8, 64 * nw)) return hipErrorInvalidConfiguration;
-    k_scan_fwd<T, SPL><<<dim3((unsigned)((units + 7) / 8 * 8)), 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, units, cbg);
+    const dim3 grid((unsigned)((units + 7) / 8 * 8));
+    auto go = [&](auto out, auto gate, auto soft) {
+        k_scan_fwd<T, decltype(out), SPL, decltype(gate)::value, decltype(soft)::value>
+            <<<grid, 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, units, cbg);
+    };
+    auto by_gate = [&](auto out, auto soft) { a.z ? go(out, std::true_type{}, soft) : go(out, std::false_type{}, soft); };
+    auto by_out = [&](auto soft) { a.p.out_dtype == GDR_F32 ? by_gate(float{}, soft) : by_gate(T{}, soft); };
+    if (a.p.dt_softplus) by_out(std::true_type{});
+    else by_out(std::false_type{});
     return hipGetLastError();
 }
 

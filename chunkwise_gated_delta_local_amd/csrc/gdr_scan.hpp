@@ -28,6 +28,9 @@ __device__ __forceinline__ float rows_sum4(float (&v)[4]) {
     return a + b;
 }
 
+// the wavefront's number in its workgroup, as a scalar
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // LDS written by some lanes of a wavefront is read by others of the same one:
 // its LDS operations complete in order; this keeps the compiler from moving them.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -47,21 +50,43 @@ __device__ __forceinline__ bool unit_of(int64_t units, int cbg, int groups, int*
     return true;
 }
 
-// The rows of B (or C) of L tokens from t0 into LDS as [token][4 SPL] fp32,
-// zero past the sequence and past state_dim.
+// Rows of a token tensor from token t on, `rows` of them: a buffer whose accesses
+// past its end read zero and store nothing, so that the tokens behind a sequence
+// need no branches. Offsets inside are bytes, (token - t) * stride + element.
+constexpr int kNowhere = 0x7fffffff;                       // an offset past the end of any of them
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t token_rows(const void* base, int64_t t, int64_t stride, int64_t rows) {
+    return buf_rsrc((const T*)base + t * stride, (uint32_t)(rows * stride * (int64_t)sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T buf_load(__amdgpu_buffer_rsrc_t rs, int off) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0));
+    else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+}
+template <typename T>
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t rs, int off, float v) {
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, to_t<T>(v)), rs, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, to_t<T>(v)), rs, off, 0, 0);
+}
+
+// The rows of B (or C) of a wavefront's L tokens, the first at row `row` of the
+// buffer, into LDS as [token][4 SPL] fp32, zero past the sequence and past state_dim.
 template <typename T, int SPL, int L>
 struct StateRows {
     static constexpr int SP = 4 * SPL, PER = L * SP / 64;
+    int off[PER];
     T r[PER];
-    __device__ __forceinline__ void load(const void* base, int64_t stride, int64_t first, int S, int64_t t0, int64_t e) {
+    __device__ __forceinline__ void init(int64_t stride, int first, int S, int row) {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int idx = i * 64 + lane, n = idx % SP;
-            const int64_t t = t0 + idx / SP;
-            r[i] = to_t<T>(0.f);
-            if (t < e && n < S) r[i] = ((const T*)base)[t * stride + first + n];
+            off[i] = n < S ? (int)(((row + idx / SP) * stride + first + n) * (int)sizeof(T)) : kNowhere;
         }
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) r[i] = buf_load<T>(rs, off[i]);
     }
     __device__ __forceinline__ void put(float* lds) const {
         const int lane = threadIdx.x & 63;
@@ -93,6 +118,30 @@ __device__ __forceinline__ void lds_write(float* p, const float (&v)[N]) {
         for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
         *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]};
+    }
+}
+
+// v <- P v + x for the pieces [w0, w1) in order (FORWARD) or from the last to the
+// first: P and x of piece w at pub + w * stride, + off. The values of
+// several pieces are on their way together.
+template <int N, bool FORWARD>
+__device__ __forceinline__ void join_pieces(const float* pub, int stride, int off, int w0, int w1, float (&v)[N]) {
+    constexpr int B = N < 16 ? 16 / N : 1;
+    for (int i0 = 0; i0 < w1 - w0; i0 += B) {
+        float P[B][N], x[B][N];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (i0 + k >= w1 - w0) break;
+            const float* p = pub + (FORWARD ? w0 + i0 + k : w1 - 1 - i0 - k) * stride;
+            lds_read(p, P[k]);
+            lds_read(p + off, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (i0 + k >= w1 - w0) break;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __builtin_fmaf(P[k][i], v[i], x[k][i]);
+        }
     }
 }
 

@@ -26,9 +26,18 @@ namespace gdr {
 
 namespace {
 
+#ifndef BJ
+#define BJ 1
+#endif
+#ifndef BL
+#define BL 8
+#endif
+#ifndef BNW
+#define BNW 8
+#endif
 // Variants by states a lane: J channels a lane, L tokens a piece, at most NW wavefronts
 template <int SPL> struct Bwd {
-    static constexpr int J = SPL <= 4 ? 2 : 1, L = SPL <= 8 ? 8 : 4, NW = SPL <= 8 ? 8 : 4;
+    static constexpr int J = SPL <= 4 ? BJ : 1, L = SPL <= 8 ? BL : 4, NW = SPL <= 8 ? BNW : 4;
     static constexpr int EPT = SPL * J, SP = 4 * SPL, CHB = kCh * J;
     static constexpr int kWaveFloats = L * CHB * 4 + 2 * L * SP;      // (delta, delta x, ds, -); B, C
     static constexpr int kPubFloats = 3 * 64 * EPT;                   // P, h_loc, G_loc
@@ -53,13 +62,13 @@ __device__ __forceinline__ float sum_states(float x) { return add_dpp<0x128>(add
 // partial tiles of the sequences before it.
 __device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) { return s / tile + n; }
 
-template <typename T, int SPL>
-__global__ __launch_bounds__(512, 2) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg) {
-    constexpr int L = Bwd<SPL>::L, K = (L + 3) / 4, SP = 4 * SPL;
+template <typename T, int SPL, bool SOFT>
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg) {
+    constexpr int L = Bwd<SPL>::L, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, g, cb;
     if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
     const bool act = cb * kCh + c < Dg;
@@ -77,39 +86,45 @@ __global__ __launch_bounds__(512, 2) void k_scan_states(ScanArgs a, float* state
         h0[i] = in && a.S0 ? a.S0[((int64_t)n * a.p.channels + ch) * S + q * SPL + i] : 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
-    const T zero = to_t<T>(0.f);
+    const int row = wave * L, tile = nw * L;
+    int ox[K], odt[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t r = row + 4 * k + q;
+        ox[k] = act ? (int)((r * a.p.x_stride + ch) * (int)sizeof(T)) : kNowhere;
+        odt[k] = act ? (int)((r * a.p.dt_stride + ch) * (int)sizeof(T)) : kNowhere;
+    }
     T rx[K], rdt[K];
     StateRows<T, SPL, L> rB;
-    auto fetch = [&](int64_t t0) {
+    rB.init(a.p.b_stride, g * S, S, row);
+    auto fetch = [&](int64_t tb) {
+        const int64_t rows = e - tb < tile ? (e - tb > 0 ? e - tb : 0) : tile;
+        const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t t = t0 + 4 * k + q;
-            rx[k] = rdt[k] = zero;
-            if (act && t < e) {
-                rx[k] = ((const T*)a.x)[t * a.p.x_stride + ch];
-                rdt[k] = ((const T*)a.dt)[t * a.p.dt_stride + ch];
-            }
+            rx[k] = buf_load<T>(bx, ox[k]);
+            rdt[k] = buf_load<T>(bdt, odt[k]);
         }
-        rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
+        rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
     };
-    fetch(s + wave * L);
-    int64_t slot = first_slot(s, nw * L, n);
+    fetch(s);
+    int64_t slot = first_slot(s, tile, n);
     int buf = 0;
-    for (int64_t tb = s; tb < e; tb += (int64_t)nw * L, buf ^= 1, ++slot) {
-        const int64_t t0 = tb + wave * L;
+    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1, ++slot) {
+        const int left = (int)(e - tb < tile ? e - tb : tile);
         wave_lds_fence();
         if (wave == 0 && act) lds_write(states + (slot * a.p.channels + ch) * SP + q * SPL, h0);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float x = to_f(rx[k]);
             float d = to_f(rdt[k]) + bias;
-            if (a.p.dt_softplus) d = softplus(d);
-            d = t0 + 4 * k + q < e ? d : 0.f;
+            if (SOFT) d = softplus(d);
+            d = row + 4 * k + q < left ? d : 0.f;
             *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x};
         }
         rB.put(sB);
         wave_lds_fence();
-        fetch(t0 + (int64_t)nw * L);
+        fetch(tb + tile);
         float P[SPL], hl[SPL], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < SPL; ++i) hl[i] = 0.f;
@@ -125,29 +140,22 @@ __global__ __launch_bounds__(512, 2) void k_scan_states(ScanArgs a, float* state
         }
 #pragma unroll
         for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
-        float* my = pub + (size_t)(buf * nw + wave) * 128 * SPL + lane * SPL;
-        lds_write(my, P);
-        lds_write(my + 64 * SPL, hl);
+        float* all = pub + buf * nw * 128 * SPL + lane * SPL;
+        lds_write(all + wave * 128 * SPL, P);
+        lds_write(all + wave * 128 * SPL + 64 * SPL, hl);
         lds_barrier();
-        for (int w = 0; w < nw; ++w) {
-            const float* p = pub + (size_t)(buf * nw + w) * 128 * SPL + lane * SPL;
-            float Pw[SPL], hw[SPL];
-            lds_read(p, Pw);
-            lds_read(p + 64 * SPL, hw);
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(Pw[i], h0[i], hw[i]);
-        }
+        join_pieces<SPL, true>(all, 128 * SPL, 64 * SPL, 0, nw, h0);
     }
 }
 
-template <typename T, int SPL>
-__global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+template <typename T, int SPL, bool GATE, bool SOFT>
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
     typedef Bwd<SPL> V;
     constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, g, cb;
     if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = (lane & 3) | ((lane >> 4) << 2), q = (lane >> 2) & 3, l3 = lane & 3;
     const int D = a.p.channels, Dg = D / a.p.groups, S = a.p.state_dim;
     float* sd = lds + wave * V::kWaveFloats;                // [L][CHB][4]
@@ -179,38 +187,73 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
             dA[j * SPL + i] = 0.f;
         }
     }
-    const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
-    const int tile = nw * L;
+    const bool dy32 = a.p.dy_dtype == GDR_F32 && sizeof(T) == 2, g32 = a.p.grad_dtype == GDR_F32;
+    const int dyb = a.p.dy_dtype == GDR_F32 ? 4 : 2, gb = g32 ? 4 : 2;
+    const int row = wave * L, tile = nw * L;
     const int64_t ntiles = (e - s + tile - 1) / tile;
     float* part = ws.bc + (int64_t)cb * 2 * a.Ttot * a.p.groups * S;
-    const T zero = to_t<T>(0.f);
+    // this lane's tokens in a tile are wave L + 4 k + q; the offsets of the first, and bytes between k and k + 1
+    const int64_t r0 = row + q;
+    int ox[J], odt[J], oz[J], ody[J], og[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        ox[j] = act[j] ? (int)((r0 * a.p.x_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
+        odt[j] = act[j] ? (int)((r0 * a.p.dt_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
+        oz[j] = act[j] ? (int)((r0 * a.p.z_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
+        ody[j] = act[j] ? (int)((r0 * D + ch[j]) * dyb) : kNowhere;
+        og[j] = act[j] ? (int)((r0 * D + ch[j]) * gb) : kNowhere;
+    }
+    const int kx = (int)(4 * a.p.x_stride * (int)sizeof(T)), kdt = (int)(4 * a.p.dt_stride * (int)sizeof(T));
+    const int kz = (int)(4 * a.p.z_stride * (int)sizeof(T)), kdy = 4 * D * dyb, kg = 4 * D * gb;
+    // rows [t, t + rows) of a dense [Ttot, D] tensor of elements of `bytes` bytes
+    auto dense_rows = [&](const void* p, int64_t t, int rows, int bytes) {
+        return buf_rsrc((const char*)p + t * D * bytes, (uint32_t)((int64_t)rows * D * bytes));
+    };
     T rx[K][J], rdt[K][J], rz[K][J];
-    float rdy[K][J];
+    uint32_t rdy[K][J];
     StateRows<T, SPL, L> rB, rC;
-    auto fetch = [&](int64_t t0) {                          // t0 < s: nothing left
+    rB.init(a.p.b_stride, g * S, S, row);
+    rC.init(a.p.c_stride, g * S, S, row);
+    auto fetch = [&](int64_t tb) {                          // tb < s: nothing left
+        const int rows = tb < s ? 0 : (int)(e - tb < tile ? e - tb : tile);
+        const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
+        const auto bdy = dense_rows(a.d_y, tb, rows, dyb);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int64_t t = t0 + 4 * k + q;
-                rx[k][j] = rdt[k][j] = rz[k][j] = zero;
-                rdy[k][j] = 0.f;
-                if (act[j] && t < e && t >= s) {
-                    rx[k][j] = ((const T*)a.x)[t * a.p.x_stride + ch[j]];
-                    rdt[k][j] = ((const T*)a.dt)[t * a.p.dt_stride + ch[j]];
-                    if (a.z) rz[k][j] = ((const T*)a.z)[t * a.p.z_stride + ch[j]];
-                    rdy[k][j] = load_as<T>(a.d_y, t * D + ch[j], dy32);
-                }
+                rx[k][j] = buf_load<T>(bx, ox[j] + k * kx);
+                rdt[k][j] = buf_load<T>(bdt, odt[j] + k * kdt);
             }
-        if (t0 >= s) {
-            rB.load(a.B, a.p.b_stride, (int64_t)g * S, S, t0, e);
-            rC.load(a.C, a.p.c_stride, (int64_t)g * S, S, t0, e);
+        if (GATE) {
+            const auto bz = token_rows<T>(a.z, tb, a.p.z_stride, rows);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < J; ++j) rz[k][j] = buf_load<T>(bz, oz[j] + k * kz);
         }
+        // the raw bits, so that nothing waits for them here
+        if (sizeof(T) == 4 || dy32) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < J; ++j) rdy[k][j] = __float_as_uint(buf_load<float>(bdy, ody[j] + k * kdy));
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    rdy[k][j] = __builtin_bit_cast(unsigned short, buf_load<bf16>(bdy, ody[j] + k * kdy));
+        }
+        rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
+        rC.load(token_rows<T>(a.C, tb, a.p.c_stride, rows));
     };
-    fetch(s + (ntiles - 1) * tile + wave * L);
+    const int shift = sizeof(T) == 4 || dy32 ? 0 : 16;      // raw bits of d_y to fp32
+    if (ntiles > 0) fetch(s + (ntiles - 1) * tile);
     int buf = 0;
     for (int64_t it = ntiles - 1; it >= 0; --it, buf ^= 1) {
-        const int64_t t0 = s + it * tile + wave * L;
+        const int64_t tb = s + it * tile, t0 = tb + row;
+        const int left = (int)(e - tb < tile ? e - tb : tile);
         float h[L + 1][EPT], ea[L][EPT];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -226,18 +269,18 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 x[k][j] = to_f(rx[k][j]);
-                z[k][j] = to_f(rz[k][j]);
-                dy[k][j] = rdy[k][j];
+                if (GATE) z[k][j] = to_f(rz[k][j]);
+                dy[k][j] = __uint_as_float(rdy[k][j] << shift);
                 pre[k][j] = to_f(rdt[k][j]) + bias[j];
-                float d = a.p.dt_softplus ? softplus(pre[k][j]) : pre[k][j];
-                d = act[j] && t0 + 4 * k + q < e ? d : 0.f;
-                const float ds = a.z ? dy[k][j] * silu(z[k][j]) : dy[k][j];
+                float d = SOFT ? softplus(pre[k][j]) : pre[k][j];
+                d = act[j] && row + 4 * k + q < left ? d : 0.f;
+                const float ds = GATE ? dy[k][j] * silu(z[k][j]) : dy[k][j];
                 *reinterpret_cast<f32x4*>(sd + ((4 * k + q) * CHB + c + kCh * j) * 4) = f32x4{d, d * x[k][j], ds, 0.f};
             }
         rB.put(sB);
         rC.put(sC);
         wave_lds_fence();
-        fetch(t0 - tile);
+        fetch(tb - tile);
 
         // the piece from a zero state, and its G from zero behind it
         float P[EPT], hl[EPT], Gl[EPT], sum[J];
@@ -279,28 +322,14 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int i = 0; i < SPL; ++i) P[j * SPL + i] = __builtin_amdgcn_exp2f(A2[j * SPL + i] * sum[j]);
-        float* my = pub + (size_t)(buf * nw + wave) * V::kPubFloats + lane * EPT;
-        lds_write(my, P);
-        lds_write(my + 64 * EPT, hl);
-        lds_write(my + 128 * EPT, Gl);
+        float* all = pub + buf * nw * V::kPubFloats + lane * EPT;
+        lds_write(all + wave * V::kPubFloats, P);
+        lds_write(all + wave * V::kPubFloats + 64 * EPT, hl);
+        lds_write(all + wave * V::kPubFloats + 128 * EPT, Gl);
         lds_barrier();
         if (it != ntiles - 1) lds_read(carry + (buf ^ 1) * 64 * EPT + lane * EPT, G);
-        for (int w = 0; w < wave; ++w) {
-            const float* p = pub + (size_t)(buf * nw + w) * V::kPubFloats + lane * EPT;
-            float u[EPT], v[EPT];
-            lds_read(p, u);
-            lds_read(p + 64 * EPT, v);
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) h[0][i] = __builtin_fmaf(u[i], h[0][i], v[i]);
-        }
-        for (int w = nw - 1; w > wave; --w) {
-            const float* p = pub + (size_t)(buf * nw + w) * V::kPubFloats + lane * EPT;
-            float u[EPT], v[EPT];
-            lds_read(p, u);
-            lds_read(p + 128 * EPT, v);
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) G[i] = __builtin_fmaf(u[i], G[i], v[i]);
-        }
+        join_pieces<EPT, true>(all, V::kPubFloats, 64 * EPT, 0, wave, h[0]);
+        join_pieces<EPT, false>(all, V::kPubFloats, 128 * EPT, wave + 1, nw, G);
 #pragma unroll
         for (int m = 0; m < L; ++m) {
             float Bv[SPL];
@@ -339,7 +368,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
                         const float gp = gr * (ea[m][o] * h[m][o]);
                         tB = __builtin_fmaf(gr, Bv[i], tB);
                         tA = __builtin_fmaf(gp, A2[o], tA);
-                        tC = __builtin_fmaf(Cv[i], h[m + 1][o], tC);
+                        if (GATE) tC = __builtin_fmaf(Cv[i], h[m + 1][o], tC);
                         dA[o] = __builtin_fmaf(gp, d[0], dA[o]);
                         dBv[i] = j ? __builtin_fmaf(gr, d[1], dBv[i]) : gr * d[1];
                         dCv[i] = j ? __builtin_fmaf(d[2], h[m + 1][o], dCv[i]) : d[2] * h[m + 1][o];
@@ -347,7 +376,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
                     }
                     tB = sum_states(tB);
                     tA = sum_states(tA);
-                    if (a.z) tC = sum_states(tC);
+                    if (GATE) tC = sum_states(tC);
                     gB[j] = q == m4 ? tB : gB[j];
                     gA[j] = q == m4 ? tA : gA[j];
                     yC[j] = q == m4 ? tC : yC[j];
@@ -373,21 +402,30 @@ __global__ __launch_bounds__(512, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, i
                 for (int i = 0; i < H2; ++i)
                     if (n0 + i < S) part[at + n0 + i] = u[i];
             }
+            const auto bdx = dense_rows(a.dx, tb, left, gb), bddt = dense_rows(a.ddt, tb, left, gb);
+            const auto bdz = dense_rows(GATE ? a.dz : a.dx, tb, left, gb);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float dy_ = dy[k][j], x_ = x[k][j];
-                float delta = a.p.dt_softplus ? softplus(pre[k][j]) : pre[k][j];
-                const float ds = a.z ? dy_ * silu(z[k][j]) : dy_;
+                const float delta = SOFT ? softplus(pre[k][j]) : pre[k][j];
+                const float ds = GATE ? dy_ * silu(z[k][j]) : dy_;
                 const float ddelta = __builtin_fmaf(gA[j], kLn2, x_ * gB[j]);
-                const float ddt = a.p.dt_softplus ? ddelta * sigmoid(pre[k][j]) : ddelta;
-                if (act[j] && tk + q < e) {
-                    const int64_t at = (tk + q) * D + ch[j];
-                    store_as<T>(a.dx, at, __builtin_fmaf(skip[j], ds, delta * gB[j]), g32);
-                    store_as<T>(a.ddt, at, ddt, g32);
-                    if (a.z) store_as<T>(a.dz, at, dy_ * __builtin_fmaf(skip[j], x_, yC[j]) * silu_grad(z[k][j]), g32);
-                    sumD[j] = __builtin_fmaf(ds, x_, sumD[j]);
-                    sumT[j] += ddt;
+                float ddt = SOFT ? ddelta * sigmoid(pre[k][j]) : ddelta;
+                const float dx_ = __builtin_fmaf(skip[j], ds, delta * gB[j]);
+                const float dz_ = GATE ? dy_ * __builtin_fmaf(skip[j], x_, yC[j]) * silu_grad(z[k][j]) : 0.f;
+                const int o = og[j] + k * kg;
+                if (g32) {
+                    buf_store<float>(bdx, o, dx_);
+                    buf_store<float>(bddt, o, ddt);
+                    if (GATE) buf_store<float>(bdz, o, dz_);
+                } else {
+                    buf_store<T>(bdx, o, dx_);
+                    buf_store<T>(bddt, o, ddt);
+                    if (GATE) buf_store<T>(bdz, o, dz_);
                 }
+                ddt = row + 4 * k + q < left ? ddt : 0.f;
+                sumD[j] = __builtin_fmaf(ds, x_, sumD[j]);  // x and d_y are zero past the end
+                sumT[j] += ddt;
             }
         }
         if (wave == 0) lds_write(carry + buf * 64 * EPT + lane * EPT, G);
@@ -490,9 +528,15 @@ hipError_t bwd(const ScanArgs& a) {
     if (!grid_fits(NG * cbs + 8, 64 * nw)) return hipErrorInvalidConfiguration;
     if (NG > 0) {
         const size_t lds = 4 * (size_t)nw * (V::L * kCh * 2 + V::L * V::SP + 2 * 128 * SPL);
-        k_scan_states<T, SPL><<<grid(NG * cbs), 64 * nw, lds, a.stream>>>(a, ws.states, NG * cbs, cbs);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        k_scan_bwd<T, SPL><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, NG * cbg, cbg);
+        auto go = [&](auto gate, auto soft) {
+            constexpr bool GATE = decltype(gate)::value, SOFT = decltype(soft)::value;
+            k_scan_states<T, SPL, SOFT><<<grid(NG * cbs), 64 * nw, lds, a.stream>>>(a, ws.states, NG * cbs, cbs);
+            if ((e = hipGetLastError()) != hipSuccess) return;
+            k_scan_bwd<T, SPL, GATE, SOFT><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, NG * cbg, cbg);
+        };
+        auto by_gate = [&](auto soft) { a.z ? go(std::true_type{}, soft) : go(std::false_type{}, soft); };
+        a.p.dt_softplus ? by_gate(std::true_type{}) : by_gate(std::false_type{});
+        if (e != hipSuccess) return e;
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t D = a.p.channels, S = a.p.state_dim, half = a.Ttot * a.p.groups * S;
