@@ -81,12 +81,18 @@ __device__ __forceinline__ float softplus(float x) {
     const float c = e - (u - 1.f);
     return fmaxf(x, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(u), kLn2, c);
 }
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-// d/dx [x sigmoid(x)]
-__device__ __forceinline__ float silu_grad(float x) {
-    const float s = sigmoid(x);
-    return s * __builtin_fmaf(x, 1.f - s, 1.f);
+// softplus and its derivative 1 / (1 + exp(-x)) = (1 or e) / u
+__device__ __forceinline__ float softplus(float x, float* slope) {
+    const float e = exp_fast(-fabsf(x));
+    const float u = 1.f + e;
+    const float c = e - (u - 1.f);
+    *slope = (x < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(u);
+    return fmaxf(x, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(u), kLn2, c);
 }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// d/dx [x sigmoid(x)], from s = sigmoid(x)
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * __builtin_fmaf(x, 1.f - s, 1.f); }
+__device__ __forceinline__ float silu_grad(float x) { return silu_slope(x, sigmoid(x)); }
 
 // element idx of a tensor that is fp32 (f32) or of type T
 template <typename T>

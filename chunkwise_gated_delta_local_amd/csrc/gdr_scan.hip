@@ -26,10 +26,6 @@ namespace gdr {
 
 namespace {
 
-// Tokens a wavefront takes at a time: SPL * piece exponentials and as many
-// products stay in registers.
-template <int SPL> constexpr int kPiece = SPL <= 4 ? 16 : 64 / SPL;
-
 template <int SPL> constexpr int kFwdWaveFloats = kPiece<SPL> * (kCh * 2 + 8 * SPL);       // delta, delta x; B, C
 template <int SPL> constexpr int kFwdPubFloats = 64 * 2 * SPL;                             // P and h_loc of a wavefront
 template <int SPL> constexpr size_t fwd_lds(int nw) {
@@ -124,7 +120,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
         for (int j = 0; j < L; ++j) {
             const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
             float Bv[SPL];
-            lds_read(sB + j * SP + q * SPL, Bv);
+            read_vec(sB + j * SP + q * SPL, Bv);
             sum += d[0];
 #pragma unroll
             for (int i = 0; i < SPL; ++i) {
@@ -136,11 +132,12 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
 #pragma unroll
         for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
         float* all = pub + buf * nw * kFwdPubFloats<SPL> + lane * SPL;
-        lds_write(all + wave * kFwdPubFloats<SPL>, P);
-        lds_write(all + wave * kFwdPubFloats<SPL> + 64 * SPL, hl);
+        write_vec(all + wave * kFwdPubFloats<SPL>, P);
+        write_vec(all + wave * kFwdPubFloats<SPL> + 64 * SPL, hl);
         lds_barrier();
-        if (tb != s) lds_read(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
+        if (tb != s) read_vec(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
         join_pieces<SPL, true>(all, kFwdPubFloats<SPL>, 64 * SPL, 0, wave, h0);
+        loads_arrived();
         const auto by = token_rows<OT>(a.y, tb, a.p.channels, left);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -149,7 +146,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
             for (int m = 0; m < 4; ++m) {
                 const int j = 4 * k + m;
                 float Cv[SPL];
-                lds_read(sC + j * SP + q * SPL, Cv);
+                read_vec(sC + j * SP + q * SPL, Cv);
                 y[m] = 0.f;
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
@@ -161,7 +158,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
             if (GATE) v *= silu(z[k]);
             buf_store<OT>(by, oy[k], v);
         }
-        if (wave == nw - 1) lds_write(carry + buf * 64 * SPL + lane * SPL, h0);
+        if (wave == nw - 1) write_vec(carry + buf * 64 * SPL + lane * SPL, h0);
     }
     if (a.ST && act && wave == nw - 1) {
 #pragma unroll

@@ -9,6 +9,10 @@ namespace gdr {
 
 constexpr int kCh = 16;                                    // channels of a wavefront
 
+// Tokens a wavefront of the forward kernels takes at a time: SPL * piece
+// exponentials and as many products stay in registers.
+template <int SPL> constexpr int kPiece = SPL <= 4 ? 16 : 64 / SPL;
+
 __device__ __forceinline__ void swap32(float& a, float& b) {   // a = {a.lo, b.lo}, b = {a.hi, b.hi} (halves of 32 lanes)
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     a = __uint_as_float(r[0]);
@@ -96,7 +100,7 @@ struct StateRows {
 };
 
 template <int N>
-__device__ __forceinline__ void lds_read(const float* p, float (&v)[N]) {
+__device__ __forceinline__ void read_vec(const float* p, float (&v)[N]) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
@@ -112,7 +116,7 @@ __device__ __forceinline__ void lds_read(const float* p, float (&v)[N]) {
     }
 }
 template <int N>
-__device__ __forceinline__ void lds_write(float* p, const float (&v)[N]) {
+__device__ __forceinline__ void write_vec(float* p, const float (&v)[N]) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
@@ -120,6 +124,11 @@ __device__ __forceinline__ void lds_write(float* p, const float (&v)[N]) {
         *reinterpret_cast<f32x2*>(p) = f32x2{v[0], v[1]};
     }
 }
+
+// Waits for the loads in flight (the next tile's), before this tile's stores join
+// them: vector memory completes in order, so a wait at their use would be one for
+// the stores too.
+__device__ __forceinline__ void loads_arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
 
 // v <- P v + x for the pieces [w0, w1) in order (FORWARD) or from the last to the
 // first: P and x of piece w at pub + w * stride, + off. The values of
@@ -133,8 +142,8 @@ __device__ __forceinline__ void join_pieces(const float* pub, int stride, int of
         for (int k = 0; k < B; ++k) {
             if (i0 + k >= w1 - w0) break;
             const float* p = pub + (FORWARD ? w0 + i0 + k : w1 - 1 - i0 - k) * stride;
-            lds_read(p, P[k]);
-            lds_read(p + off, x[k]);
+            read_vec(p, P[k]);
+            read_vec(p + off, x[k]);
         }
 #pragma unroll
         for (int k = 0; k < B; ++k) {

@@ -32,6 +32,9 @@ namespace {
 #ifndef BL
 #define BL 8
 #endif
+#ifndef BLB
+#define BLB 2
+#endif
 #ifndef BNW
 #define BNW 8
 #endif
@@ -60,11 +63,11 @@ __device__ __forceinline__ float sum_states(float x) { return add_dpp<0x128>(add
 
 // Slot of a sequence's first tile: floor(s / tile) + n leaves room for the
 // partial tiles of the sequences before it.
-__device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) { return s / tile + n; }
+__device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) { return (int64_t)((uint32_t)s / (uint32_t)tile) + n; }
 
 template <typename T, int SPL, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg) {
-    constexpr int L = Bwd<SPL>::L, K = L / 4, SP = 4 * SPL;
+__global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg, int btile) {
+    constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, g, cb;
     if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
@@ -76,6 +79,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, f
     float* sd = lds + wave * (L * kCh * 2 + L * SP);
     float* sB = sd + L * kCh * 2;
     float* pub = lds + nw * (L * kCh * 2 + L * SP);         // [2][nw][2][64][SPL]
+    float* carry = pub + 2 * nw * 128 * SPL;                // [2][64][SPL]
     int64_t s, e;
     seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
     float A2[SPL], h0[SPL];
@@ -108,12 +112,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, f
         rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
     };
     fetch(s);
-    int64_t slot = first_slot(s, tile, n);
+    const int64_t slot = first_slot(s, btile, n);
     int buf = 0;
-    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1, ++slot) {
+    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1) {
         const int left = (int)(e - tb < tile ? e - tb : tile);
         wave_lds_fence();
-        if (wave == 0 && act) lds_write(states + (slot * a.p.channels + ch) * SP + q * SPL, h0);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float x = to_f(rx[k]);
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, f
         for (int j = 0; j < L; ++j) {
             const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
             float Bv[SPL];
-            lds_read(sB + j * SP + q * SPL, Bv);
+            read_vec(sB + j * SP + q * SPL, Bv);
             sum += d[0];
 #pragma unroll
             for (int i = 0; i < SPL; ++i)
@@ -141,15 +144,26 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_states(ScanArgs a, f
 #pragma unroll
         for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
         float* all = pub + buf * nw * 128 * SPL + lane * SPL;
-        lds_write(all + wave * 128 * SPL, P);
-        lds_write(all + wave * 128 * SPL + 64 * SPL, hl);
+        write_vec(all + wave * 128 * SPL, P);
+        write_vec(all + wave * 128 * SPL + 64 * SPL, hl);
         lds_barrier();
-        join_pieces<SPL, true>(all, 128 * SPL, 64 * SPL, 0, nw, h0);
+        if (tb != s) read_vec(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
+        join_pieces<SPL, true>(all, 128 * SPL, 64 * SPL, 0, wave, h0);
+        loads_arrived();
+        // a backward tile starts with this piece (pieces are whole parts of a tile, or the tile is all there is)
+        const int at = (int)(tb - s) + row;
+        if (at % btile == 0 && row < left && act)
+            write_vec(states + ((slot + at / btile) * a.p.channels + ch) * SP + q * SPL, h0);
+        if (wave == nw - 1) {
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(P[i], h0[i], hl[i]);
+            write_vec(carry + buf * 64 * SPL + lane * SPL, h0);
+        }
     }
 }
 
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
     typedef Bwd<SPL> V;
     constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -190,8 +204,9 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
     const bool dy32 = a.p.dy_dtype == GDR_F32 && sizeof(T) == 2, g32 = a.p.grad_dtype == GDR_F32;
     const int dyb = a.p.dy_dtype == GDR_F32 ? 4 : 2, gb = g32 ? 4 : 2;
     const int row = wave * L, tile = nw * L;
-    const int64_t ntiles = (e - s + tile - 1) / tile;
+    const int ntiles = (int)((uint32_t)(e - s + tile - 1) / (uint32_t)tile);
     float* part = ws.bc + (int64_t)cb * 2 * a.Ttot * a.p.groups * S;
+    const float* states = ws.states + first_slot(s, tile, n) * D * SP;
     // this lane's tokens in a tile are wave L + 4 k + q; the offsets of the first, and bytes between k and k + 1
     const int64_t r0 = row + q;
     int ox[J], odt[J], oz[J], ody[J], og[J];
@@ -211,11 +226,13 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
     };
     T rx[K][J], rdt[K][J], rz[K][J];
     uint32_t rdy[K][J];
+    float rh[J][SPL];
     StateRows<T, SPL, L> rB, rC;
     rB.init(a.p.b_stride, g * S, S, row);
     rC.init(a.p.c_stride, g * S, S, row);
-    auto fetch = [&](int64_t tb) {                          // tb < s: nothing left
-        const int rows = tb < s ? 0 : (int)(e - tb < tile ? e - tb : tile);
+    auto fetch = [&](int it) {                              // it < 0: nothing left
+        const int64_t tb = s + (int64_t)it * tile;
+        const int rows = it < 0 ? 0 : (int)(e - tb < tile ? e - tb : tile);
         const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
         const auto bdy = dense_rows(a.d_y, tb, rows, dyb);
 #pragma unroll
@@ -247,40 +264,48 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
         }
         rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
         rC.load(token_rows<T>(a.C, tb, a.p.c_stride, rows));
+        if (rows > 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                read_vec(states + ((int64_t)it * D + ch[j]) * SP + q * SPL, rh[j]);
+        }
     };
     const int shift = sizeof(T) == 4 || dy32 ? 0 : 16;      // raw bits of d_y to fp32
-    if (ntiles > 0) fetch(s + (ntiles - 1) * tile);
+    if (ntiles > 0) fetch(ntiles - 1);
     int buf = 0;
-    for (int64_t it = ntiles - 1; it >= 0; --it, buf ^= 1) {
-        const int64_t tb = s + it * tile, t0 = tb + row;
+    for (int it = ntiles - 1; it >= 0; --it, buf ^= 1) {
+        const int64_t tb = s + (int64_t)it * tile, t0 = tb + row;
         const int left = (int)(e - tb < tile ? e - tb : tile);
         float h[L + 1][EPT], ea[L][EPT];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            float v[SPL];
-            lds_read(ws.states + ((first_slot(s, tile, n) + it) * D + ch[j]) * SP + q * SPL, v);
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) h[0][j * SPL + i] = act[j] ? v[i] : 0.f;
-        }
+            for (int i = 0; i < SPL; ++i) h[0][j * SPL + i] = act[j] ? rh[j][i] : 0.f;
         wave_lds_fence();
-        float x[K][J], pre[K][J], z[K][J], dy[K][J];
+        // of this lane's tokens: x, delta, d delta / d dt, ds, d_y silu'(z)
+        float x[K][J], delta[K][J], slope[K][J], ds[K][J], dyg[K][J];
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 x[k][j] = to_f(rx[k][j]);
-                if (GATE) z[k][j] = to_f(rz[k][j]);
-                dy[k][j] = __uint_as_float(rdy[k][j] << shift);
-                pre[k][j] = to_f(rdt[k][j]) + bias[j];
-                float d = SOFT ? softplus(pre[k][j]) : pre[k][j];
-                d = act[j] && row + 4 * k + q < left ? d : 0.f;
-                const float ds = GATE ? dy[k][j] * silu(z[k][j]) : dy[k][j];
-                *reinterpret_cast<f32x4*>(sd + ((4 * k + q) * CHB + c + kCh * j) * 4) = f32x4{d, d * x[k][j], ds, 0.f};
+                ds[k][j] = __uint_as_float(rdy[k][j] << shift);
+                if (GATE) {
+                    const float z = to_f(rz[k][j]), sg = sigmoid(z);
+                    dyg[k][j] = ds[k][j] * silu_slope(z, sg);
+                    ds[k][j] *= z * sg;
+                }
+                const float pre = to_f(rdt[k][j]) + bias[j];
+                slope[k][j] = 1.f;
+                const float d = SOFT ? softplus(pre, &slope[k][j]) : pre;
+                delta[k][j] = act[j] && row + 4 * k + q < left ? d : 0.f;
+                *reinterpret_cast<f32x4*>(sd + ((4 * k + q) * CHB + c + kCh * j) * 4) =
+                    f32x4{delta[k][j], delta[k][j] * x[k][j], ds[k][j], 0.f};
             }
         rB.put(sB);
         rC.put(sC);
         wave_lds_fence();
-        fetch(tb - tile);
+        fetch(it - 1);
 
         // the piece from a zero state, and its G from zero behind it
         float P[EPT], hl[EPT], Gl[EPT], sum[J];
@@ -291,7 +316,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
 #pragma unroll
         for (int m = 0; m < L; ++m) {
             float Bv[SPL];
-            lds_read(sB + m * SP + q * SPL, Bv);
+            read_vec(sB + m * SP + q * SPL, Bv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
@@ -307,7 +332,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
 #pragma unroll
         for (int m = L - 1; m >= 0; --m) {
             float Cv[SPL];
-            lds_read(sC + m * SP + q * SPL, Cv);
+            read_vec(sC + m * SP + q * SPL, Cv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float ds = sd[(m * CHB + c + kCh * j) * 4 + 2];
@@ -323,17 +348,18 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
 #pragma unroll
             for (int i = 0; i < SPL; ++i) P[j * SPL + i] = __builtin_amdgcn_exp2f(A2[j * SPL + i] * sum[j]);
         float* all = pub + buf * nw * V::kPubFloats + lane * EPT;
-        lds_write(all + wave * V::kPubFloats, P);
-        lds_write(all + wave * V::kPubFloats + 64 * EPT, hl);
-        lds_write(all + wave * V::kPubFloats + 128 * EPT, Gl);
+        write_vec(all + wave * V::kPubFloats, P);
+        write_vec(all + wave * V::kPubFloats + 64 * EPT, hl);
+        write_vec(all + wave * V::kPubFloats + 128 * EPT, Gl);
         lds_barrier();
-        if (it != ntiles - 1) lds_read(carry + (buf ^ 1) * 64 * EPT + lane * EPT, G);
+        if (it != ntiles - 1) read_vec(carry + (buf ^ 1) * 64 * EPT + lane * EPT, G);
         join_pieces<EPT, true>(all, V::kPubFloats, 64 * EPT, 0, wave, h[0]);
         join_pieces<EPT, false>(all, V::kPubFloats, 128 * EPT, wave + 1, nw, G);
+        loads_arrived();
 #pragma unroll
         for (int m = 0; m < L; ++m) {
             float Bv[SPL];
-            lds_read(sB + m * SP + q * SPL, Bv);
+            read_vec(sB + m * SP + q * SPL, Bv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float dx = sd[(m * CHB + c + kCh * j) * 4 + 1];
@@ -355,8 +381,8 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
             for (int m4 = 3; m4 >= 0; --m4) {
                 const int m = 4 * k + m4;
                 float Bv[SPL], Cv[SPL], dBv[SPL], dCv[SPL];
-                lds_read(sB + m * SP + q * SPL, Bv);
-                lds_read(sC + m * SP + q * SPL, Cv);
+                read_vec(sB + m * SP + q * SPL, Bv);
+                read_vec(sC + m * SP + q * SPL, Cv);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
@@ -406,13 +432,10 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
             const auto bdz = dense_rows(GATE ? a.dz : a.dx, tb, left, gb);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float dy_ = dy[k][j], x_ = x[k][j];
-                const float delta = SOFT ? softplus(pre[k][j]) : pre[k][j];
-                const float ds = GATE ? dy_ * silu(z[k][j]) : dy_;
-                const float ddelta = __builtin_fmaf(gA[j], kLn2, x_ * gB[j]);
-                float ddt = SOFT ? ddelta * sigmoid(pre[k][j]) : ddelta;
-                const float dx_ = __builtin_fmaf(skip[j], ds, delta * gB[j]);
-                const float dz_ = GATE ? dy_ * __builtin_fmaf(skip[j], x_, yC[j]) * silu_grad(z[k][j]) : 0.f;
+                const float ddelta = __builtin_fmaf(gA[j], kLn2, x[k][j] * gB[j]);
+                float ddt = ddelta * slope[k][j];
+                const float dx_ = __builtin_fmaf(skip[j], ds[k][j], delta[k][j] * gB[j]);
+                const float dz_ = GATE ? dyg[k][j] * __builtin_fmaf(skip[j], x[k][j], yC[j]) : 0.f;
                 const int o = og[j] + k * kg;
                 if (g32) {
                     buf_store<float>(bdx, o, dx_);
@@ -424,11 +447,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW) void k_scan_bwd(ScanArgs a, Scan
                     if (GATE) buf_store<T>(bdz, o, dz_);
                 }
                 ddt = row + 4 * k + q < left ? ddt : 0.f;
-                sumD[j] = __builtin_fmaf(ds, x_, sumD[j]);  // x and d_y are zero past the end
+                sumD[j] = __builtin_fmaf(ds[k][j], x[k][j], sumD[j]);  // x and d_y are zero past the end
                 sumT[j] += ddt;
             }
         }
-        if (wave == 0) lds_write(carry + buf * 64 * EPT + lane * EPT, G);
+        if (wave == 0) write_vec(carry + buf * 64 * EPT + lane * EPT, G);
     }
     if (a.dS0 && wave == 0) {
 #pragma unroll
@@ -527,10 +550,11 @@ hipError_t bwd(const ScanArgs& a) {
     hipError_t e = hipSuccess;
     if (!grid_fits(NG * cbs + 8, 64 * nw)) return hipErrorInvalidConfiguration;
     if (NG > 0) {
-        const size_t lds = 4 * (size_t)nw * (V::L * kCh * 2 + V::L * V::SP + 2 * 128 * SPL);
+        const int nws = waves_for(a.max_len, kPiece<SPL>, SPL == 16 ? 4 : 8);
+        const size_t lds = 4 * ((size_t)nws * (kPiece<SPL> * (kCh * 2 + V::SP) + 2 * 128 * SPL) + 2 * 64 * SPL);
         auto go = [&](auto gate, auto soft) {
             constexpr bool GATE = decltype(gate)::value, SOFT = decltype(soft)::value;
-            k_scan_states<T, SPL, SOFT><<<grid(NG * cbs), 64 * nw, lds, a.stream>>>(a, ws.states, NG * cbs, cbs);
+            k_scan_states<T, SPL, SOFT><<<grid(NG * cbs), 64 * nws, lds, a.stream>>>(a, ws.states, NG * cbs, cbs, nw * V::L);
             if ((e = hipGetLastError()) != hipSuccess) return;
             k_scan_bwd<T, SPL, GATE, SOFT><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, NG * cbg, cbg);
         };
