@@ -234,7 +234,9 @@ hipError_t fwd(const ScanArgs& a) {
     const int64_t units = (int64_t)a.p.num_seqs * a.p.groups * cbg;
     constexpr int most = SPL == 16 ? 4 : 8;
     static_assert(fwd_lds<SPL>(most) <= 160 * 1024, "LDS of a compute unit");
-    const int nw = waves_for(a.max_len, kPiece<SPL>, most);
+    // 4096 wavefronts fill the card (four a SIMD as registers allow): 13 sequences of 4,099 tokens, 1,300 units: 132 us
+    // (2048: 195, 8192: 164; one sequence of 8,192, 256 units, takes all 8 in any case)
+    const int nw = waves_for(units, a.max_len, kPiece<SPL>, 4096, 1, most);
     if (!grid_fits(units + 8, 64 * nw)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((units + 7) / 8 * 8));
     auto go = [&](auto out, auto gate, auto soft) {

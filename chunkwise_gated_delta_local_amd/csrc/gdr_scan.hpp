@@ -155,10 +155,11 @@ __device__ __forceinline__ void join_pieces(const float* pub, int stride, int of
 }
 
 // ---------------------------------------------------------------- host
-// Wavefronts of a workgroup: enough pieces for the longest sequence, a power of two up to `most`.
-inline int waves_for(int64_t max_len, int piece, int most) {
+// Wavefronts of a workgroup, a power of two: as many as make `fill` in all units
+// together, at least `least`, no more than pieces in the longest sequence or than `most`.
+inline int waves_for(int64_t units, int64_t max_len, int piece, int fill, int least, int most) {
     int nw = 1;
-    while (nw < most && (int64_t)nw * piece < max_len) nw *= 2;
+    while (nw < most && (int64_t)nw * piece < max_len && (nw < least || units * nw < fill)) nw *= 2;
     return nw;
 }
 

@@ -13,10 +13,12 @@
 // incoming G from the later tile's and its successors' (P, G_loc): G at the
 // start of a piece is P G_in + G_loc.
 //
-// Layout: channel on lane bits 0, 1, 4, 5 (and J of them in a lane), state group
-// on bits 2, 3. The sums over channels (dB and dC, 2 SPL values a token) then
-// take swaps and adds over bits 5 and 4, each halving the values, and quad
-// permutes; the sums over states take row rotations by 4 and 8.
+// Layout: state group on lane bits 0 and 1, channel on bits 2 to 5 (and J of them
+// in a lane). The sums over channels (dB and dC, 2 SPL values a token) take swaps
+// and adds over bits 5 and 4, each halving the values, and row rotations by 4 and
+// 8; those over states take quad permutes. (The sums over channels as products
+// with columns of an identity on the fp32 matrix cores were slower, 463 us
+// against 395 at 4 x 2,048 x 2,048 x 16: eight 32-cycle products a token.)
 //
 // dB and dC of a token sum over all channels of a group: every workgroup stores
 // its channels' sums and k_sum_partials joins them in a fixed order.
@@ -26,23 +28,13 @@ namespace gdr {
 
 namespace {
 
-#ifndef BJ
-#define BJ 1
-#endif
-#ifndef BL
-#define BL 8
-#endif
-#ifndef BLB
-#define BLB 2
-#endif
-#ifndef BNW
-#define BNW 8
-#endif
-// Variants by states a lane: J channels a lane, L tokens a piece, at most NW wavefronts
+// Variants by states a lane: J channels a lane, L tokens a piece, at most NW wavefronts, and at least LEAST of them
+// where a sequence has the pieces (the states before the tiles are written and read once more)
 template <int SPL> struct Bwd {
-    static constexpr int J = SPL <= 4 ? BJ : 1, L = SPL <= 8 ? BL : 4, NW = SPL <= 8 ? BNW : 4;
+    static constexpr int J = SPL <= 2 ? 2 : 1, L = SPL <= 8 ? 8 : 4, NW = SPL <= 8 ? 8 : 4, LEAST = 4;
     static constexpr int EPT = SPL * J, SP = 4 * SPL, CHB = kCh * J;
-    static constexpr int kWaveFloats = L * CHB * 4 + 2 * L * SP;      // (delta, delta x, ds, -); B, C
+    static constexpr int TOK = CHB * 4 + 8;                           // floats of a token's row: its 4 writers on other banks
+    static constexpr int kWaveFloats = L * TOK + 2 * L * SP;      // (delta, delta x, ds, -); B, C
     static constexpr int kPubFloats = 3 * 64 * EPT;                   // P, h_loc, G_loc
     static constexpr size_t lds(int nw) { return 4 * ((size_t)nw * (kWaveFloats + 2 * kPubFloats) + 2 * 64 * EPT); }
 };
@@ -54,12 +46,28 @@ struct ScanBwdWs {
     float* dch;                // [N][2][D]: dD, ddt_bias
 };
 
+// own + x of another lane
 template <int CTRL>
-__device__ __forceinline__ float add_dpp(float x) {
-    return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
+__device__ __forceinline__ float add_dpp(float x, float own) {
+    return own + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float sum_quad(float x) { return add_dpp<0xb1>(add_dpp<0x4e>(x)); }      // over lane bits 0, 1
-__device__ __forceinline__ float sum_states(float x) { return add_dpp<0x128>(add_dpp<0x124>(x)); }  // over bits 2, 3
+// over lane bits 0 and 1, the state groups
+__device__ __forceinline__ float sum_states(float x) {
+    x = add_dpp<0x4e>(x, x);
+    return add_dpp<0xb1>(x, x);
+}
+// over lane bits 2 and 3, the last four channels of a row
+__device__ __forceinline__ float sum_row(float x) {
+    x = add_dpp<0x124>(x, x);
+    return add_dpp<0x128>(x, x);
+}
+// v[i] summed over the four state groups; lanes of group q keep the sum of v[q]
+__device__ __forceinline__ float states_sum4(const float (&v)[4], int q) {
+    const bool hi = q & 2, odd = q & 1;
+    const float a = add_dpp<0x4e>(hi ? v[0] : v[2], hi ? v[2] : v[0]);      // v[0] or v[2] of groups q and q ^ 2
+    const float b = add_dpp<0x4e>(hi ? v[1] : v[3], hi ? v[3] : v[1]);
+    return add_dpp<0xb1>(odd ? a : b, odd ? b : a);
+}
 
 // Slot of a sequence's first tile: floor(s / tile) + n leaves room for the
 // partial tiles of the sequences before it.
@@ -163,17 +171,17 @@ __global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, float* states, 
 }
 
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
     typedef Bwd<SPL> V;
-    constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, H2 = SPL / 2;
+    constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, TOK = V::TOK, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, g, cb;
     if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
-    const int c = (lane & 3) | ((lane >> 4) << 2), q = (lane >> 2) & 3, l3 = lane & 3;
+    const int c = lane >> 2, q = lane & 3, l4 = c & 3;
     const int D = a.p.channels, Dg = D / a.p.groups, S = a.p.state_dim;
-    float* sd = lds + wave * V::kWaveFloats;                // [L][CHB][4]
-    float* sB = sd + L * CHB * 4;                           // [L][SP]
+    float* sd = lds + wave * V::kWaveFloats;                // [L][TOK]: [CHB][4]
+    float* sB = sd + L * TOK;                           // [L][SP]
     float* sC = sB + L * SP;
     float* pub = lds + nw * V::kWaveFloats;                 // [2][nw][3][64][EPT]
     float* carry = pub + 2 * nw * V::kPubFloats;            // [2][64][EPT]
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
                 slope[k][j] = 1.f;
                 const float d = SOFT ? softplus(pre, &slope[k][j]) : pre;
                 delta[k][j] = act[j] && row + 4 * k + q < left ? d : 0.f;
-                *reinterpret_cast<f32x4*>(sd + ((4 * k + q) * CHB + c + kCh * j) * 4) =
+                *reinterpret_cast<f32x4*>(sd + (4 * k + q) * TOK + (c + kCh * j) * 4) =
                     f32x4{delta[k][j], delta[k][j] * x[k][j], ds[k][j], 0.f};
             }
         rB.put(sB);
@@ -319,7 +327,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
             read_vec(sB + m * SP + q * SPL, Bv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
+                const f32x4 d = *reinterpret_cast<const f32x4*>(sd + m * TOK + (c + kCh * j) * 4);
                 sum[j] += d[0];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
@@ -335,7 +343,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
             read_vec(sC + m * SP + q * SPL, Cv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float ds = sd[(m * CHB + c + kCh * j) * 4 + 2];
+                const float ds = sd[m * TOK + (c + kCh * j) * 4 + 2];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
                     const int o = j * SPL + i;
@@ -362,7 +370,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
             read_vec(sB + m * SP + q * SPL, Bv);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float dx = sd[(m * CHB + c + kCh * j) * 4 + 1];
+                const float dx = sd[m * TOK + (c + kCh * j) * 4 + 1];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
                     const int o = j * SPL + i;
@@ -372,9 +380,8 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
         }
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
-            float gB[J], gA[J], yC[J], u[H2];
-#pragma unroll
-            for (int j = 0; j < J; ++j) gB[j] = gA[j] = yC[j] = 0.f;
+            float gB[J][4], gA[J][4], yC[J][4];
+            float u[H2];
 #pragma unroll
             for (int i = 0; i < H2; ++i) u[i] = 0.f;
 #pragma unroll
@@ -385,7 +392,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
                 read_vec(sC + m * SP + q * SPL, Cv);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const f32x4 d = *reinterpret_cast<const f32x4*>(sd + (m * CHB + c + kCh * j) * 4);
+                    const f32x4 d = *reinterpret_cast<const f32x4*>(sd + m * TOK + (c + kCh * j) * 4);
                     float tB = 0.f, tA = 0.f, tC = 0.f;
 #pragma unroll
                     for (int i = 0; i < SPL; ++i) {
@@ -400,12 +407,9 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
                         dCv[i] = j ? __builtin_fmaf(d[2], h[m + 1][o], dCv[i]) : d[2] * h[m + 1][o];
                         G[o] = ea[m][o] * gr;
                     }
-                    tB = sum_states(tB);
-                    tA = sum_states(tA);
-                    if (GATE) tC = sum_states(tC);
-                    gB[j] = q == m4 ? tB : gB[j];
-                    gA[j] = q == m4 ? tA : gA[j];
-                    yC[j] = q == m4 ? tC : yC[j];
+                    gB[j][m4] = tB;
+                    gA[j][m4] = tA;
+                    yC[j][m4] = tC;
                 }
                 // over the channels: lanes below 32 keep dB, the others dC; rows then halve the states
 #pragma unroll
@@ -416,13 +420,13 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
 #pragma unroll
                 for (int i = 0; i < H2; ++i) {
                     swap16(dBv[i], dBv[i + H2]);
-                    const float t = sum_quad(dBv[i] + dBv[i + H2]);
-                    u[i] = l3 == m4 ? t : u[i];
+                    const float v = sum_row(dBv[i] + dBv[i + H2]);
+                    u[i] = l4 == m4 ? v : u[i];
                 }
             }
             const int64_t tk = t0 + 4 * k;
-            if (tk + l3 < e) {
-                const int64_t at = (((int64_t)(lane >> 5) * a.Ttot + tk + l3) * a.p.groups + g) * S;
+            if (tk + l4 < e) {
+                const int64_t at = (((int64_t)(lane >> 5) * a.Ttot + tk + l4) * a.p.groups + g) * S;
                 const int n0 = q * SPL + ((lane >> 4) & 1) * H2;
 #pragma unroll
                 for (int i = 0; i < H2; ++i)
@@ -432,10 +436,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, BLB) void k_scan_bwd(ScanArgs a,
             const auto bdz = dense_rows(GATE ? a.dz : a.dx, tb, left, gb);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float ddelta = __builtin_fmaf(gA[j], kLn2, x[k][j] * gB[j]);
+                const float gBs = states_sum4(gB[j], q), gAs = states_sum4(gA[j], q);
+                const float ddelta = __builtin_fmaf(gAs, kLn2, x[k][j] * gBs);
                 float ddt = ddelta * slope[k][j];
-                const float dx_ = __builtin_fmaf(skip[j], ds[k][j], delta[k][j] * gB[j]);
-                const float dz_ = GATE ? dyg[k][j] * __builtin_fmaf(skip[j], x[k][j], yC[j]) : 0.f;
+                const float dx_ = __builtin_fmaf(skip[j], ds[k][j], delta[k][j] * gBs);
+                const float dz_ = GATE ? dyg[k][j] * __builtin_fmaf(skip[j], x[k][j], states_sum4(yC[j], q)) : 0.f;
                 const int o = og[j] + k * kg;
                 if (g32) {
                     buf_store<float>(bdx, o, dx_);
@@ -513,8 +518,8 @@ struct ChannelOut {
 };
 
 // Workspace regions. States kept: one a tile of nw L tokens, and one more a
-// sequence. With fewer than NW wavefronts no sequence is longer than a tile,
-// so that T / tile <= N; otherwise the tile has NW L tokens.
+// sequence. With fewer than LEAST wavefronts no sequence is longer than a tile,
+// so that T / tile <= N; otherwise the tile has LEAST L tokens or more.
 struct BwdPlan {
     size_t states, bc, dA, dch, end;
 };
@@ -526,7 +531,7 @@ BwdPlan plan(const gdr_scan_problem_t& p) {
     BwdPlan b;
     size_t off = 0;
     auto take = [&](size_t floats) { size_t o = off; off = (off + floats * 4 + 255) & ~(size_t)255; return o; };
-    const size_t most = N < T ? N : T, tiles = T / (V::NW * V::L);
+    const size_t most = N < T ? N : T, tiles = T / (V::LEAST * V::L);
     b.states = take(((tiles > most ? tiles : most) + N) * D * V::SP);
     b.bc = take(cbg * 2 * T * p.groups * S);
     b.dA = take(N * D * S);
@@ -539,18 +544,18 @@ template <typename T, int SPL>
 hipError_t bwd(const ScanArgs& a) {
     typedef Bwd<SPL> V;
     static_assert(V::lds(V::NW) <= 160 * 1024, "LDS of a compute unit");
-    const int nw = waves_for(a.max_len, V::L, V::NW);
     const BwdPlan pl = plan<SPL>(a.p);
     auto f = [&](size_t off) { return reinterpret_cast<float*>(a.ws + off); };
     const ScanBwdWs ws = {f(pl.states), f(pl.bc), f(pl.dA), f(pl.dch)};
     const int Dg = a.p.channels / a.p.groups;
     const int64_t NG = (int64_t)a.p.num_seqs * a.p.groups;
     const int cbs = (Dg + kCh - 1) / kCh, cbg = (Dg + V::CHB - 1) / V::CHB;
+    const int nw = waves_for(NG * cbg, a.max_len, V::L, 2048, V::LEAST, V::NW);
     auto grid = [](int64_t units) { return dim3((unsigned)((units + 7) / 8 * 8)); };
     hipError_t e = hipSuccess;
     if (!grid_fits(NG * cbs + 8, 64 * nw)) return hipErrorInvalidConfiguration;
     if (NG > 0) {
-        const int nws = waves_for(a.max_len, kPiece<SPL>, SPL == 16 ? 4 : 8);
+        const int nws = waves_for(NG * cbs, a.max_len, kPiece<SPL>, 4096, 1, SPL == 16 ? 4 : 8);
         const size_t lds = 4 * ((size_t)nws * (kPiece<SPL> * (kCh * 2 + V::SP) + 2 * 128 * SPL) + 2 * 64 * SPL);
         auto go = [&](auto gate, auto soft) {
             constexpr bool GATE = decltype(gate)::value, SOFT = decltype(soft)::value;
