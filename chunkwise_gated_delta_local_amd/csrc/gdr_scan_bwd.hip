@@ -28,10 +28,12 @@ namespace gdr {
 
 namespace {
 
-// Variants by states a lane: J channels a lane, L tokens a piece, at most NW wavefronts, and at least LEAST of them
+// Variants by states a lane (ea and h of a piece and the sums take 2 SPL J L + 4 SPL J registers: pieces of 8 tokens
+// at 32 states, and 64 states at two wavefronts a SIMD, went to scratch, 1.20 and 4.47 ms against 0.61 and 1.44 at
+// as many states as 4 x 2,048 x 2,048 x 16): J channels a lane, L tokens a piece, at most NW wavefronts, and at least LEAST of them
 // where a sequence has the pieces (the states before the tiles are written and read once more)
 template <int SPL> struct Bwd {
-    static constexpr int J = SPL <= 2 ? 2 : 1, L = SPL <= 8 ? 8 : 4, NW = SPL <= 8 ? 8 : 4, LEAST = 4;
+    static constexpr int J = SPL <= 2 ? 2 : 1, L = SPL <= 4 ? 8 : 4, NW = SPL <= 8 ? 8 : 4, LEAST = 4;
     static constexpr int EPT = SPL * J, SP = 4 * SPL, CHB = kCh * J;
     static constexpr int TOK = CHB * 4 + 8;                           // floats of a token's row: its 4 writers on other banks
     static constexpr int kWaveFloats = L * TOK + 2 * L * SP;      // (delta, delta x, ds, -); B, C
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, float* states, 
 }
 
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW, 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
     typedef Bwd<SPL> V;
     constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, TOK = V::TOK, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
