@@ -26,11 +26,11 @@ constexpr int kGroup = 4;      // rows loaded together (8: 431 us instead of 412
 constexpr int kFwdV = 8, kBwdV = 4;
 
 // Tokens a wavefront walks: the longest run, up to `most`, that still makes 2048
-// wavefronts (two a SIMD); 16 where there is too little work for that. Longest:
+// wavefronts (two a SIMD); one group where there is too little work for that. Longest:
 // forward 64 (32: 422 us, 128: 422, 64: 412), backward 128 (64: 143 us, 128: 140).
 int run_length(int64_t Ttot, int wavefronts, int most) {
     int run = most;
-    while (run > 16 && (Ttot + run - 1) / run * wavefronts < 2048) run /= 2;
+    while (run > kGroup && (Ttot + run - 1) / run * wavefronts < 2048) run /= 2;
     return run;
 }
 
@@ -84,10 +84,16 @@ __device__ __forceinline__ void push(float (&hist)[W - 1][V], const float (&x)[V
 
 template <typename T, int V, int W>
 __global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a, int ncb, int64_t ntiles, int run) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % ncb;
     const int64_t tile = blockIdx.x / ncb;
     const int D = a.p.channels, ch = (cb * 64 + lane) * V;
+    const int64_t t0 = (tile * kWaves + wave) * run;
+    int q = 0;
+    if (tile < ntiles) {
+        if (t0 >= a.Ttot) return;
+        q = seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t0);
+    }
     if (ch >= D) return;
     if (tile >= ntiles) {                                // the final rows of sequences, kWaves of them a workgroup
         const int64_t q = (tile - ntiles) * kWaves + wave;
@@ -102,13 +108,10 @@ __global__ __launch_bounds__(256) void k_conv_fwd(ConvArgs a, int ncb, int64_t n
         }
         return;
     }
-    const int64_t t0 = (tile * kWaves + wave) * run;
-    if (t0 >= a.Ttot) return;
     const int64_t t1 = t0 + run < a.Ttot ? t0 + run : a.Ttot;
     Taps<T, V, W> taps;
     taps.load(a, ch);
     const bool silu_on = a.p.activation == GDR_ACT_SILU;
-    int q = seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t0);
     int64_t s, e;
     seq_range(a.cu, q, a.p.seq_len, a.Ttot, &s, &e);
     float hist[W - 1][V];
@@ -187,6 +190,8 @@ template <typename T, typename DT, typename GT, int V, int W, bool SILU>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t ntiles, int run) {
     const int64_t tile = blockIdx.x / ncb;
     const int D = a.p.channels, ch = ((int)(blockIdx.x % ncb) * (int)blockDim.x + (int)threadIdx.x) * V;
+    const int64_t t0 = tile * run;
+    int q = tile < ntiles ? seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t0) : 0;
     if (ch >= D) return;
     GT* dxp = (GT*)a.dx;
     GT* dS0 = (GT*)a.dS0;
@@ -206,13 +211,11 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t n
         }
         return;
     }
-    const int64_t t0 = tile * run;
     float dw[W][V] = {}, db[V] = {};
     {
         const int64_t t1 = t0 + run < a.Ttot ? t0 + run : a.Ttot;
         Taps<T, V, W> taps;
         taps.load(a, ch);
-        int q = seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t0);
         int64_t s, e;
         seq_range(a.cu, q, a.p.seq_len, a.Ttot, &s, &e);
         float hist[W - 1][V], dph[W - 1][V];             // rows before the token; dp of the tokens before it

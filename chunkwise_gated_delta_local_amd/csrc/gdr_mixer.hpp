@@ -181,19 +181,24 @@ __device__ __forceinline__ void seq_range(const int32_t* cu, int n, int64_t T_ro
     *e = f;
 }
 // Sequence that holds token t: the last n in [0, N) with start <= t (packed
-// sequences; empty ones before it end at its start and are passed over).
+// sequences; empty ones before it end at its start and are passed over). All 64
+// lanes of the wavefront call it with the same t: each looks at a 64th of what is
+// left, so that thousands of sequences take two loads in a row.
 __device__ __forceinline__ int seq_of_token(const int32_t* cu, int N, int64_t T_row, int64_t t) {
     if (!cu) {
-        const int64_t n = t / T_row;
+        const int64_t n = (uint32_t)t / (uint32_t)T_row;     // token indices fit 31 bits
         return (int)(n < N ? n : N - 1);
     }
-    int lo = 0, hi = N;                        // cu[lo] <= t < cu[hi] for a sound cu
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)cu[mid] <= t) lo = mid;
-        else hi = mid;
+    int lo = 0, len = N;                       // the answer is in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 63) / 64, i = lo + (int)(threadIdx.x & 63) * step;
+        const bool before = i < lo + len && (int64_t)cu[i] <= t;
+        const int k = __popcll(__ballot(before));            // starts are sorted: the first k lanes
+        const int at = k > 0 ? (k - 1) * step : 0;
+        len = len - at < step ? len - at : step;
+        lo += at;
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Workgroups of a one-dimensional launch: HIP counts its threads in 32 bits.

@@ -34,11 +34,11 @@ template <int SPL> constexpr size_t fwd_lds(int nw) {
 
 // OT: type of y; GATE: z is there; SOFT: softplus of dt
 template <typename T, typename OT, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, int cbg) {
+__global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, Segments sg, int64_t units, int cbg) {
     constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    int n, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    int n, seg, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
@@ -52,6 +52,9 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
 
     int64_t s, e;
     seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    const int64_t seq = s;
+    bool last;
+    if (!sg.range(seg, &s, &e, &last)) return;
     float A2[SPL], h0[SPL];
     const int64_t st0 = ((int64_t)n * a.p.channels + ch) * S + q * SPL;
 #pragma unroll
@@ -60,6 +63,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
         A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
         h0[i] = in && a.S0 ? a.S0[st0 + i] : 0.f;
     }
+    sg.template enter<SPL>(n, seg, seq, a.p.channels, ch, q, A2, h0);
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.D ? a.D[ch] : 0.f;
 
     // this lane's tokens in a tile are wave L + 4 k + q
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, int64_t units, 
         }
         if (wave == nw - 1) write_vec(carry + buf * 64 * SPL + lane * SPL, h0);
     }
-    if (a.ST && act && wave == nw - 1) {
+    if (a.ST && act && last && wave == nw - 1) {
 #pragma unroll
         for (int i = 0; i < SPL; ++i)
             if (q * SPL + i < S) a.ST[st0 + i] = h0[i];
@@ -228,20 +232,45 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int64_t nch) {
     }
 }
 
+// Units of whole sequences.
+int64_t units_of(const gdr_scan_problem_t& p) {
+    return (int64_t)p.num_seqs * p.groups * ((p.channels / p.groups + kCh - 1) / kCh);
+}
+template <int SPL> constexpr int kMostWaves = SPL == 16 ? 4 : 8;
+
+template <int SPL>
+size_t ends_bytes(const gdr_scan_problem_t& p, size_t* sums) {
+    const size_t slots = segment_slots(units_of(p), kMostWaves<SPL>, p.num_seqs);
+    *sums = (slots * p.channels * 4 * SPL * 4 + 255) & ~(size_t)255;
+    return *sums + slots * p.channels * 4;
+}
+
 template <typename T, int SPL>
 hipError_t fwd(const ScanArgs& a) {
-    const int Dg = a.p.channels / a.p.groups, cbg = (Dg + kCh - 1) / kCh;
-    const int64_t units = (int64_t)a.p.num_seqs * a.p.groups * cbg;
-    constexpr int most = SPL == 16 ? 4 : 8;
+    constexpr int most = kMostWaves<SPL>;
     static_assert(fwd_lds<SPL>(most) <= 160 * 1024, "LDS of a compute unit");
+    const int cbg = (a.p.channels / a.p.groups + kCh - 1) / kCh;
+    const int64_t whole = units_of(a.p);
+    Segments sg = segments_for(whole, most, a.max_len);
+    const int64_t units = whole * sg.most;
     // 4096 wavefronts fill the card (four a SIMD as registers allow): 13 sequences of 4,099 tokens, 1,300 units: 132 us
     // (2048: 195, 8192: 164; one sequence of 8,192, 256 units, takes all 8 in any case)
-    const int nw = waves_for(units, a.max_len, kPiece<SPL>, 4096, 1, most);
+    const int nw = waves_for(units, sg.most > 1 ? sg.len : a.max_len, kPiece<SPL>, 4096, 1, most);
     if (!grid_fits(units + 8, 64 * nw)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((units + 7) / 8 * 8));
+    hipError_t e = hipSuccess;
+    if (sg.most > 1) {
+        size_t sums;
+        ends_bytes<SPL>(a.p, &sums);
+        sg.end = reinterpret_cast<float*>(a.ws);
+        sg.sum = reinterpret_cast<float*>(a.ws + sums);
+        if (a.p.dt_softplus) k_scan_states<T, SPL, true, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, units, cbg, 1);
+        else k_scan_states<T, SPL, false, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, units, cbg, 1);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     auto go = [&](auto out, auto gate, auto soft) {
         k_scan_fwd<T, decltype(out), SPL, decltype(gate)::value, decltype(soft)::value>
-            <<<grid, 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, units, cbg);
+            <<<grid, 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, sg, units, cbg);
     };
     auto by_gate = [&](auto out, auto soft) { a.z ? go(out, std::true_type{}, soft) : go(out, std::false_type{}, soft); };
     auto by_out = [&](auto soft) { a.p.out_dtype == GDR_F32 ? by_gate(float{}, soft) : by_gate(T{}, soft); };
@@ -271,7 +300,13 @@ hipError_t step(const ScanArgs& a) {
 
 }  // namespace
 
-size_t scan_fwd_workspace(const gdr_scan_problem_t&) { return 0; }
+size_t scan_fwd_workspace(const gdr_scan_problem_t& p) {
+    return by_state_dim(p.state_dim, [&](auto spl) {
+        constexpr int SPL = decltype(spl)::value;
+        size_t sums;
+        return segment_slots(units_of(p), kMostWaves<SPL>, p.num_seqs) ? ends_bytes<SPL>(p, &sums) : (size_t)0;
+    });
+}
 
 hipError_t launch_scan_fwd(const ScanArgs& a) {
     if (a.p.num_seqs == 0) return hipSuccess;

@@ -42,16 +42,24 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Workgroup -> (sequence, group, channel block): consecutive blocks of channels
-// on the same XCD (workgroups are dealt to the eight XCDs in turn), so that the
-// 32-byte pieces of a 128-byte line meet in one L2.
-__device__ __forceinline__ bool unit_of(int64_t units, int cbg, int groups, int* n, int* g, int* cb) {
+// Workgroup -> (sequence, segment, group, channel block): consecutive blocks of
+// channels on the same XCD (workgroups are dealt to the eight XCDs in turn), so
+// that the 32-byte pieces of a 128-byte line meet in one L2.
+__device__ __forceinline__ bool unit_of(int64_t units, int cbg, int groups, int nseg, int* n, int* seg, int* g, int* cb) {
     const int64_t per = (units + 7) / 8, u = (blockIdx.x % 8) * per + blockIdx.x / 8;
     if (u >= units || blockIdx.x / 8 >= per) return false;
     *cb = (int)(u % cbg);
-    *g = (int)(u / cbg % groups);
-    *n = (int)(u / ((int64_t)cbg * groups));
+    const int64_t v = u / cbg;
+    *g = (int)(v % groups);
+    *seg = (int)(v / groups % nseg);
+    *n = (int)(v / groups / nseg);
     return true;
+}
+
+// Slot of a sequence's first tile (or segment) of `tile` tokens: floor(s / tile) + n
+// leaves room for the partial ones of the sequences before it.
+__device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) {
+    return (int64_t)((uint32_t)s / (uint32_t)tile) + n;
 }
 
 // Rows of a token tensor from token t on, `rows` of them: a buffer whose accesses
@@ -154,7 +162,193 @@ __device__ __forceinline__ void join_pieces(const float* pub, int stride, int of
     }
 }
 
+// Sequences cut into segments of `len` tokens that run side by side (most == 1:
+// not cut). A segment's end from a zero state and the sum of its deltas give the
+// state behind it, P h + end with P = exp(A sum), so that a first pass over the
+// segments lets a second one start each from its true state.
+struct Segments {
+    int len, most;             // tokens a segment; segments of the longest sequence
+    float* end;                // [Ttot / len + N][D][4 SPL]
+    float* sum;                // [Ttot / len + N][D]
+    // the tokens of segment `seg`; false: the sequence has no such segment (the first one always is)
+    __device__ __forceinline__ bool range(int seg, int64_t* s, int64_t* e, bool* last) const {
+        *last = true;
+        if (most == 1) return true;
+        const int64_t b = *s + (int64_t)seg * len;
+        if (seg > 0 && b >= *e) return false;
+        *last = b + len >= *e;
+        *s = b;
+        *e = *last ? *e : b + len;
+        return true;
+    }
+    // h: the initial state -> the state before segment `seg` of the sequence that starts at token s
+    template <int SPL>
+    __device__ __forceinline__ void enter(int n, int seg, int64_t s, int D, int ch, int q, const float (&A2)[SPL],
+                                          float (&h)[SPL]) const {
+        if (most == 1) return;
+        const int64_t slot = first_slot(s, len, n);
+#pragma unroll 4
+        for (int i = 0; i < seg; ++i) through<SPL>(slot + i, D, ch, q, A2, h);
+    }
+    // h <- P h + end of one segment
+    template <int SPL>
+    __device__ __forceinline__ void through(int64_t slot, int D, int ch, int q, const float (&A2)[SPL],
+                                            float (&h)[SPL]) const {
+        float x[SPL];
+        read_vec(end + (slot * D + ch) * 4 * SPL + q * SPL, x);
+        const float d = sum[slot * D + ch];
+#pragma unroll
+        for (int k = 0; k < SPL; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[k] * d), h[k], x[k]);
+    }
+    // Stores a segment's end, which wavefront `holder` has in h, and the sum over the wavefronts of `total`.
+    template <int SPL>
+    __device__ __forceinline__ void leave(int n, int seg, int64_t s, int D, int ch, int q, bool act, int wave, int nw,
+                                          int holder, const float (&h)[SPL], float total, float* lds) const {
+        const int lane = threadIdx.x & 63;
+        const int64_t slot = first_slot(s, len, n) + seg;
+        lds_barrier();
+        lds[wave * 64 + lane] = total;
+        lds_barrier();
+        if (wave != holder || !act) return;
+        float v = 0.f;
+        for (int w = 0; w < nw; ++w) v += lds[w * 64 + lane];
+        write_vec(end + (slot * D + ch) * 4 * SPL + q * SPL, h);
+        if (q == 0) sum[slot * D + ch] = v;
+    }
+};
+
+// The recurrence without outputs. ENDS: over every segment but a sequence's last,
+// from a zero state, for `sg`'s ends; else from the initial state (joined from the
+// ends), storing the state before every tile of btile tokens.
+template <typename T, int SPL, bool SOFT, bool ENDS>
+__global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, Segments sg, float* states, int64_t units, int cbg,
+                                                     int btile) {
+    constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    int n, seg, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
+    const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
+    const int c = lane & 15, q = lane >> 4;
+    const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
+    const bool act = cb * kCh + c < Dg;
+    const int ch = g * Dg + (act ? cb * kCh + c : Dg - 1);
+    float* sd = lds + wave * (L * kCh * 2 + L * SP);
+    float* sB = sd + L * kCh * 2;
+    float* pub = lds + nw * (L * kCh * 2 + L * SP);         // [2][nw][2][64][SPL]
+    float* carry = pub + 2 * nw * 128 * SPL;                // [2][64][SPL]
+    int64_t s, e;
+    seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    const int64_t seq = s;
+    bool last;
+    if (!sg.range(seg, &s, &e, &last) || (ENDS && last)) return;
+    float A2[SPL], h0[SPL], total = 0.f;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+        const bool in = act && q * SPL + i < S;
+        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        h0[i] = !ENDS && in && a.S0 ? a.S0[((int64_t)n * a.p.channels + ch) * S + q * SPL + i] : 0.f;
+    }
+    if (!ENDS) sg.template enter<SPL>(n, seg, seq, a.p.channels, ch, q, A2, h0);
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
+    const int row = wave * L, tile = nw * L;
+    int ox[K], odt[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t r = row + 4 * k + q;
+        ox[k] = act ? (int)((r * a.p.x_stride + ch) * (int)sizeof(T)) : kNowhere;
+        odt[k] = act ? (int)((r * a.p.dt_stride + ch) * (int)sizeof(T)) : kNowhere;
+    }
+    T rx[K], rdt[K];
+    StateRows<T, SPL, L> rB;
+    rB.init(a.p.b_stride, g * S, S, row);
+    auto fetch = [&](int64_t tb) {
+        const int64_t rows = e - tb < tile ? (e - tb > 0 ? e - tb : 0) : tile;
+        const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            rx[k] = buf_load<T>(bx, ox[k]);
+            rdt[k] = buf_load<T>(bdt, odt[k]);
+        }
+        rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
+    };
+    fetch(s);
+    const int64_t slot = first_slot(seq, btile, n);
+    int buf = 0;
+    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1) {
+        const int left = (int)(e - tb < tile ? e - tb : tile);
+        wave_lds_fence();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float x = to_f(rx[k]);
+            float d = to_f(rdt[k]) + bias;
+            if (SOFT) d = softplus(d);
+            d = row + 4 * k + q < left ? d : 0.f;
+            *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x};
+        }
+        rB.put(sB);
+        wave_lds_fence();
+        fetch(tb + tile);
+        float P[SPL], hl[SPL], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) hl[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
+            float Bv[SPL];
+            read_vec(sB + j * SP + q * SPL, Bv);
+            sum += d[0];
+#pragma unroll
+            for (int i = 0; i < SPL; ++i)
+                hl[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * d[0]), hl[i], d[1] * Bv[i]);
+        }
+        total += sum;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
+        float* all = pub + buf * nw * 128 * SPL + lane * SPL;
+        write_vec(all + wave * 128 * SPL, P);
+        write_vec(all + wave * 128 * SPL + 64 * SPL, hl);
+        lds_barrier();
+        if (tb != s) read_vec(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
+        join_pieces<SPL, true>(all, 128 * SPL, 64 * SPL, 0, wave, h0);
+        loads_arrived();
+        // a backward tile starts with this piece (pieces are whole parts of a tile, or the tile is all there is)
+        const int at = (int)(tb - seq) + row;
+        if (!ENDS && at % btile == 0 && row < left && act)
+            write_vec(states + ((slot + at / btile) * a.p.channels + ch) * SP + q * SPL, h0);
+        if (wave == nw - 1) {
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(P[i], h0[i], hl[i]);
+            write_vec(carry + buf * 64 * SPL + lane * SPL, h0);
+        }
+    }
+    if (ENDS) sg.template leave<SPL>(n, seg, seq, a.p.channels, ch, q, act, wave, nw, nw - 1, h0, total, lds);
+}
+
 // ---------------------------------------------------------------- host
+// Segments where whole sequences leave more than half of 2048 wavefronts idle: as
+// many as fill them, of 256 tokens or more; three at least, for the work of the
+// recurrence is done twice.
+constexpr int kMostSegments = 64;
+inline int most_segments(int64_t units, int nw) {
+    const int64_t want = units > 0 ? 2048 / (units * nw) : 0;
+    return (int)(want < 3 ? 1 : want > kMostSegments ? kMostSegments : want);
+}
+inline Segments segments_for(int64_t units, int nw, int64_t max_len) {
+    Segments sg{0, 1, nullptr, nullptr};
+    int64_t want = most_segments(units, nw);
+    want = want < max_len / 256 ? want : max_len / 256;
+    if (want < 3) return sg;
+    sg.len = (int)(((max_len + want - 1) / want + 127) / 128 * 128);   // whole tiles of every kernel
+    sg.most = (int)((max_len + sg.len - 1) / sg.len);
+    return sg;
+}
+// Slots that the segments of any sequences of these sizes need: at most `most` for
+// a sequence and one more left free, and the last sequence's wherever it starts.
+inline int64_t segment_slots(int64_t units, int nw, int64_t N) {
+    const int most = most_segments(units, nw);
+    return most < 3 ? 0 : N * (most + 1) + most;
+}
+
 // Wavefronts of a workgroup, a power of two: as many as make `fill` in all units
 // together, at least `least`, no more than pieces in the longest sequence or than `most`.
 inline int waves_for(int64_t units, int64_t max_len, int piece, int fill, int least, int most) {
@@ -163,16 +357,23 @@ inline int waves_for(int64_t units, int64_t max_len, int piece, int fill, int le
     return nw;
 }
 
+template <int SPL> constexpr size_t states_lds(int nw) {
+    return 4 * ((size_t)nw * (kPiece<SPL> * (kCh * 2 + 4 * SPL) + 2 * 128 * SPL) + 2 * 64 * SPL);
+}
+
+// f(states a lane)
+template <typename F>
+auto by_state_dim(int S, F f) {
+    if (S <= 8) return f(std::integral_constant<int, 2>{});
+    if (S <= 16) return f(std::integral_constant<int, 4>{});
+    if (S <= 32) return f(std::integral_constant<int, 8>{});
+    return f(std::integral_constant<int, 16>{});
+}
 template <typename F>
 hipError_t by_states(const ScanArgs& a, F f) {
-    auto pick = [&](auto type) {
-        const int S = a.p.state_dim;
-        if (S <= 8) return f(type, std::integral_constant<int, 2>{});
-        if (S <= 16) return f(type, std::integral_constant<int, 4>{});
-        if (S <= 32) return f(type, std::integral_constant<int, 8>{});
-        return f(type, std::integral_constant<int, 16>{});
-    };
-    return a.p.io_dtype == GDR_BF16 ? pick(bf16{}) : pick(float{});
+    return by_state_dim(a.p.state_dim, [&](auto spl) {
+        return a.p.io_dtype == GDR_BF16 ? f(bf16{}, spl) : f(float{}, spl);
+    });
 }
 
 }  // namespace gdr

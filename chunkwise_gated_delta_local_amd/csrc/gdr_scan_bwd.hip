@@ -44,8 +44,8 @@ template <int SPL> struct Bwd {
 struct ScanBwdWs {
     float* states;             // [Ttot / tile + N][D][4 SPL] states before the tiles
     float* bc;                 // [channel blocks of a group][2][Ttot][groups][S]: dB, dC
-    float* dA;                 // [N][D][S]
-    float* dch;                // [N][2][D]: dD, ddt_bias
+    float* dA;                 // [N][segments][D][S]
+    float* dch;                // [N][segments][2][D]: dD, ddt_bias
 };
 
 // own + x of another lane
@@ -71,114 +71,95 @@ __device__ __forceinline__ float states_sum4(const float (&v)[4], int q) {
     return add_dpp<0xb1>(odd ? a : b, odd ? b : a);
 }
 
-// Slot of a sequence's first tile: floor(s / tile) + n leaves room for the
-// partial tiles of the sequences before it.
-__device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) { return (int64_t)((uint32_t)s / (uint32_t)tile) + n; }
-
-template <typename T, int SPL, bool SOFT>
-__global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, float* states, int64_t units, int cbg, int btile) {
+// G at the start of every segment but a sequence's first from zero behind it, and
+// the sum of its deltas: the recurrence backwards, G <- exp(delta A) (ds C + G).
+template <typename T, int SPL, bool GATE, bool SOFT>
+__global__ __launch_bounds__(512) void k_scan_grad_ends(ScanArgs a, Segments sg, int64_t units, int cbg) {
     constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    int n, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    int n, seg, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
     const bool act = cb * kCh + c < Dg;
     const int ch = g * Dg + (act ? cb * kCh + c : Dg - 1);
     float* sd = lds + wave * (L * kCh * 2 + L * SP);
-    float* sB = sd + L * kCh * 2;
+    float* sC = sd + L * kCh * 2;
     float* pub = lds + nw * (L * kCh * 2 + L * SP);         // [2][nw][2][64][SPL]
     float* carry = pub + 2 * nw * 128 * SPL;                // [2][64][SPL]
     int64_t s, e;
     seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
-    float A2[SPL], h0[SPL];
+    const int64_t seq = s;
+    bool last;
+    if (!sg.range(seg, &s, &e, &last) || seg == 0) return;
+    float A2[SPL], G[SPL], total = 0.f;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
-        const bool in = act && q * SPL + i < S;
-        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
-        h0[i] = in && a.S0 ? a.S0[((int64_t)n * a.p.channels + ch) * S + q * SPL + i] : 0.f;
+        A2[i] = act && q * SPL + i < S ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        G[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
-    const int row = wave * L, tile = nw * L;
-    int ox[K], odt[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int64_t r = row + 4 * k + q;
-        ox[k] = act ? (int)((r * a.p.x_stride + ch) * (int)sizeof(T)) : kNowhere;
-        odt[k] = act ? (int)((r * a.p.dt_stride + ch) * (int)sizeof(T)) : kNowhere;
-    }
-    T rx[K], rdt[K];
-    StateRows<T, SPL, L> rB;
-    rB.init(a.p.b_stride, g * S, S, row);
-    auto fetch = [&](int64_t tb) {
-        const int64_t rows = e - tb < tile ? (e - tb > 0 ? e - tb : 0) : tile;
-        const auto bx = token_rows<T>(a.x, tb, a.p.x_stride, rows), bdt = token_rows<T>(a.dt, tb, a.p.dt_stride, rows);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            rx[k] = buf_load<T>(bx, ox[k]);
-            rdt[k] = buf_load<T>(bdt, odt[k]);
-        }
-        rB.load(token_rows<T>(a.B, tb, a.p.b_stride, rows));
-    };
-    fetch(s);
-    const int64_t slot = first_slot(s, btile, n);
+    const int dy32 = a.p.dy_dtype == GDR_F32, row = wave * L, tile = nw * L;
+    const int ntiles = (int)((uint32_t)(e - s + tile - 1) / (uint32_t)tile);
+    StateRows<T, SPL, L> rC;
+    rC.init(a.p.c_stride, g * S, S, row);
     int buf = 0;
-    for (int64_t tb = s; tb < e; tb += tile, buf ^= 1) {
+    for (int it = ntiles - 1; it >= 0; --it, buf ^= 1) {
+        const int64_t tb = s + (int64_t)it * tile;
         const int left = (int)(e - tb < tile ? e - tb : tile);
+        rC.load(token_rows<T>(a.C, tb, a.p.c_stride, left));
         wave_lds_fence();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const float x = to_f(rx[k]);
-            float d = to_f(rdt[k]) + bias;
-            if (SOFT) d = softplus(d);
-            d = row + 4 * k + q < left ? d : 0.f;
-            *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, d * x};
+            const int64_t t = tb + row + 4 * k + q;
+            float d = 0.f, ds = 0.f;
+            if (act && row + 4 * k + q < left) {
+                d = to_f(((const T*)a.dt)[t * a.p.dt_stride + ch]) + bias;
+                if (SOFT) d = softplus(d);
+                ds = load_as<T>(a.d_y, t * a.p.channels + ch, dy32);
+                if (GATE) ds *= silu(to_f(((const T*)a.z)[t * a.p.z_stride + ch]));
+            }
+            *reinterpret_cast<f32x2*>(sd + ((4 * k + q) * kCh + c) * 2) = f32x2{d, ds};
         }
-        rB.put(sB);
+        rC.put(sC);
         wave_lds_fence();
-        fetch(tb + tile);
-        float P[SPL], hl[SPL], sum = 0.f;
+        float P[SPL], Gl[SPL], sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < SPL; ++i) hl[i] = 0.f;
+        for (int i = 0; i < SPL; ++i) Gl[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
+        for (int j = L - 1; j >= 0; --j) {
             const f32x2 d = *reinterpret_cast<const f32x2*>(sd + (j * kCh + c) * 2);
-            float Bv[SPL];
-            read_vec(sB + j * SP + q * SPL, Bv);
+            float Cv[SPL];
+            read_vec(sC + j * SP + q * SPL, Cv);
             sum += d[0];
 #pragma unroll
             for (int i = 0; i < SPL; ++i)
-                hl[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[i] * d[0]), hl[i], d[1] * Bv[i]);
+                Gl[i] = __builtin_amdgcn_exp2f(A2[i] * d[0]) * __builtin_fmaf(d[1], Cv[i], Gl[i]);
         }
+        total += sum;
 #pragma unroll
         for (int i = 0; i < SPL; ++i) P[i] = __builtin_amdgcn_exp2f(A2[i] * sum);
         float* all = pub + buf * nw * 128 * SPL + lane * SPL;
         write_vec(all + wave * 128 * SPL, P);
-        write_vec(all + wave * 128 * SPL + 64 * SPL, hl);
+        write_vec(all + wave * 128 * SPL + 64 * SPL, Gl);
         lds_barrier();
-        if (tb != s) read_vec(carry + (buf ^ 1) * 64 * SPL + lane * SPL, h0);
-        join_pieces<SPL, true>(all, 128 * SPL, 64 * SPL, 0, wave, h0);
-        loads_arrived();
-        // a backward tile starts with this piece (pieces are whole parts of a tile, or the tile is all there is)
-        const int at = (int)(tb - s) + row;
-        if (at % btile == 0 && row < left && act)
-            write_vec(states + ((slot + at / btile) * a.p.channels + ch) * SP + q * SPL, h0);
-        if (wave == nw - 1) {
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) h0[i] = __builtin_fmaf(P[i], h0[i], hl[i]);
-            write_vec(carry + buf * 64 * SPL + lane * SPL, h0);
+        if (wave == 0) {
+            if (it != ntiles - 1) read_vec(carry + (buf ^ 1) * 64 * SPL + lane * SPL, G);
+            join_pieces<SPL, false>(all, 128 * SPL, 64 * SPL, 0, nw, G);
+            write_vec(carry + buf * 64 * SPL + lane * SPL, G);
         }
     }
+    sg.template leave<SPL>(n, seg, seq, a.p.channels, ch, q, act, wave, nw, 0, G, total, lds);
 }
 
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, int64_t units, int cbg) {
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, Segments sg, int64_t units, int cbg) {
     typedef Bwd<SPL> V;
     constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, TOK = V::TOK, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    int n, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, &n, &g, &cb)) return;
+    int n, seg, g, cb;
+    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane >> 2, q = lane & 3, l4 = c & 3;
     const int D = a.p.channels, Dg = D / a.p.groups, S = a.p.state_dim;
@@ -189,6 +170,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
     float* carry = pub + 2 * nw * V::kPubFloats;            // [2][64][EPT]
     int64_t s, e;
     seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    const int64_t seq = s;
+    int nseg = sg.most == 1 || e == s ? 1 : (int)((uint32_t)(e - s + sg.len - 1) / (uint32_t)sg.len);
+    nseg = nseg < sg.most ? nseg : sg.most;
+    bool last;
+    if (!sg.range(seg, &s, &e, &last)) e = s;               // no such segment: its sums are zero
 
     bool act[J];
     int ch[J];
@@ -210,13 +196,26 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
             G[j * SPL + i] = in && a.dST ? a.dST[st0[j] + i] : 0.f;
             dA[j * SPL + i] = 0.f;
         }
+        if (nseg > 1) {                                     // G behind this segment, from the later ones
+            float A2j[SPL], Gj[SPL];
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) {
+                A2j[i] = A2[j * SPL + i];
+                Gj[i] = G[j * SPL + i];
+            }
+            const int64_t slot = first_slot(seq, sg.len, n);
+#pragma unroll 4
+            for (int i = nseg - 1; i > seg; --i) sg.template through<SPL>(slot + i, D, ch[j], q, A2j, Gj);
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) G[j * SPL + i] = Gj[i];
+        }
     }
     const bool dy32 = a.p.dy_dtype == GDR_F32 && sizeof(T) == 2, g32 = a.p.grad_dtype == GDR_F32;
     const int dyb = a.p.dy_dtype == GDR_F32 ? 4 : 2, gb = g32 ? 4 : 2;
     const int row = wave * L, tile = nw * L;
     const int ntiles = (int)((uint32_t)(e - s + tile - 1) / (uint32_t)tile);
     float* part = ws.bc + (int64_t)cb * 2 * a.Ttot * a.p.groups * S;
-    const float* states = ws.states + first_slot(s, tile, n) * D * SP;
+    const float* states = ws.states + (first_slot(seq, tile, n) + (uint32_t)(s - seq) / (uint32_t)tile) * D * SP;
     // this lane's tokens in a tile are wave L + 4 k + q; the offsets of the first, and bytes between k and k + 1
     const int64_t r0 = row + q;
     int ox[J], odt[J], oz[J], ody[J], og[J];
@@ -460,7 +459,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
         }
         if (wave == 0) write_vec(carry + buf * 64 * EPT + lane * EPT, G);
     }
-    if (a.dS0 && wave == 0) {
+    if (a.dS0 && seg == 0 && wave == 0) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -487,9 +486,9 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
         const int j = i < EPT ? i / SPL : (i - EPT) % J;
         if (!act[j]) continue;
         if (i < EPT) {
-            if (q * SPL + i % SPL < S) ws.dA[st0[j] + i % SPL] = v;
+            if (q * SPL + i % SPL < S) ws.dA[st0[j] + i % SPL + ((int64_t)n * (sg.most - 1) + seg) * D * S] = v;
         } else if (q == 0) {
-            ws.dch[((int64_t)n * 2 + (i - EPT) / J) * D + ch[j]] = v;
+            ws.dch[(((int64_t)n * sg.most + seg) * 2 + (i - EPT) / J) * D + ch[j]] = v;
         }
     }
 }
@@ -523,22 +522,31 @@ struct ChannelOut {
 // sequence. With fewer than LEAST wavefronts no sequence is longer than a tile,
 // so that T / tile <= N; otherwise the tile has LEAST L tokens or more.
 struct BwdPlan {
-    size_t states, bc, dA, dch, end;
+    size_t states, bc, dA, dch, end, sum, gend, gsum, all;
 };
+template <int SPL> int64_t bwd_units(const gdr_scan_problem_t& p) {
+    return (int64_t)p.num_seqs * p.groups * ((p.channels / p.groups + Bwd<SPL>::CHB - 1) / Bwd<SPL>::CHB);
+}
 template <int SPL>
 BwdPlan plan(const gdr_scan_problem_t& p) {
     typedef Bwd<SPL> V;
     const size_t D = p.channels, S = p.state_dim, N = p.num_seqs, T = (size_t)(p.batch * p.seq_len);
     const size_t cbg = (D / p.groups + V::CHB - 1) / V::CHB;
+    const size_t slots = segment_slots(bwd_units<SPL>(p), V::NW, N);
+    const size_t nseg = slots ? most_segments(bwd_units<SPL>(p), V::NW) : 1;
     BwdPlan b;
     size_t off = 0;
     auto take = [&](size_t floats) { size_t o = off; off = (off + floats * 4 + 255) & ~(size_t)255; return o; };
     const size_t most = N < T ? N : T, tiles = T / (V::LEAST * V::L);
     b.states = take(((tiles > most ? tiles : most) + N) * D * V::SP);
     b.bc = take(cbg * 2 * T * p.groups * S);
-    b.dA = take(N * D * S);
-    b.dch = take(N * 2 * D);
-    b.end = off;
+    b.dA = take(N * nseg * D * S);
+    b.dch = take(N * nseg * 2 * D);
+    b.end = take(slots * D * V::SP);
+    b.sum = take(slots * D);
+    b.gend = take(slots * D * V::SP);
+    b.gsum = take(slots * D);
+    b.all = off;
     return b;
 }
 
@@ -550,20 +558,32 @@ hipError_t bwd(const ScanArgs& a) {
     auto f = [&](size_t off) { return reinterpret_cast<float*>(a.ws + off); };
     const ScanBwdWs ws = {f(pl.states), f(pl.bc), f(pl.dA), f(pl.dch)};
     const int Dg = a.p.channels / a.p.groups;
-    const int64_t NG = (int64_t)a.p.num_seqs * a.p.groups;
     const int cbs = (Dg + kCh - 1) / kCh, cbg = (Dg + V::CHB - 1) / V::CHB;
-    const int nw = waves_for(NG * cbg, a.max_len, V::L, 2048, V::LEAST, V::NW);
+    Segments sg = segments_for(bwd_units<SPL>(a.p), V::NW, a.max_len), gsg = sg;
+    sg.end = f(pl.end);
+    sg.sum = f(pl.sum);
+    gsg.end = f(pl.gend);
+    gsg.sum = f(pl.gsum);
+    const int64_t NG = (int64_t)a.p.num_seqs * a.p.groups * sg.most, longest = sg.most > 1 ? sg.len : a.max_len;
+    const int nw = waves_for(NG * cbg, longest, V::L, 2048, V::LEAST, V::NW);
+    const int nws = waves_for(NG * cbs, longest, kPiece<SPL>, 4096, 1, SPL == 16 ? 4 : 8);
     auto grid = [](int64_t units) { return dim3((unsigned)((units + 7) / 8 * 8)); };
     hipError_t e = hipSuccess;
-    if (!grid_fits(NG * cbs + 8, 64 * nw)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(NG * cbs + 8, 64 * (nw > nws ? nw : nws))) return hipErrorInvalidConfiguration;
     if (NG > 0) {
-        const int nws = waves_for(NG * cbs, a.max_len, kPiece<SPL>, 4096, 1, SPL == 16 ? 4 : 8);
-        const size_t lds = 4 * ((size_t)nws * (kPiece<SPL> * (kCh * 2 + V::SP) + 2 * 128 * SPL) + 2 * 64 * SPL);
+        const size_t lds = states_lds<SPL>(nws);
+        const dim3 sgrid = grid(NG * cbs);
         auto go = [&](auto gate, auto soft) {
             constexpr bool GATE = decltype(gate)::value, SOFT = decltype(soft)::value;
-            k_scan_states<T, SPL, SOFT><<<grid(NG * cbs), 64 * nws, lds, a.stream>>>(a, ws.states, NG * cbs, cbs, nw * V::L);
+            if (sg.most > 1) {
+                k_scan_states<T, SPL, SOFT, true><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, nullptr, NG * cbs, cbs, 1);
+                if ((e = hipGetLastError()) != hipSuccess) return;
+                k_scan_grad_ends<T, SPL, GATE, SOFT><<<sgrid, 64 * nws, lds, a.stream>>>(a, gsg, NG * cbs, cbs);
+                if ((e = hipGetLastError()) != hipSuccess) return;
+            }
+            k_scan_states<T, SPL, SOFT, false><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, ws.states, NG * cbs, cbs, nw * V::L);
             if ((e = hipGetLastError()) != hipSuccess) return;
-            k_scan_bwd<T, SPL, GATE, SOFT><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, NG * cbg, cbg);
+            k_scan_bwd<T, SPL, GATE, SOFT><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, gsg, NG * cbg, cbg);
         };
         auto by_gate = [&](auto soft) { a.z ? go(std::true_type{}, soft) : go(std::false_type{}, soft); };
         a.p.dt_softplus ? by_gate(std::true_type{}) : by_gate(std::false_type{});
@@ -571,25 +591,18 @@ hipError_t bwd(const ScanArgs& a) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t D = a.p.channels, S = a.p.state_dim, half = a.Ttot * a.p.groups * S;
+    const int64_t parts = (int64_t)a.p.num_seqs * sg.most;
     e = sum_partials(ws.bc, cbg, 2 * half, StateGradOut<T>{a.dB, a.dC, half, a.p.grad_dtype == GDR_F32}, a.stream);
-    if (e == hipSuccess) e = sum_partials(ws.dA, a.p.num_seqs, D * S, PlainOut{a.dA}, a.stream);
+    if (e == hipSuccess) e = sum_partials(ws.dA, parts, D * S, PlainOut{a.dA}, a.stream);
     if (e == hipSuccess && (a.dD || a.ddt_bias))
-        e = sum_partials(ws.dch, a.p.num_seqs, 2 * D, ChannelOut{a.dD, a.ddt_bias, D}, a.stream);
+        e = sum_partials(ws.dch, parts, 2 * D, ChannelOut{a.dD, a.ddt_bias, D}, a.stream);
     return e;
 }
 
 }  // namespace
 
 size_t scan_bwd_workspace(const gdr_scan_problem_t& p) {
-    const int S = p.state_dim;
-    auto need = [&](auto spl) {
-        constexpr int SPL = decltype(spl)::value;
-        return plan<SPL>(p).end;
-    };
-    if (S <= 8) return need(std::integral_constant<int, 2>{});
-    if (S <= 16) return need(std::integral_constant<int, 4>{});
-    if (S <= 32) return need(std::integral_constant<int, 8>{});
-    return need(std::integral_constant<int, 16>{});
+    return by_state_dim(p.state_dim, [&](auto spl) { return plan<decltype(spl)::value>(p).all; });
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a) {

@@ -147,6 +147,12 @@ SCAN = {
     "bare": dict(dtype="f32", lens=[50, 20], D=16, S=16, state=False, gate=False, skip=False, bias=False, soft=False),
     "no_gate": dict(dtype="bf16", lens=[50, 20], D=32, S=8, gate=False),
     "one_token": dict(dtype="f32", lens=[1], D=1, S=3),
+    # few channels and long sequences: cut into segments that run side by side
+    "segments": dict(dtype="f32", lens=[1500, 0, 300, 900], D=24, S=16),
+    "segments_groups": dict(dtype="bf16", lens=[1100, 1100], D=20, S=24, G=2, batch=True),
+    "segments_state_64": dict(dtype="bf16", lens=[2000], D=6, S=40, gate=False),
+    "segments_bare": dict(dtype="f32", lens=[770, 769], D=3, S=5, state=False, gate=False, skip=False, bias=False,
+                          soft=False),
     "many_short": dict(dtype="bf16", lens=[2, 1, 3, 0, 5, 1, 1, 2, 7, 4], D=50, S=16, G=2),
 }
 
