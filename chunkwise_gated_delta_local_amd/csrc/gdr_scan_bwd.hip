@@ -44,8 +44,7 @@ template <int SPL> struct Bwd {
 struct ScanBwdWs {
     float* states;             // [Ttot / tile + N][D][4 SPL] states before the tiles
     float* bc;                 // [channel blocks of a group][2][Ttot][groups][S]: dB, dC
-    float* dA;                 // [N][segments][D][S]
-    float* dch;                // [N][segments][2][D]: dD, ddt_bias
+    float* par;                // [N][segments]: dA [D][S], dD [D], ddt_bias [D]
 };
 
 // own + x of another lane
@@ -152,6 +151,18 @@ __global__ __launch_bounds__(512) void k_scan_grad_ends(ScanArgs a, Segments sg,
     }
     sg.template leave<SPL>(n, seg, seq, a.p.channels, ch, q, act, wave, nw, 0, G, total, lds);
 }
+
+// What a token brings to a lane: (delta, delta x, ds, -) of its channels, B and C of its states.
+template <int SPL, int J> struct Operands {
+    f32x4 d[J];
+    float B[SPL], C[SPL];
+    __device__ __forceinline__ void read(const float* pd, const float* pB, const float* pC) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) d[j] = *reinterpret_cast<const f32x4*>(pd + j * kCh * 4);
+        read_vec(pB, B);
+        read_vec(pC, C);
+    }
+};
 
 template <typename T, int SPL, bool GATE, bool SOFT>
 __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, Segments sg, int64_t units, int cbg) {
@@ -316,6 +327,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
         wave_lds_fence();
         fetch(it - 1);
 
+        // a piece's operands are read from LDS together, ahead of their use
+        Operands<SPL, J> op[L];
+#pragma unroll
+        for (int m = 0; m < L; ++m) op[m].read(sd + m * TOK + c * 4, sB + m * SP + q * SPL, sC + m * SP + q * SPL);
+
         // the piece from a zero state, and its G from zero behind it
         float P[EPT], hl[EPT], Gl[EPT], sum[J];
 #pragma unroll
@@ -323,35 +339,26 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
 #pragma unroll
         for (int j = 0; j < J; ++j) sum[j] = 0.f;
 #pragma unroll
-        for (int m = 0; m < L; ++m) {
-            float Bv[SPL];
-            read_vec(sB + m * SP + q * SPL, Bv);
+        for (int m = 0; m < L; ++m)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const f32x4 d = *reinterpret_cast<const f32x4*>(sd + m * TOK + (c + kCh * j) * 4);
-                sum[j] += d[0];
+                sum[j] += op[m].d[j][0];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
                     const int o = j * SPL + i;
-                    ea[m][o] = __builtin_amdgcn_exp2f(A2[o] * d[0]);
-                    hl[o] = __builtin_fmaf(ea[m][o], hl[o], d[1] * Bv[i]);
+                    ea[m][o] = __builtin_amdgcn_exp2f(A2[o] * op[m].d[j][0]);
+                    hl[o] = __builtin_fmaf(ea[m][o], hl[o], op[m].d[j][1] * op[m].B[i]);
                 }
             }
-        }
 #pragma unroll
-        for (int m = L - 1; m >= 0; --m) {
-            float Cv[SPL];
-            read_vec(sC + m * SP + q * SPL, Cv);
+        for (int m = L - 1; m >= 0; --m)
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const float ds = sd[m * TOK + (c + kCh * j) * 4 + 2];
+            for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
                     const int o = j * SPL + i;
-                    Gl[o] = ea[m][o] * __builtin_fmaf(ds, Cv[i], Gl[o]);
+                    Gl[o] = ea[m][o] * __builtin_fmaf(op[m].d[j][2], op[m].C[i], Gl[o]);
                 }
-            }
-        }
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -365,22 +372,30 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
         join_pieces<EPT, true>(all, V::kPubFloats, 64 * EPT, 0, wave, h[0]);
         join_pieces<EPT, false>(all, V::kPubFloats, 128 * EPT, wave + 1, nw, G);
         loads_arrived();
+        {
+            float Bv[L][SPL], dx[L][J];
 #pragma unroll
-        for (int m = 0; m < L; ++m) {
-            float Bv[SPL];
-            read_vec(sB + m * SP + q * SPL, Bv);
+            for (int m = 0; m < L; ++m) {
+                read_vec(sB + m * SP + q * SPL, Bv[m]);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const float dx = sd[m * TOK + (c + kCh * j) * 4 + 1];
-#pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    const int o = j * SPL + i;
-                    h[m + 1][o] = __builtin_fmaf(ea[m][o], h[m][o], dx * Bv[i]);
-                }
+                for (int j = 0; j < J; ++j) dx[m][j] = sd[m * TOK + (c + kCh * j) * 4 + 1];
             }
+#pragma unroll
+            for (int m = 0; m < L; ++m)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < SPL; ++i) {
+                        const int o = j * SPL + i;
+                        h[m + 1][o] = __builtin_fmaf(ea[m][o], h[m][o], dx[m][j] * Bv[m][i]);
+                    }
         }
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
+            Operands<SPL, J> o4[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                o4[m].read(sd + (4 * k + m) * TOK + c * 4, sB + (4 * k + m) * SP + q * SPL, sC + (4 * k + m) * SP + q * SPL);
             float gB[J][4], gA[J][4], yC[J][4];
             float u[H2];
 #pragma unroll
@@ -388,24 +403,21 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
 #pragma unroll
             for (int m4 = 3; m4 >= 0; --m4) {
                 const int m = 4 * k + m4;
-                float Bv[SPL], Cv[SPL], dBv[SPL], dCv[SPL];
-                read_vec(sB + m * SP + q * SPL, Bv);
-                read_vec(sC + m * SP + q * SPL, Cv);
+                float dBv[SPL], dCv[SPL];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const f32x4 d = *reinterpret_cast<const f32x4*>(sd + m * TOK + (c + kCh * j) * 4);
                     float tB = 0.f, tA = 0.f, tC = 0.f;
 #pragma unroll
                     for (int i = 0; i < SPL; ++i) {
                         const int o = j * SPL + i;
-                        const float gr = __builtin_fmaf(d[2], Cv[i], G[o]);
+                        const float gr = __builtin_fmaf(o4[m4].d[j][2], o4[m4].C[i], G[o]);
                         const float gp = gr * (ea[m][o] * h[m][o]);
-                        tB = __builtin_fmaf(gr, Bv[i], tB);
+                        tB = __builtin_fmaf(gr, o4[m4].B[i], tB);
                         tA = __builtin_fmaf(gp, A2[o], tA);
-                        if (GATE) tC = __builtin_fmaf(Cv[i], h[m + 1][o], tC);
-                        dA[o] = __builtin_fmaf(gp, d[0], dA[o]);
-                        dBv[i] = j ? __builtin_fmaf(gr, d[1], dBv[i]) : gr * d[1];
-                        dCv[i] = j ? __builtin_fmaf(d[2], h[m + 1][o], dCv[i]) : d[2] * h[m + 1][o];
+                        if (GATE) tC = __builtin_fmaf(o4[m4].C[i], h[m + 1][o], tC);
+                        dA[o] = __builtin_fmaf(gp, o4[m4].d[j][0], dA[o]);
+                        dBv[i] = j ? __builtin_fmaf(gr, o4[m4].d[j][1], dBv[i]) : gr * o4[m4].d[j][1];
+                        dCv[i] = j ? __builtin_fmaf(o4[m4].d[j][2], h[m + 1][o], dCv[i]) : o4[m4].d[j][2] * h[m + 1][o];
                         G[o] = ea[m][o] * gr;
                     }
                     gB[j][m4] = tB;
@@ -479,6 +491,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
     }
     lds_barrier();
     if (wave != 0) return;
+    float* par = ws.par + ((int64_t)n * sg.most + seg) * D * (S + 2);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         float v = 0.f;
@@ -486,9 +499,9 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
         const int j = i < EPT ? i / SPL : (i - EPT) % J;
         if (!act[j]) continue;
         if (i < EPT) {
-            if (q * SPL + i % SPL < S) ws.dA[st0[j] + i % SPL + ((int64_t)n * (sg.most - 1) + seg) * D * S] = v;
+            if (q * SPL + i % SPL < S) par[(int64_t)ch[j] * S + q * SPL + i % SPL] = v;
         } else if (q == 0) {
-            ws.dch[(((int64_t)n * sg.most + seg) * 2 + (i - EPT) / J) * D + ch[j]] = v;
+            par[(int64_t)D * S + (int64_t)((i - EPT) / J) * D + ch[j]] = v;
         }
     }
 }
@@ -502,18 +515,15 @@ template <typename T> struct StateGradOut {                 // dB, dC in grad_dt
         else store_as<T>(dC, i - half, v, f32);
     }
 };
-struct PlainOut {
-    float* p;
-    __device__ void operator()(int64_t i, float v) const { p[i] = v; }
-};
-struct ChannelOut {
-    float *dD, *ddt_bias;
-    int64_t D;
+struct ParameterOut {                                       // dA [D][S], then dD [D], ddt_bias [D]
+    float *dA, *dD, *ddt_bias;
+    int64_t DS, D;
     __device__ void operator()(int64_t i, float v) const {
-        if (i < D) {
-            if (dD) dD[i] = v;
+        if (i < DS) dA[i] = v;
+        else if (i < DS + D) {
+            if (dD) dD[i - DS] = v;
         } else if (ddt_bias) {
-            ddt_bias[i - D] = v;
+            ddt_bias[i - DS - D] = v;
         }
     }
 };
@@ -522,7 +532,7 @@ struct ChannelOut {
 // sequence. With fewer than LEAST wavefronts no sequence is longer than a tile,
 // so that T / tile <= N; otherwise the tile has LEAST L tokens or more.
 struct BwdPlan {
-    size_t states, bc, dA, dch, end, sum, gend, gsum, all;
+    size_t states, bc, par, end, sum, gend, gsum, all;
 };
 template <int SPL> int64_t bwd_units(const gdr_scan_problem_t& p) {
     return (int64_t)p.num_seqs * p.groups * ((p.channels / p.groups + Bwd<SPL>::CHB - 1) / Bwd<SPL>::CHB);
@@ -540,8 +550,7 @@ BwdPlan plan(const gdr_scan_problem_t& p) {
     const size_t most = N < T ? N : T, tiles = T / (V::LEAST * V::L);
     b.states = take(((tiles > most ? tiles : most) + N) * D * V::SP);
     b.bc = take(cbg * 2 * T * p.groups * S);
-    b.dA = take(N * nseg * D * S);
-    b.dch = take(N * nseg * 2 * D);
+    b.par = take(N * nseg * D * (S + 2));
     b.end = take(slots * D * V::SP);
     b.sum = take(slots * D);
     b.gend = take(slots * D * V::SP);
@@ -556,7 +565,7 @@ hipError_t bwd(const ScanArgs& a) {
     static_assert(V::lds(V::NW) <= 160 * 1024, "LDS of a compute unit");
     const BwdPlan pl = plan<SPL>(a.p);
     auto f = [&](size_t off) { return reinterpret_cast<float*>(a.ws + off); };
-    const ScanBwdWs ws = {f(pl.states), f(pl.bc), f(pl.dA), f(pl.dch)};
+    const ScanBwdWs ws = {f(pl.states), f(pl.bc), f(pl.par)};
     const int Dg = a.p.channels / a.p.groups;
     const int cbs = (Dg + kCh - 1) / kCh, cbg = (Dg + V::CHB - 1) / V::CHB;
     Segments sg = segments_for(bwd_units<SPL>(a.p), V::NW, a.max_len), gsg = sg;
@@ -593,9 +602,7 @@ hipError_t bwd(const ScanArgs& a) {
     const int64_t D = a.p.channels, S = a.p.state_dim, half = a.Ttot * a.p.groups * S;
     const int64_t parts = (int64_t)a.p.num_seqs * sg.most;
     e = sum_partials(ws.bc, cbg, 2 * half, StateGradOut<T>{a.dB, a.dC, half, a.p.grad_dtype == GDR_F32}, a.stream);
-    if (e == hipSuccess) e = sum_partials(ws.dA, parts, D * S, PlainOut{a.dA}, a.stream);
-    if (e == hipSuccess && (a.dD || a.ddt_bias))
-        e = sum_partials(ws.dch, parts, 2 * D, ChannelOut{a.dD, a.ddt_bias, D}, a.stream);
+    if (e == hipSuccess) e = sum_partials(ws.par, parts, D * (S + 2), ParameterOut{a.dA, a.dD, a.ddt_bias, D * S, D}, a.stream);
     return e;
 }
 
