@@ -34,11 +34,11 @@ template <int SPL> constexpr size_t fwd_lds(int nw) {
 
 // OT: type of y; GATE: z is there; SOFT: softplus of dt
 template <typename T, typename OT, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, Segments sg, int64_t units, int cbg) {
+__global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, Segments sg, int64_t lines, int cbg) {
     constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, seg, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
+    if (!unit_of(a, lines, cbg, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
@@ -256,21 +256,22 @@ hipError_t fwd(const ScanArgs& a) {
     // 4096 wavefronts fill the card (four a SIMD as registers allow): 13 sequences of 4,099 tokens, 1,300 units: 132 us
     // (2048: 195, 8192: 164; one sequence of 8,192, 256 units, takes all 8 in any case)
     const int nw = waves_for(units, sg.most > 1 ? sg.len : a.max_len, kPiece<SPL>, 4096, 1, most);
-    if (!grid_fits(units + 8, 64 * nw)) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((units + 7) / 8 * 8));
+    const int64_t lines = line_units((int64_t)a.p.num_seqs * a.p.groups * sg.most, cbg), blocks = unit_blocks(lines);
+    if (!grid_fits(blocks, 64 * nw)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks);
     hipError_t e = hipSuccess;
     if (sg.most > 1) {
         size_t sums;
         ends_bytes<SPL>(a.p, &sums);
         sg.end = reinterpret_cast<float*>(a.ws);
         sg.sum = reinterpret_cast<float*>(a.ws + sums);
-        if (a.p.dt_softplus) k_scan_states<T, SPL, true, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, units, cbg, 1);
-        else k_scan_states<T, SPL, false, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, units, cbg, 1);
+        if (a.p.dt_softplus) k_scan_states<T, SPL, true, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, lines, cbg, 1);
+        else k_scan_states<T, SPL, false, true><<<grid, 64 * nw, states_lds<SPL>(nw), a.stream>>>(a, sg, nullptr, lines, cbg, 1);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     auto go = [&](auto out, auto gate, auto soft) {
         k_scan_fwd<T, decltype(out), SPL, decltype(gate)::value, decltype(soft)::value>
-            <<<grid, 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, sg, units, cbg);
+            <<<grid, 64 * nw, fwd_lds<SPL>(nw), a.stream>>>(a, sg, lines, cbg);
     };
     auto by_gate = [&](auto out, auto soft) { a.z ? go(out, std::true_type{}, soft) : go(out, std::false_type{}, soft); };
     auto by_out = [&](auto soft) { a.p.out_dtype == GDR_F32 ? by_gate(float{}, soft) : by_gate(T{}, soft); };

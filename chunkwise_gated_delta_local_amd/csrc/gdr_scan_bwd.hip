@@ -73,11 +73,11 @@ __device__ __forceinline__ float states_sum4(const float (&v)[4], int q) {
 // G at the start of every segment but a sequence's first from zero behind it, and
 // the sum of its deltas: the recurrence backwards, G <- exp(delta A) (ds C + G).
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(512) void k_scan_grad_ends(ScanArgs a, Segments sg, int64_t units, int cbg) {
+__global__ __launch_bounds__(512) void k_scan_grad_ends(ScanArgs a, Segments sg, int64_t lines, int cbg) {
     constexpr int L = kPiece<SPL>, K = L / 4, SP = 4 * SPL;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, seg, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
+    if (!unit_of(a, lines, cbg, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
     const int Dg = a.p.channels / a.p.groups, S = a.p.state_dim;
@@ -165,12 +165,12 @@ template <int SPL, int J> struct Operands {
 };
 
 template <typename T, int SPL, bool GATE, bool SOFT>
-__global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, Segments sg, int64_t units, int cbg) {
+__global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_bwd(ScanArgs a, ScanBwdWs ws, Segments sg, int64_t lines, int cbg) {
     typedef Bwd<SPL> V;
     constexpr int J = V::J, L = V::L, K = L / 4, SP = V::SP, EPT = V::EPT, CHB = V::CHB, TOK = V::TOK, H2 = SPL / 2;
     extern __shared__ __attribute__((aligned(16))) float lds[];
     int n, seg, g, cb;
-    if (!unit_of(units, cbg, a.p.groups, sg.most, &n, &seg, &g, &cb)) return;
+    if (!unit_of(a, lines, cbg, sg.most, &n, &seg, &g, &cb)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
     const int c = lane >> 2, q = lane & 3, l4 = c & 3;
     const int D = a.p.channels, Dg = D / a.p.groups, S = a.p.state_dim;
@@ -576,23 +576,23 @@ hipError_t bwd(const ScanArgs& a) {
     const int64_t NG = (int64_t)a.p.num_seqs * a.p.groups * sg.most, longest = sg.most > 1 ? sg.len : a.max_len;
     const int nw = waves_for(NG * cbg, longest, V::L, 2048, V::LEAST, V::NW);
     const int nws = waves_for(NG * cbs, longest, kPiece<SPL>, 4096, 1, SPL == 16 ? 4 : 8);
-    auto grid = [](int64_t units) { return dim3((unsigned)((units + 7) / 8 * 8)); };
+    const int64_t slines = line_units(NG, cbs), lines = line_units(NG, cbg);
     hipError_t e = hipSuccess;
-    if (!grid_fits(NG * cbs + 8, 64 * (nw > nws ? nw : nws))) return hipErrorInvalidConfiguration;
+    if (!grid_fits(unit_blocks(slines), 64 * (nw > nws ? nw : nws))) return hipErrorInvalidConfiguration;
     if (NG > 0) {
         const size_t lds = states_lds<SPL>(nws);
-        const dim3 sgrid = grid(NG * cbs);
+        const dim3 sgrid((unsigned)unit_blocks(slines)), bgrid((unsigned)unit_blocks(lines));
         auto go = [&](auto gate, auto soft) {
             constexpr bool GATE = decltype(gate)::value, SOFT = decltype(soft)::value;
             if (sg.most > 1) {
-                k_scan_states<T, SPL, SOFT, true><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, nullptr, NG * cbs, cbs, 1);
+                k_scan_states<T, SPL, SOFT, true><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, nullptr, slines, cbs, 1);
                 if ((e = hipGetLastError()) != hipSuccess) return;
-                k_scan_grad_ends<T, SPL, GATE, SOFT><<<sgrid, 64 * nws, lds, a.stream>>>(a, gsg, NG * cbs, cbs);
+                k_scan_grad_ends<T, SPL, GATE, SOFT><<<sgrid, 64 * nws, lds, a.stream>>>(a, gsg, slines, cbs);
                 if ((e = hipGetLastError()) != hipSuccess) return;
             }
-            k_scan_states<T, SPL, SOFT, false><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, ws.states, NG * cbs, cbs, nw * V::L);
+            k_scan_states<T, SPL, SOFT, false><<<sgrid, 64 * nws, lds, a.stream>>>(a, sg, ws.states, slines, cbs, nw * V::L);
             if ((e = hipGetLastError()) != hipSuccess) return;
-            k_scan_bwd<T, SPL, GATE, SOFT><<<grid(NG * cbg), 64 * nw, V::lds(nw), a.stream>>>(a, ws, gsg, NG * cbg, cbg);
+            k_scan_bwd<T, SPL, GATE, SOFT><<<bgrid, 64 * nw, V::lds(nw), a.stream>>>(a, ws, gsg, lines, cbg);
         };
         auto by_gate = [&](auto soft) { a.z ? go(std::true_type{}, soft) : go(std::false_type{}, soft); };
         a.p.dt_softplus ? by_gate(std::true_type{}) : by_gate(std::false_type{});
