@@ -253,9 +253,11 @@ hipError_t fwd(const ScanArgs& a) {
     const int64_t whole = units_of(a.p);
     Segments sg = segments_for(whole, most, a.max_len);
     const int64_t units = whole * sg.most;
-    // 4096 wavefronts fill the card (four a SIMD as registers allow): 13 sequences of 4,099 tokens, 1,300 units: 132 us
-    // (2048: 195, 8192: 164; one sequence of 8,192, 256 units, takes all 8 in any case)
-    const int nw = waves_for(units, sg.most > 1 ? sg.len : a.max_len, kPiece<SPL>, 4096, 1, most);
+    // 2048 wavefronts fill the card at two a SIMD (16 sequences of 512 tokens and 2,048 channels: 93 us, with twice as
+    // many 104); ragged sequences take 4096, for the longest one is a chain that the others do not shorten (13 of 4,099
+    // tokens, the longest 1,272, fp32: 90 us, with 2048 143).
+    const int fill = a.max_len * a.p.num_seqs > 2 * a.Ttot ? 4096 : 2048;
+    const int nw = waves_for(units, sg.most > 1 ? sg.len : a.max_len, kPiece<SPL>, fill, 1, most);
     const int64_t lines = line_units((int64_t)a.p.num_seqs * a.p.groups * sg.most, cbg), blocks = unit_blocks(lines);
     if (!grid_fits(blocks, 64 * nw)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks);
