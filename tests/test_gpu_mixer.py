@@ -140,6 +140,7 @@ SCAN = {
     "state_1": dict(dtype="f32", lens=[37, 5], D=17, S=1),
     "state_7_odd": dict(dtype="bf16", lens=[130, 3], D=35, S=7, G=5),
     "state_24": dict(dtype="f32", lens=[90, 1, 17], D=36, S=24, G=2),
+    "state_18_strided": dict(dtype="bf16", lens=[45, 45], D=34, S=18, G=2, batch=True, pad=6),
     "state_32": dict(dtype="bf16", lens=[140], D=33, S=32),
     "state_64": dict(dtype="f32", lens=[75, 2], D=18, S=64),
     "state_50": dict(dtype="bf16", lens=[41], D=16, S=50),
