@@ -14,7 +14,6 @@ void clear_error();
 struct ConvArgs {
     gdr_conv_problem_t p;
     int64_t Ttot;
-    bool wide;                 // addresses, strides and D allow 16-byte accesses
     const void *x, *weight, *bias, *S0;
     const int32_t* cu;
     void *y, *ST;
@@ -105,16 +104,26 @@ __device__ __forceinline__ void store_as(void* p, int64_t idx, float v, int f32)
     else reinterpret_cast<T*>(p)[idx] = to_t<T>(v);
 }
 
-// V consecutive elements; V = 16 bytes of T (one wide access) or 1
+// V consecutive elements, moved in one access; global memory takes 4, 8 and 16
+// bytes at the alignment of an element
 template <typename T, int V> struct Raw {
-    typedef T type __attribute__((ext_vector_type(V)));
+    typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
 template <typename T> struct Raw<T, 1> {
     typedef T type;
 };
-template <typename T, int V>
+// ONCE: past the caches, for data that they could not hold until its next use
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ typename Raw<T, V>::type load_raw(const T* p) {
-    return *reinterpret_cast<const typename Raw<T, V>::type*>(p);
+    auto* q = reinterpret_cast<const typename Raw<T, V>::type*>(p);
+    if constexpr (ONCE) return __builtin_nontemporal_load(q);
+    else return *q;
+}
+template <typename T, int V, bool ONCE = false>
+__device__ __forceinline__ void store_raw(T* p, typename Raw<T, V>::type r) {
+    auto* q = reinterpret_cast<typename Raw<T, V>::type*>(p);
+    if constexpr (ONCE) __builtin_nontemporal_store(r, q);
+    else *q = r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const typename Raw<T, V>::type& r, float (&f)[V]) {
@@ -125,7 +134,7 @@ __device__ __forceinline__ void unpack(const typename Raw<T, V>::type& r, float 
         for (int i = 0; i < V; ++i) f[i] = to_f(r[i]);
     }
 }
-template <typename T, int V>
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
     typename Raw<T, V>::type r;
     if constexpr (V == 1) {
@@ -134,7 +143,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) r[i] = to_t<T>(f[i]);
     }
-    *reinterpret_cast<typename Raw<T, V>::type*>(p) = r;
+    store_raw<T, V, ONCE>(p, r);
 }
 // V consecutive elements of a tensor that is fp32 or T; fp32 elements move 4 at a time
 template <typename T, int V>
@@ -200,6 +209,11 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int N, int64_t T_
     }
     return __builtin_amdgcn_readfirstlane(lo);
 }
+
+// Whether a call moves more bytes than the last cache holds (256 MB): its rows then
+// go past the caches where that was faster.
+inline bool beyond_caches(int64_t bytes) { return bytes > ((int64_t)256 << 20); }
+inline int64_t size_of(int32_t dtype) { return dtype == GDR_BF16 ? 2 : 4; }
 
 // Workgroups of a one-dimensional launch: HIP counts its threads in 32 bits.
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }

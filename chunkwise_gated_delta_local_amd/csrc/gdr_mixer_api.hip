@@ -9,7 +9,6 @@ using gdr::fail;
 bool is_dtype(int32_t t) { return t == GDR_F32 || t == GDR_BF16; }
 // a type that may be the io type or fp32
 bool io_or_f32(int32_t t, int32_t io) { return t == io || t == GDR_F32; }
-size_t size_of(int32_t dtype) { return dtype == GDR_BF16 ? 2 : 4; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 struct Ptr {
@@ -22,7 +21,7 @@ template <int N>
 gdr_status_t check_ptrs(const Ptr (&ptrs)[N], bool any) {
     for (const Ptr& t : ptrs) {
         if (t.required && any && !t.p) return fail(GDR_ERR_NULL, "%s is required", t.name);
-        if (!aligned(t.p, size_of(t.dtype)))
+        if (!aligned(t.p, (size_t)gdr::size_of(t.dtype)))
             return fail(GDR_ERR_SHAPE, "%s is not aligned to its element type", t.name);
     }
     return GDR_OK;
@@ -108,12 +107,6 @@ gdr_status_t check_conv(const gdr_conv_problem_t* p) {
     return check_stride("x_stride", p->x_stride, p->channels);
 }
 
-// 16 bytes of the io type divide the rows and their strides
-bool wide_rows(int32_t io_dtype, int64_t cols, int64_t stride) {
-    const int64_t v = io_dtype == GDR_BF16 ? 8 : 4;
-    return cols % v == 0 && stride % v == 0;
-}
-
 gdr::ConvArgs conv_args(const gdr_conv_problem_t* p, const void* x, const void* weight, const void* bias,
                         const void* S0, const int32_t* cu, void* stream) {
     gdr::ConvArgs a{};
@@ -121,8 +114,6 @@ gdr::ConvArgs conv_args(const gdr_conv_problem_t* p, const void* x, const void* 
     a.Ttot = p->batch * p->seq_len;
     a.x = x; a.weight = weight; a.bias = bias; a.S0 = S0; a.cu = cu;
     a.stream = static_cast<hipStream_t>(stream);
-    a.wide = wide_rows(p->io_dtype, p->channels, p->x_stride) && aligned(x, 16) && aligned(weight, 16) &&
-             aligned(bias, 16) && aligned(S0, 16);
     return a;
 }
 
@@ -201,7 +192,6 @@ gdr_status_t gdr_conv_fwd(const gdr_conv_problem_t* p, const void* x, const void
     gdr::ConvArgs a = conv_args(p, x, weight, bias, initial_state, cu_dev, stream);
     a.y = y;
     a.ST = final_state;
-    a.wide = a.wide && aligned(y, 16) && aligned(final_state, 16);
     return done(gdr::launch_conv_fwd(a));
 }
 
@@ -217,7 +207,6 @@ gdr_status_t gdr_conv_step(const gdr_conv_problem_t* p, const void* x, const voi
     gdr::ConvArgs a = conv_args(p, x, weight, bias, nullptr, nullptr, stream);
     a.y = y;
     a.ST = state;
-    a.wide = a.wide && aligned(state, 16) && aligned(y, 16);
     return done(gdr::launch_conv_step(a));
 }
 
@@ -248,7 +237,6 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* p, const void* x, const void
     a.d_y = d_y; a.dST = d_final_state; a.dx = dx; a.dS0 = d_initial_state;
     a.dweight = dweight; a.dbias = dbias;
     a.partial = static_cast<float*>(workspace);
-    a.wide = a.wide && aligned(d_y, 16) && aligned(d_final_state, 16) && aligned(dx, 16) && aligned(d_initial_state, 16);
     return done(gdr::launch_conv_bwd(a));
 }
 

@@ -18,25 +18,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int V> struct Piece {
-    typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-};
 // elements c .. c + V - 1 of a row of C, zero past its end
-template <typename T, int V>
-__device__ __forceinline__ typename Piece<T, V>::type load_piece(const T* row, int c, int C) {
-    typename Piece<T, V>::type r;
-    if (c + V <= C) return *reinterpret_cast<const typename Piece<T, V>::type*>(row + c);
+template <typename T, int V, bool ONCE = false>
+__device__ __forceinline__ typename Raw<T, V>::type load_piece(const T* row, int c, int C) {
+    typename Raw<T, V>::type r;
+    if (c + V <= C) return load_raw<T, V, ONCE>(row + c);
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = c + v < C ? row[c + v] : to_t<T>(0.f);
     return r;
 }
+// a parameter's elements, which are T or fp32; `none` where there is no parameter
 template <typename T, int V>
+__device__ __forceinline__ void load_param(const void* p, int c, int C, int f32, float none, float (&f)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = none;
+    if (!p || c >= C) return;
+    if (f32) unpack<float, V>(load_piece<float, V>((const float*)p, c, C), f);
+    else unpack<T, V>(load_piece<T, V>((const T*)p, c, C), f);
+}
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void store_piece(T* row, int c, int C, const float (&f)[V]) {
-    typename Piece<T, V>::type r;
+    typename Raw<T, V>::type r;
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = to_t<T>(f[v]);
     if (c + V <= C) {
-        *reinterpret_cast<typename Piece<T, V>::type*>(row + c) = r;
+        store_raw<T, V, ONCE>(row + c, r);
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -59,7 +65,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[4], int& slot) {
     return v;
 }
 
-template <typename T, typename OT, int V, int NV, int TPR>
+// ONCE: y goes past the caches
+template <typename T, typename OT, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
     __shared__ float red[2][4];
     int slot = 0;
@@ -69,14 +76,11 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + l) * V;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            w[i][v] = a.weight && c + v < C ? load_as<T>(a.weight, c + v, w32) : 1.f;
-            b[i][v] = a.bias && c + v < C ? load_as<T>(a.bias, c + v, w32) : 0.f;
-        }
+        load_param<T, V>(a.weight, c, C, w32, 1.f, w[i]);
+        load_param<T, V>(a.bias, c, C, w32, 0.f, b[i]);
     }
     const float inv = 1.f / (float)C;
-    typename Piece<T, V>::type raw[NV];
+    typename Raw<T, V>::type raw[NV];
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -118,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
             float y[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) y[v] = __builtin_fmaf(x[i][v] * rstd, w[i][v], b[i][v]);
-            store_piece<OT, V>((OT*)a.y + r * C, c, C, y);
+            store_piece<OT, V, ONCE>((OT*)a.y + r * C, c, C, y);
         }
         if (l == 0) {
             if (a.mean) a.mean[r] = mean;
@@ -130,8 +134,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
 // Backward: with xhat = (x - mean) rstd and c = d_y weight,
 //   dx = rstd (c - mean(c) - xhat mean(c xhat)).
 // Each thread also sums d_y xhat and d_y of its columns over its rows; the rows
-// of a workgroup are joined in LDS, the workgroups by k_sum_partials.
-template <typename T, typename DT, typename GT, int V, int NV, int TPR>
+// of a workgroup are joined in LDS, the workgroups by k_sum_partials. ONCE: x and
+// d_y are read past the caches.
+template <typename T, typename DT, typename GT, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_norm_bwd(NormArgs a) {
     constexpr int RPB = kThreads / TPR;
     __shared__ float red[2][2][4];
@@ -143,23 +148,21 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + l) * V;
+        load_param<T, V>(a.weight, c, C, w32, 1.f, w[i]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            w[i][v] = a.weight && c + v < C ? load_as<T>(a.weight, c + v, w32) : 1.f;
-            dw[i][v] = db[i][v] = 0.f;
-        }
+        for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
     }
     const float inv = 1.f / (float)C;
-    typename Piece<T, V>::type rx[NV];
-    typename Piece<DT, V>::type rdy[NV];
+    typename Raw<T, V>::type rx[NV];
+    typename Raw<DT, V>::type rdy[NV];
     float rmean = 0.f, rrstd = 0.f;
     auto fetch = [&](int64_t r) {
         if (r >= a.p.rows) return;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if ((i * TPR + l) * V < C) {
-                rx[i] = load_piece<T, V>((const T*)a.x + r * a.p.x_stride, (i * TPR + l) * V, C);
-                rdy[i] = load_piece<DT, V>((const DT*)a.d_y + r * C, (i * TPR + l) * V, C);
+                rx[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, (i * TPR + l) * V, C);
+                rdy[i] = load_piece<DT, V, ONCE>((const DT*)a.d_y + r * C, (i * TPR + l) * V, C);
             }
         rmean = a.mean[r];
         rrstd = a.rstd[r];
@@ -312,11 +315,17 @@ hipError_t launch_norm_fwd(const NormArgs& a) {
     return by_shape(a, [&](auto type, auto vec, auto nv, auto tpr) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-        // 2,097,152 rows of 128: 226 us, 4.8 TB/s with 8192 workgroups (2048: 234, 16384: 228)
-        const int64_t n = row_blocks(a.p.rows, TPR), most = 8192;
+        // four trips a workgroup: 2,097,152 rows of 128 take 203 us, 5.4 TB/s (with 16: 223, one: 249), 65,536 of 4,096
+        // 189 (eight: 198, one: 240)
+        const int64_t n = row_blocks(a.p.rows, TPR), most = n / 4 > 8192 ? n / 4 : 8192;
         const dim3 grid((unsigned)(n < most ? n : most));
-        if (a.p.out_dtype == GDR_F32) k_norm_fwd<T, float, V, NV, TPR><<<grid, kThreads, 0, a.stream>>>(a);
-        else k_norm_fwd<T, T, V, NV, TPR><<<grid, kThreads, 0, a.stream>>>(a);
+        // (65,536 x 4,096: 184 us against 189 with y past the caches, 2,097,152 x 128: 193 against 203; x too: 200, 202)
+        const bool once = beyond_caches(a.p.rows * a.p.cols * (size_of(a.p.io_dtype) + size_of(a.p.out_dtype)));
+        auto go = [&](auto otype, auto past) {
+            k_norm_fwd<T, decltype(otype), V, NV, TPR, decltype(past)::value><<<grid, kThreads, 0, a.stream>>>(a);
+        };
+        auto by_out = [&](auto past) { a.p.out_dtype == GDR_F32 ? go(float{}, past) : go(T{}, past); };
+        once ? by_out(std::true_type{}) : by_out(std::false_type{});
     });
 }
 
@@ -326,11 +335,16 @@ hipError_t launch_norm_bwd(const NormArgs& a) {
         hipError_t e = by_shape(a, [&](auto type, auto vec, auto nv, auto tpr) {
             typedef decltype(type) T;
             constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-            auto go = [&](auto dtype, auto gtype) {
-                k_norm_bwd<T, decltype(dtype), decltype(gtype), V, NV, TPR><<<dim3((unsigned)blocks), kThreads, 0, a.stream>>>(a);
+            // (16,384 x 4,096 bf16: 82 us against 87; dx past the caches too: 86)
+            const bool once = beyond_caches(
+                a.p.rows * a.p.cols * (size_of(a.p.io_dtype) + size_of(a.p.dy_dtype) + size_of(a.p.grad_dtype)));
+            auto go = [&](auto dtype, auto gtype, auto past) {
+                k_norm_bwd<T, decltype(dtype), decltype(gtype), V, NV, TPR, decltype(past)::value>
+                    <<<dim3((unsigned)blocks), kThreads, 0, a.stream>>>(a);
             };
-            auto by_dy = [&](auto gtype) { a.p.dy_dtype == GDR_F32 ? go(float{}, gtype) : go(T{}, gtype); };
-            a.p.grad_dtype == GDR_F32 ? by_dy(float{}) : by_dy(T{});
+            auto by_dy = [&](auto gtype, auto past) { a.p.dy_dtype == GDR_F32 ? go(float{}, gtype, past) : go(T{}, gtype, past); };
+            auto by_grad = [&](auto past) { a.p.grad_dtype == GDR_F32 ? by_dy(float{}, past) : by_dy(T{}, past); };
+            once ? by_grad(std::true_type{}) : by_grad(std::false_type{});
         });
         if (e != hipSuccess) return e;
     }

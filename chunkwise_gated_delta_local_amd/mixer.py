@@ -73,15 +73,19 @@ def _token_stride(t, name, width):
         if n > 1 and st != inner:
             raise ValueError("the elements of a token of %s must be contiguous" % name)
         inner *= n
-    ld = rows = 0
+    ld = rows = None
     for n, st in zip(reversed(sizes), reversed(strides)):
-        if n > 1 and ld and st != ld * rows:
+        if n == 1:
+            continue
+        if ld is None:
+            ld, rows = st, n
+        elif st == ld * rows:
+            rows *= n
+        else:
             raise ValueError("the tokens of %s must be evenly strided" % name)
-        if n > 1:
-            ld, rows = (ld, rows * n) if ld else (st, n)
-    if ld and ld < width:
+    if ld is not None and ld < width:           # an expanded tensor, for one
         raise ValueError("the tokens of %s must not overlap" % name)
-    return ld or width
+    return width if ld is None else ld
 
 
 def _seqs(B, cu_seqlens, cu_seqlens_cpu, dev):

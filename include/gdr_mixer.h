@@ -11,9 +11,7 @@
  * synchronised, argument errors are found on the host before anything is
  * enqueued, statuses and gdr_last_error_message are shared. Differences:
  *
- * - Base addresses need the alignment of their element type only; wide
- *   accesses are used where addresses, strides and sizes are multiples of 16
- *   bytes.
+ * - Base addresses need the alignment of their element type only.
  * - Input rows may be strided: x_stride (and the other *_stride fields) is the
  *   distance in elements between consecutive tokens (or rows), the elements of
  *   one token being contiguous. Token t of batch row b is row b * seq_len + t.
@@ -91,7 +89,8 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* problem, const void* x, cons
  *   A        [channels][state_dim], D, dt_bias [channels] or NULL: fp32
  *   state    [num_seqs][channels][state_dim] fp32
  * exp(delta A) is meant to be at most one; a growing state may overflow where
- * pieces of a sequence are joined although its running value does not.
+ * pieces of a sequence are joined although its running value does not, and an
+ * infinite one become NaN there.
  */
 typedef struct {
     int64_t batch, seq_len;
@@ -108,8 +107,9 @@ typedef struct {
     int32_t reserved;       /* 0                                                         */
 } gdr_scan_problem_t;
 
-/* initial_state NULL means zeros; final_state NULL is skipped. workspace: at
- * least gdr_scan_fwd_workspace_size bytes, which may be 0 (then NULL is taken). */
+/* initial_state NULL means zeros; final_state NULL is skipped (it may not
+ * overlap initial_state). workspace: at least gdr_scan_fwd_workspace_size bytes,
+ * which may be 0 (then NULL is taken). */
 gdr_status_t gdr_scan_fwd_workspace_size(const gdr_scan_problem_t* problem, size_t* bytes);
 gdr_status_t gdr_scan_fwd(const gdr_scan_problem_t* problem, const void* x, const void* dt, const float* A,
                           const void* B, const void* C, const float* D, const void* z, const float* dt_bias,

@@ -38,6 +38,8 @@ CONV = {
     "odd_f32_no_state": dict(dtype="f32", lens=[33, 64], D=65, W=2, state=False, bias=False),
     "batch_strided": dict(dtype="bf16", lens=[150, 150], D=264, W=4, batch=True, pad=24),
     "strided_odd": dict(dtype="bf16", lens=[70], D=64, W=3, pad=5, param="bf16"),
+    "seven_channels": dict(dtype="bf16", lens=[30, 0, 5], D=7, W=3, pad=2),
+    "odd_and_long": dict(dtype="bf16", lens=[300, 301], D=523, W=4),
     "no_activation": dict(dtype="f32", lens=[10, 129], D=64, W=4, act=False),
     "shorter_than_taps": dict(dtype="bf16", lens=[1, 2, 1, 1, 2, 0, 1], D=64, W=4),
     "one_token": dict(dtype="f32", lens=[1], D=1, W=4),
@@ -85,7 +87,8 @@ def test_conv_bwd(case, grad):
         assert got[name].dtype == (c["x"].dtype if grad == "io" and name in ("dx", "dh0") else torch.float32)
 
 
-@pytest.mark.parametrize("dtype,D,W,pad", [("bf16", 512, 4, 0), ("f32", 100, 3, 0), ("bf16", 33, 2, 0), ("bf16", 64, 4, 8)])
+@pytest.mark.parametrize("dtype,D,W,pad", [("bf16", 512, 4, 0), ("f32", 100, 3, 0), ("bf16", 33, 2, 0), ("bf16", 64, 4, 8),
+                                           ("f32", 530, 4, 3)])
 def test_conv_step_continues_a_prompt(dtype, D, W, pad):
     """A prompt, then single tokens from its final state: bitwise the outputs of the whole."""
     c = conv_case(dtype, [9, 9, 9], D, W, batch=True, seed=3)
@@ -420,6 +423,42 @@ def test_outputs_stay_inside_their_rows():
     v = conv_case("bf16", [2], 33, 4)
     gdr.conv_step(dev(v["x"])[0], rows[1:3], dev(v["weight"]), dev(v["bias"]))
     assert (rows[0] == 7).all() and (rows[3] == 7).all() and (rows[1:3, 2] != 7).any()
+
+
+def test_more_than_the_caches_hold():
+    """Calls of over 256 MB go past the caches: the bits of the same work in two smaller calls."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    new = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    x, dy, w, b = new(2, 11000, 4100), new(2, 11000, 4100), torch.randn(4100, 4, device="cuda"), torch.randn(4100, device="cuda")
+    h0 = new(2, 3, 4100)
+    y, last = gdr.conv_fwd(x, w, b, initial_state=h0)
+    g = gdr.conv_bwd(x, w, dy, b, initial_state=h0, d_final_state=h0, grad_dtype=x.dtype)
+    parts = [gdr.conv_bwd(x[i:i + 1], w, dy[i:i + 1], b, initial_state=h0[i:i + 1], d_final_state=h0[i:i + 1],
+                          grad_dtype=x.dtype) for i in range(2)]
+    for i in range(2):
+        yi, li = gdr.conv_fwd(x[i:i + 1], w, b, initial_state=h0[i:i + 1])
+        assert torch.equal(yi[0], y[i]) and torch.equal(li[0], last[i])
+        assert torch.equal(parts[i]["dx"][0], g["dx"][i]) and torch.equal(parts[i]["dh0"][0], g["dh0"][i])
+    # two orders of a sum of products: at most 160 additions on any path (runs of 128 tokens, their sums by 16
+    # wavefronts), |silu'| < 1.1, and sum |dy u| <= |dy| |u|
+    n_dy, n_u = (t.float().square().sum((0, 1)).sqrt().max() for t in (dy, x))
+    for k, n in (("dweight", n_u + 10), ("dbias", 22000 ** 0.5)):
+        assert float((g[k] - parts[0][k] - parts[1][k]).abs().max()) <= 2 * 160 * U * 1.1 * float(n_dy * n)
+    N, D, S = 520, 4096, 16                              # states of 136 MB, read and written
+    sx, sB = new(N, D), new(N, 1, S)
+    A, st = -torch.rand(D, S, device="cuda"), torch.randn(N, D, S, device="cuda")
+    st2 = st.clone()
+    sy = gdr.scan_step(sx, sx, A, sB, sB, st, dt_softplus=True)
+    for s in (slice(0, 260), slice(260, 520)):
+        assert torch.equal(gdr.scan_step(sx[s], sx[s], A, sB[s], sB[s], st2[s], dt_softplus=True), sy[s])
+    assert torch.equal(st, st2)
+    x, dy = x.view(-1, 4100), dy.view(-1, 4100)
+    y, m, r = gdr.layer_norm_fwd(x, b, b)
+    g = gdr.layer_norm_bwd(x, dy, m, r, b, grad_dtype=x.dtype)
+    for s in (slice(0, 9000), slice(9000, 22000)):
+        ys, ms, rs = gdr.layer_norm_fwd(x[s], b, b)
+        assert torch.equal(ys, y[s]) and torch.equal(ms, m[s]) and torch.equal(rs, r[s])
+        assert torch.equal(gdr.layer_norm_bwd(x[s], dy[s], ms, rs, b, grad_dtype=x.dtype)["dx"], g["dx"][s])
 
 
 def test_empty_calls():

@@ -176,3 +176,21 @@ def test_binding_refuses_cpu_tensors(lib):
               lambda: gdr.layer_norm_fwd(x), lambda: gdr.layer_norm_bwd(x, x, x, x)):
         with pytest.raises(ValueError):
             f()
+
+
+def test_token_strides():
+    """Slices of a wider projection give their stride; anything that is not evenly strided rows is refused."""
+    from chunkwise_gated_delta_local_amd.mixer import _token_stride, _tokens
+    wide = torch.zeros(3, 5, 40)
+    assert _token_stride(wide[..., 8:16], "x", 8) == 40
+    assert _token_stride(wide[..., 8:24].unflatten(-1, (2, 8)), "B", 16) == 40
+    assert _token_stride(wide[:, 0, :8], "x", 8) == 200
+    assert _token_stride(wide[:1, :1, :8], "x", 8) == 8 and _token_stride(wide[:, :1, :8], "x", 8) == 200
+    assert _token_stride(wide[..., 3:4], "x", 1) == 40
+    assert _tokens(wide, "x", wide.shape, 40, torch.float32, wide.device) == 40
+    one = torch.zeros(1, 1, 8)
+    for bad, width in ((wide[:, :4, :8], 8), (wide[..., ::2], 20), (one.expand(3, 5, 8), 8), (one.expand(1, 5, 8), 8),
+                       (wide[0].t(), 5), (wide[:, 1:3, :8], 8), (torch.zeros(8).as_strided((4, 5), (1, 1)), 5),
+                       (wide[..., :16].unflatten(-1, (2, 8))[..., :4], 8)):
+        with pytest.raises(ValueError):
+            _token_stride(bad, "x", width)
