@@ -8,7 +8,7 @@
 // moves once, 8 or 16 bytes a lane, and a wavefront walks a run of tokens with
 // the last W - 1 rows of its channels in registers; only the W - 1 rows before
 // a run (and, backward, behind it) are read again. 65,536 tokens of 8,192 bf16
-// channels: 412 us, 5.2 TB/s, the rate of a copy.
+// channels: 386 us, 5.6 TB/s (a copy of 1 GiB: 5.2).
 #include <type_traits>
 
 #include "gdr_mixer.hpp"
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, int ncb) {
 // W - 1 zeros. A position is stored by the run that holds its token; an initial
 // row by the run that holds the sequence's first token.
 // DT: the type of d_y and d_final_state; GT: that of dx and d_initial_state;
-// ONCE: x and d_y are read past the caches.
+// ONCE: x, d_y and dx go past the caches.
 template <typename T, typename DT, typename GT, int V, int W, bool SILU, bool ONCE>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t ntiles, int run) {
     const int64_t tile = blockIdx.x / ncb;
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int ncb, int64_t n
                         token(cx[j], cdy[j], true, [&](const float (&dp)[V]) {
                             float f[V];
                             gather(dp, f);
-                            store_vec<GT, V>(dxp + (t + j - (W - 1)) * D + ch, f);
+                            store_vec<GT, V, ONCE>(dxp + (t + j - (W - 1)) * D + ch, f);
                         });
                     t += kGroup;
                 } while (more);
@@ -401,7 +401,7 @@ hipError_t launch_conv_fwd(const ConvArgs& a) {
         if (!grid_fits(all * ncb, 256)) return hipErrorInvalidConfiguration;
         if (all == 0) return hipSuccess;
         const dim3 grid((unsigned)(all * ncb));
-        // (65,536 x 8,192 bf16: 390 us, 5.5 TB/s, against 420; y alone past the caches: 406)
+        // (65,536 x 8,192 bf16: 386 us, 5.6 TB/s, against 413; x alone 438, y alone 404)
         if (beyond_caches(2 * a.Ttot * a.p.channels * size_of(a.p.io_dtype)))
             k_conv_fwd<T, V, W, true><<<grid, 256, 0, a.stream>>>(a, ncb, ntiles, run);
         else k_conv_fwd<T, V, W, false><<<grid, 256, 0, a.stream>>>(a, ncb, ntiles, run);
@@ -437,8 +437,8 @@ hipError_t launch_conv_bwd(const ConvArgs& a) {
             typedef decltype(dtype) DT;
             typedef decltype(gtype) GT;
             constexpr bool SILU = decltype(silu_on)::value;
-            // (16,384 x 6,144 bf16: 119 us against 139, dx past the caches too: 130; what the caches hold is 5 % faster
-            // from them)
+            // (16,384 x 6,144 bf16: 126 us against 138, the reads alone 135, dx alone 134; what the caches hold is 5 %
+            // faster from them)
             if (beyond_caches(a.Ttot * a.p.channels * (int64_t)(sizeof(T) + sizeof(DT) + sizeof(GT))))
                 k_conv_bwd<T, DT, GT, V, W, SILU, true><<<grid, 64 * nw, 0, a.stream>>>(a, ncb, ntiles, run);
             else k_conv_bwd<T, DT, GT, V, W, SILU, false><<<grid, 64 * nw, 0, a.stream>>>(a, ncb, ntiles, run);

@@ -65,7 +65,7 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[4], int& slot) {
     return v;
 }
 
-// ONCE: y goes past the caches
+// ONCE: x and y go past the caches
 template <typename T, typename OT, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
     __shared__ float red[2][4];
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (r < a.p.rows && (i * TPR + l) * V < C)
-                raw[i] = load_piece<T, V>((const T*)a.x + r * a.p.x_stride, (i * TPR + l) * V, C);
+                raw[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, (i * TPR + l) * V, C);
     };
     const int64_t step = (int64_t)gridDim.x * rpb;
     int64_t r = (int64_t)blockIdx.x * rpb + threadIdx.x / TPR;
@@ -134,8 +134,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(NormArgs a) {
 // Backward: with xhat = (x - mean) rstd and c = d_y weight,
 //   dx = rstd (c - mean(c) - xhat mean(c xhat)).
 // Each thread also sums d_y xhat and d_y of its columns over its rows; the rows
-// of a workgroup are joined in LDS, the workgroups by k_sum_partials. ONCE: x and
-// d_y are read past the caches.
+// of a workgroup are joined in LDS, the workgroups by k_sum_partials. ONCE: x,
+// d_y and dx go past the caches.
 template <typename T, typename DT, typename GT, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_norm_bwd(NormArgs a) {
     constexpr int RPB = kThreads / TPR;
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(NormArgs a) {
             float d[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) d[v] = rstd * (g[i][v] - s1 - h[i][v] * s2);
-            store_piece<GT, V>((GT*)a.dx + r * C, c, C, d);
+            store_piece<GT, V, ONCE>((GT*)a.dx + r * C, c, C, d);
         }
     }
     float* part = a.partial + (int64_t)blockIdx.x * 2 * C;
@@ -315,11 +315,11 @@ hipError_t launch_norm_fwd(const NormArgs& a) {
     return by_shape(a, [&](auto type, auto vec, auto nv, auto tpr) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-        // four trips a workgroup: 2,097,152 rows of 128 take 203 us, 5.4 TB/s (with 16: 223, one: 249), 65,536 of 4,096
-        // 189 (eight: 198, one: 240)
+        // four trips a workgroup: 2,097,152 rows of 128 take 206 us (with 16: 223, one: 249), 65,536 of 4,096 189
+        // (eight: 198, one: 240)
         const int64_t n = row_blocks(a.p.rows, TPR), most = n / 4 > 8192 ? n / 4 : 8192;
         const dim3 grid((unsigned)(n < most ? n : most));
-        // (65,536 x 4,096: 184 us against 189 with y past the caches, 2,097,152 x 128: 193 against 203; x too: 200, 202)
+        // (65,536 x 4,096: 180 us against 189, 2,097,152 x 128: 188 against 206; y alone 184 and 194, x alone 186 and 201)
         const bool once = beyond_caches(a.p.rows * a.p.cols * (size_of(a.p.io_dtype) + size_of(a.p.out_dtype)));
         auto go = [&](auto otype, auto past) {
             k_norm_fwd<T, decltype(otype), V, NV, TPR, decltype(past)::value><<<grid, kThreads, 0, a.stream>>>(a);
@@ -335,7 +335,7 @@ hipError_t launch_norm_bwd(const NormArgs& a) {
         hipError_t e = by_shape(a, [&](auto type, auto vec, auto nv, auto tpr) {
             typedef decltype(type) T;
             constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-            // (16,384 x 4,096 bf16: 82 us against 87; dx past the caches too: 86)
+            // (65,536 x 4,096 bf16: 281 us against 290, 16,384 x 4,096: 85 against 87; the reads alone 295 and 84)
             const bool once = beyond_caches(
                 a.p.rows * a.p.cols * (size_of(a.p.io_dtype) + size_of(a.p.dy_dtype) + size_of(a.p.grad_dtype)));
             auto go = [&](auto dtype, auto gtype, auto past) {
