@@ -60,7 +60,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_fwd(ScanArgs a, Segments sg, in
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
         const bool in = act && q * SPL + i < S;
-        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        A2[i] = in ? log2_rate(a.A[(int64_t)ch * S + q * SPL + i]) : 0.f;
         h0[i] = in && a.S0 ? a.S0[st0 + i] : 0.f;
     }
     sg.template enter<SPL>(n, seg, seq, a.p.channels, ch, q, A2, h0);

@@ -13,6 +13,12 @@ constexpr int kCh = 16;                                    // channels of a wave
 // exponentials and as many products stay in registers.
 template <int SPL> constexpr int kPiece = SPL <= 4 ? 16 : SPL <= 8 ? 8 : 4;
 
+// A log2 e, finite where A is -inf or near the lowest float: tokens past a
+// sequence's end multiply it by a delta of zero. NaN stays.
+__device__ __forceinline__ float log2_rate(float A) {
+    const float r = A * kLog2e;
+    return r < -__FLT_MAX__ ? -__FLT_MAX__ : r;
+}
 __device__ __forceinline__ void swap32(float& a, float& b) {   // a = {a.lo, b.lo}, b = {a.hi, b.hi} (halves of 32 lanes)
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     a = __uint_as_float(r[0]);
@@ -271,7 +277,7 @@ __global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, Segments sg, fl
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
         const bool in = act && q * SPL + i < S;
-        A2[i] = in ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        A2[i] = in ? log2_rate(a.A[(int64_t)ch * S + q * SPL + i]) : 0.f;
         h0[i] = !ENDS && in && a.S0 ? a.S0[((int64_t)n * a.p.channels + ch) * S + q * SPL + i] : 0.f;
     }
     if (!ENDS) sg.template enter<SPL>(n, seg, seq, a.p.channels, ch, q, A2, h0);

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(512) void k_scan_grad_ends(ScanArgs a, Segments sg,
     float A2[SPL], G[SPL], total = 0.f;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
-        A2[i] = act && q * SPL + i < S ? a.A[(int64_t)ch * S + q * SPL + i] * kLog2e : 0.f;
+        A2[i] = act && q * SPL + i < S ? log2_rate(a.A[(int64_t)ch * S + q * SPL + i]) : 0.f;
         G[i] = 0.f;
     }
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f;
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
 #pragma unroll
         for (int i = 0; i < SPL; ++i) {
             const bool in = act[j] && q * SPL + i < S;
-            A2[j * SPL + i] = in ? a.A[(int64_t)ch[j] * S + q * SPL + i] * kLog2e : 0.f;
+            A2[j * SPL + i] = in ? log2_rate(a.A[(int64_t)ch[j] * S + q * SPL + i]) : 0.f;
             G[j * SPL + i] = in && a.dST ? a.dST[st0[j] + i] : 0.f;
             dA[j * SPL + i] = 0.f;
         }

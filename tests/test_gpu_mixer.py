@@ -355,6 +355,19 @@ def test_sequences_do_not_touch_each_other():
         assert torch.equal(back["dh0"][[0, 2]], clean[1]["dh0"][[0, 2]])
 
 
+@pytest.mark.parametrize("lens,D", [([70, 5, 0, 33], 32), ([3001], 16)])
+def test_transitions_that_forget_at_once(lens, D):
+    """exp(delta A) is 0 for A = -1e30 and for the lowest A, whose product with log2 e is no longer finite: the
+    same bits. The lengths end inside a tile; the long sequence is cut into segments."""
+    def all_of(low):
+        c = scan_case("bf16", lens, D, 16)
+        c["A"][1] = c["A"][:, 3] = low
+        return [*run_scan(c), *run_scan(c, back=True).values()]
+    for low in (-3e38, float("-inf")):
+        for i, (a, b) in enumerate(zip(all_of(-1e30), all_of(low))):
+            assert torch.isfinite(b).all() and torch.equal(a, b), (low, i)
+
+
 def test_same_bits_again_and_on_another_stream():
     c, v = scan_case("bf16", [300, 41], 96, 16), conv_case("bf16", [300, 41], 96, 4)
     x, w, b, dy = (dev(t) for t in norm_case("bf16", 1000, 256))
