@@ -474,6 +474,67 @@ def test_more_than_the_caches_hold():
         assert torch.equal(gdr.layer_norm_bwd(x[s], dy[s], ms, rs, b, grad_dtype=x.dtype)["dx"], g["dx"][s])
 
 
+def test_elements_past_31_bits():
+    """Tensors of more than 2^31 elements: the sequence (or the rows) at their end against the same work alone, or
+    against the definition where the split of the work differs. Every call is issued on more than 2^31 elements."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    new = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)
+    n, D, S, tail = 131000, 16400, 4, 50
+    x = new(1, n, D)
+    cu = torch.tensor([0, n - tail, n], dtype=torch.int32)
+    kw, end = dict(cu_seqlens=cu.cuda(), cu_seqlens_cpu=cu), x[:, n - tail:].contiguous()
+    w = torch.randn(D, 4, device="cuda") / 2
+    y, last = gdr.conv_fwd(x, w, **kw)
+    ye, le = gdr.conv_fwd(end, w)
+    assert torch.equal(y[0, n - tail:], ye[0]) and torch.equal(last[1], le[0])
+    del y
+    dx = gdr.conv_bwd(x, w, x, grad_dtype=x.dtype, **kw)["dx"]
+    assert torch.equal(dx[0, n - tail:], gdr.conv_bwd(end, w, end, grad_dtype=x.dtype)["dx"][0])
+    del dx
+
+    A, B = -torch.rand(D, S, device="cuda") - 0.1, new(1, n, 1, S)
+    y, last = gdr.scan_fwd(x, x, A, B, B, z=x, dt_softplus=True, **kw)
+    y = y[0, n - tail:].clone()
+    g = gdr.scan_bwd(x, x, A, B, B, x, z=x, dt_softplus=True, grad_dtype=x.dtype, **kw)
+    g = {k: (v[0, n - tail:] if v.dim() > 2 and k != "dh0" else v[1:] if k == "dh0" else v).clone() for k, v in g.items()}
+    xf, Bf = f64(end[0]), f64(B[0, n - tail:])
+    delta, gate, zm = om.softplus(xf), om.silu(xf), np.abs(xf).max()
+    r = dict(x=xf, delta=delta, A=f64(A), B=Bf, C=Bf, skip=np.zeros(D), cu=offsets([tail]), h0=np.zeros((1, D, S)))
+    a = {k: np.abs(v) if k not in ("A", "cu") else v for k, v in r.items()}
+    eta = 2 * zm + 12
+    chain = tail * (float((delta[:, :, None] * -r["A"]).max()) * (20 + eta) + 3)
+    v, _, rlast = om.scan(**r)
+    M, _, Mlast = om.scan(**a)
+    close("final state", last[1:], rlast, Mlast, chain + eta + S + 10)
+    close("y", y, v * gate, M * np.abs(gate), chain + eta + S + 20 + 2 * zm)
+    ds, base = xf * gate, 2 * chain + 2 * eta + 2 * zm + 12 + S + 20
+    zero = np.zeros((1, D, S))
+    ref = om.scan_backward(**r, ds=ds, d_last=zero)
+    M = om.scan_backward(**a, ds=np.abs(ds), d_last=zero, factor_A=-r["A"])
+    for name, i, terms in (("dx", 0, 0), ("dB", 3, D), ("dC", 4, D), ("dh0", 6, 0)):
+        close(name, g[name], ref[i], M[i], base + terms)
+    s = 1 / (1 + np.exp(-xf))
+    close("ddt", g["ddt"], ref[1] * s, M[1] * s, base + 2 * zm + 10)
+    del y, g, x, B
+
+    N, S = 8200, 16                                      # states of 2^31 elements
+    sx, sB = new(N, D), new(N, 1, S)
+    A, st = -torch.rand(D, S, device="cuda"), torch.full((N, D, S), 0.5, device="cuda")
+    sy = gdr.scan_step(sx, sx, A, sB, sB, st, dt_softplus=True)
+    st2 = torch.full((9, D, S), 0.5, device="cuda")
+    ye = gdr.scan_step(sx[-9:], sx[-9:], A, sB[-9:], sB[-9:], st2, dt_softplus=True)
+    assert torch.equal(sy[-9:], ye) and torch.equal(st[-9:], st2)
+    del st
+
+    x, w = new((1 << 24) + 70, 128), torch.randn(128, device="cuda")
+    y, m, r = gdr.layer_norm_fwd(x, w, w)
+    ys, ms, rs = gdr.layer_norm_fwd(x[-20000:], w, w)
+    assert torch.equal(y[-20000:], ys) and torch.equal(m[-20000:], ms) and torch.equal(r[-20000:], rs)
+    del y
+    g = gdr.layer_norm_bwd(x, x, m, r, w, grad_dtype=x.dtype)
+    assert torch.equal(g["dx"][-20000:], gdr.layer_norm_bwd(x[-20000:], x[-20000:], ms, rs, w, grad_dtype=x.dtype)["dx"])
+
+
 def test_empty_calls():
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
     f = torch.float32
