@@ -64,7 +64,8 @@ gdr_status_t check_seqs(int64_t batch, int64_t seq_len, int32_t num_seqs, const 
     return GDR_OK;
 }
 
-gdr_status_t check_stride(const char* name, int64_t stride, int64_t row, int64_t most = (int64_t)1 << 40) {
+constexpr int64_t kMostStride = (int64_t)1 << 40;
+gdr_status_t check_stride(const char* name, int64_t stride, int64_t row, int64_t most = kMostStride) {
     if (stride < row || stride > most)
         return fail(GDR_ERR_SHAPE, "%s (%lld) must be at least the row's %lld elements and at most %lld", name,
                     (long long)stride, (long long)row, (long long)most);
@@ -122,7 +123,10 @@ size_t conv_bwd_bytes(const gdr_conv_problem_t* p) {
 }
 
 // ---------------------------------------------------------------- scan
-gdr_status_t check_scan(const gdr_scan_problem_t* p, bool has_z) {
+// the tile kernels' limit: a tile of 128 tokens lies within the 2^31 bytes of a buffer's offsets
+constexpr int64_t kMostTileStride = ((int64_t)1 << 22) - 1;
+
+gdr_status_t check_scan(const gdr_scan_problem_t* p, bool has_z, int64_t most = kMostTileStride) {
     if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
     GDR_TRY(check_tokens(p->batch, p->seq_len, p->num_seqs, p->channels));
     if (p->groups < 1 || p->channels % p->groups != 0)
@@ -136,9 +140,8 @@ gdr_status_t check_scan(const gdr_scan_problem_t* p, bool has_z) {
     if (p->dt_softplus != 0 && p->dt_softplus != 1)
         return fail(GDR_ERR_UNSUPPORTED, "dt_softplus must be 0 or 1 (got %d)", p->dt_softplus);
     const int64_t rows = (int64_t)p->groups * p->state_dim;
-    // a tile of 128 tokens lies within the 2^31 bytes of a buffer's offsets
-    const int64_t most = ((int64_t)1 << 22) - 1;
-    if (p->channels > most) return fail(GDR_ERR_SHAPE, "channels must be at most %lld", (long long)most);
+    if (p->channels > kMostTileStride)
+        return fail(GDR_ERR_SHAPE, "channels must be at most %lld", (long long)kMostTileStride);
     GDR_TRY(check_stride("x_stride", p->x_stride, p->channels, most));
     GDR_TRY(check_stride("dt_stride", p->dt_stride, p->channels, most));
     if (has_z) GDR_TRY(check_stride("z_stride", p->z_stride, p->channels, most));
@@ -271,7 +274,7 @@ gdr_status_t gdr_scan_fwd(const gdr_scan_problem_t* p, const void* x, const void
 gdr_status_t gdr_scan_step(const gdr_scan_problem_t* p, const void* x, const void* dt, const float* A, const void* B,
                            const void* C, const float* D, const void* z, const float* dt_bias, float* state, void* y,
                            void* stream) {
-    GDR_TRY(check_scan(p, z != nullptr));
+    GDR_TRY(check_scan(p, z != nullptr, kMostStride));          // indexed in 64 bits
     if (p->batch != p->num_seqs || p->seq_len != 1)
         return fail(GDR_ERR_SHAPE, "one token a sequence: batch must equal num_seqs and seq_len 1");
     const int32_t io = p->io_dtype;

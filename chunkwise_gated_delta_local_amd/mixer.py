@@ -5,7 +5,8 @@ scan and layer norm.
 As in ``api``, argument marshalling only: torch supplies device memory and the
 current HIP stream. Inputs that hold tokens ([B, T, ...]) may be slices of a
 wider projection: the elements of a token are contiguous and the tokens evenly
-strided. Everything else is contiguous. Variable-length batches: B = 1 and
+strided (fewer than 2^22 elements apart in scan_fwd and scan_bwd). Everything
+else is contiguous. Variable-length batches: B = 1 and
 ``cu_seqlens`` (with ``cu_seqlens_cpu``, its host copy, no device
 synchronisation is needed); empty sequences are allowed.
 """

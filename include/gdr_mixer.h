@@ -94,7 +94,7 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* problem, const void* x, cons
  */
 typedef struct {
     int64_t batch, seq_len;
-    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;   /* elements between tokens, below 2^22 */
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;   /* elements between tokens; fwd, bwd: below 2^22 */
     int32_t num_seqs;
     int32_t channels;       /* >= 1                                                      */
     int32_t groups;         /* >= 1, divides channels                                    */
