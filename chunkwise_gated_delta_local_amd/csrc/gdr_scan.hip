@@ -186,11 +186,11 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int64_t nch) {
     const float* Ap = a.A + (int64_t)ch * S + s0;
     const T* Bp = (const T*)a.B + n * a.p.b_stride + (int64_t)g * S + s0;
     const T* Cp = (const T*)a.C + n * a.p.c_stride + (int64_t)g * S + s0;
-    float h[4] = {}, A2[4] = {}, B[4] = {}, C[4] = {};
+    float h[4] = {}, A[4] = {}, B[4] = {}, C[4] = {};
     if (WIDE) {
         if (s0 < S) {
             unpack<float, 4>(load_raw<float, 4, ONCE>(st), h);
-            unpack<float, 4>(load_raw<float, 4>(Ap), A2);
+            unpack<float, 4>(load_raw<float, 4>(Ap), A);
             unpack<T, 4>(load_raw<T, 4>(Bp), B);
             unpack<T, 4>(load_raw<T, 4>(Cp), C);
         }
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int64_t nch) {
         for (int j = 0; j < 4; ++j)
             if (s0 + j < S) {
                 h[j] = st[j];
-                A2[j] = Ap[j];
+                A[j] = Ap[j];
                 B[j] = to_f(Bp[j]);
                 C[j] = to_f(Cp[j]);
             }
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int64_t nch) {
     float y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        h[j] = __builtin_fmaf(exp_fast(A2[j] * d), h[j], dx * B[j]);
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(log2_rate(A[j]) * d), h[j], dx * B[j]);
         y = __builtin_fmaf(C[j], h[j], y);
     }
     if (WIDE) {

@@ -90,7 +90,8 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* problem, const void* x, cons
  *   state    [num_seqs][channels][state_dim] fp32
  * exp(delta A) is meant to be at most one; a growing state may overflow where
  * pieces of a sequence are joined although its running value does not, and an
- * infinite one become NaN there.
+ * infinite one become NaN there. A may be -inf: a step size above zero then
+ * forgets the state, one of zero keeps it.
  */
 typedef struct {
     int64_t batch, seq_len;

@@ -28,3 +28,27 @@ def test_scan_step_of_time_slices(dtype):
     sliced, alone = step(lambda t: t, h0.clone()), step(lambda t: t.contiguous(), h0.clone())
     assert torch.equal(sliced[0], alone[0]) and torch.equal(sliced[1], alone[1])
     assert not torch.equal(alone[1], h0)
+
+
+@pytest.mark.parametrize("S", [16, 6])
+def test_transitions_that_forget_at_once_in_one_token(S):
+    """A = -inf and A near the lowest float, step sizes of zero among them (softplus far below its underflow, or dt = 0):
+    a token alone leaves the state that a prompt of one token leaves, bit for bit: exp(-inf 0) counts as 1."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    N, D = 5, 48
+    x, z = normal(gen, N, D), normal(gen, N, D)
+    B, C, h0 = normal(gen, N, 1, S), normal(gen, N, 1, S), normal(gen, N, D, S)
+    A = -torch.rand(D, S, device="cuda")
+    A[1], A[:, 3], A[7, 2] = float("-inf"), float("-inf"), -3e38
+    for soft, dt, zero in ((True, normal(gen, N, D), -300.0), (False, torch.rand(N, D, device="cuda"), 0.0)):
+        dt[1], dt[3, ::2] = zero, zero
+        state = h0.clone()
+        y = gdr.scan_step(x, dt, A, B, C, state, z=z, dt_softplus=soft)
+        one = lambda t: t[:, None].contiguous()
+        yp, last = gdr.scan_fwd(one(x), one(dt), A, one(B), one(C), z=one(z), dt_softplus=soft, initial_state=h0)
+        assert torch.isfinite(state).all() and torch.isfinite(y).all()
+        assert torch.equal(state, last)
+        assert torch.equal(state[1], h0[1])                 # no step: the state stays
+        # two orders of a sum of S products and the gate
+        bound = (S + 4) * 2.0 ** -24 * ((C.abs() * last.abs()).sum(-1) * z.abs()) + 1e-30
+        assert ((y - yp[:, 0]).abs() <= 2 * bound).all()
