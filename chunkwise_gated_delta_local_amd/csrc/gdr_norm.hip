@@ -1,9 +1,9 @@
 // Layer norm over rows, forward and backward (include/gdr_mixer.h). A few
 // operations an element: HBM bounds both, so a row is read once and stays in
 // registers between the statistics and the output. TPR threads share a row,
-// each holding NV pieces of V = 16 bytes; rows go round a grid that fills the
-// card once, the weights stay in registers meanwhile, and the next row is on
-// its way while one is worked on.
+// each holding NV pieces of V = 16 bytes; rows go round the grid, the weights
+// stay in registers meanwhile, and the next row is on its way while one is
+// worked on.
 //
 // Rows of any length and alignment move in 16-byte accesses (global memory
 // takes them at the alignment of an element); only the piece that the row's end
@@ -301,6 +301,16 @@ hipError_t by_shape(const NormArgs& a, F f) {
 
 int64_t row_blocks(int64_t rows, int TPR) { return (rows + kThreads / TPR - 1) / (kThreads / TPR); }
 
+// Workgroups of the forward pass, for n that one trip each would take: four trips a
+// workgroup (2,097,152 rows of 128: 206 us, with 16 trips 223, one 249; 65,536 of
+// 4,096: 189, eight 198, one 240), and more where a launch's threads would pass 32 bits.
+int64_t norm_fwd_blocks(int64_t n) {
+    constexpr int64_t least = 8192, most = (int64_t)1 << 22;
+    static_assert(most * kThreads < ((int64_t)1 << 32), "threads of a launch");
+    const int64_t quarter = n / 4 > least ? n / 4 : least;
+    return n < quarter ? n : quarter < most ? quarter : most;
+}
+
 }  // namespace
 
 // Workgroups of the backward pass, whose partial sums are written and read once
@@ -315,10 +325,7 @@ hipError_t launch_norm_fwd(const NormArgs& a) {
     return by_shape(a, [&](auto type, auto vec, auto nv, auto tpr) {
         typedef decltype(type) T;
         constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;
-        // four trips a workgroup: 2,097,152 rows of 128 take 206 us (with 16: 223, one: 249), 65,536 of 4,096 189
-        // (eight: 198, one: 240)
-        const int64_t n = row_blocks(a.p.rows, TPR), most = n / 4 > 8192 ? n / 4 : 8192;
-        const dim3 grid((unsigned)(n < most ? n : most));
+        const dim3 grid((unsigned)norm_fwd_blocks(row_blocks(a.p.rows, TPR)));
         // (65,536 x 4,096: 180 us against 189, 2,097,152 x 128: 188 against 206; y alone 184 and 194, x alone 186 and 201)
         const bool once = beyond_caches(a.p.rows * a.p.cols * (size_of(a.p.io_dtype) + size_of(a.p.out_dtype)));
         auto go = [&](auto otype, auto past) {

@@ -52,3 +52,19 @@ def test_transitions_that_forget_at_once_in_one_token(S):
         # two orders of a sum of S products and the gate
         bound = (S + 4) * 2.0 ** -24 * ((C.abs() * last.abs()).sum(-1) * z.abs()) + 1e-30
         assert ((y - yp[:, 0]).abs() <= 2 * bound).all()
+
+
+def test_norm_of_more_rows_than_threads_of_a_launch():
+    """2^30 + 37 short rows, forward and backward: the bits of the same rows in smaller calls."""
+    rows, cols, part = (1 << 30) + 37, 2, 1 << 28
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(0, 1 << 14, (rows, cols), generator=gen, device="cuda", dtype=torch.int16).view(torch.bfloat16)
+    w, b = normal(gen, cols), normal(gen, cols)
+    y, mean, rstd = gdr.layer_norm_fwd(x, w, b)
+    dx = gdr.layer_norm_bwd(x, y, mean, rstd, w, grad_dtype=x.dtype)["dx"]
+    for i in range(0, rows, part):
+        s = slice(i, min(i + part, rows))
+        ys, ms, rs = gdr.layer_norm_fwd(x[s], w, b)
+        assert torch.equal(y[s], ys) and torch.equal(mean[s], ms) and torch.equal(rstd[s], rs), i
+        assert torch.equal(dx[s], gdr.layer_norm_bwd(x[s], ys, ms, rs, w, grad_dtype=x.dtype)["dx"]), i
+    assert float(rstd.max()) <= 1e-5 ** -0.5 * 1.001 and bool((mean[-37:] > 0).any())
