@@ -59,6 +59,9 @@ struct ScanArgs {
     char* ws;
     hipStream_t stream;
 };
+// Elements between tokens that the scan's tile kernels take, and channels: a tile of
+// 128 tokens lies within the 2^31 bytes of a buffer's offsets.
+constexpr int64_t kMostTileStride = ((int64_t)1 << 22) - 1;
 size_t scan_fwd_workspace(const gdr_scan_problem_t& p);
 size_t scan_bwd_workspace(const gdr_scan_problem_t& p);
 hipError_t launch_scan_fwd(const ScanArgs& a);

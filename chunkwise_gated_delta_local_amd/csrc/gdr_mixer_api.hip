@@ -5,6 +5,7 @@
 namespace {
 
 using gdr::fail;
+using gdr::kMostTileStride;
 
 bool is_dtype(int32_t t) { return t == GDR_F32 || t == GDR_BF16; }
 // a type that may be the io type or fp32
@@ -123,9 +124,6 @@ size_t conv_bwd_bytes(const gdr_conv_problem_t* p) {
 }
 
 // ---------------------------------------------------------------- scan
-// the tile kernels' limit: a tile of 128 tokens lies within the 2^31 bytes of a buffer's offsets
-constexpr int64_t kMostTileStride = ((int64_t)1 << 22) - 1;
-
 gdr_status_t check_scan(const gdr_scan_problem_t* p, bool has_z, int64_t most = kMostTileStride) {
     if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
     GDR_TRY(check_tokens(p->batch, p->seq_len, p->num_seqs, p->channels));

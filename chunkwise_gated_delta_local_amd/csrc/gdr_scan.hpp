@@ -93,6 +93,7 @@ __device__ __forceinline__ int64_t first_slot(int64_t s, int tile, int n) {
 // past its end read zero and store nothing, so that the tokens behind a sequence
 // need no branches. Offsets inside are bytes, (token - t) * stride + element.
 constexpr int kNowhere = 0x7fffffff;                       // an offset past the end of any of them
+static_assert(128 * kMostTileStride * 4 <= kNowhere, "a tile of 128 tokens");
 template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t token_rows(const void* base, int64_t t, int64_t stride, int64_t rows) {
     return buf_rsrc((const T*)base + t * stride, (uint32_t)(rows * stride * (int64_t)sizeof(T)));

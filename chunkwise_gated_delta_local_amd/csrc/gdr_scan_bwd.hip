@@ -41,6 +41,11 @@ template <int SPL> struct Bwd {
     static constexpr int TOK = CHB * 4 + 8;                           // floats of a token's row: its 4 writers on other banks
     static constexpr int kWaveFloats = L * TOK + 2 * L * SP;      // (delta, delta x, ds, -); B, C
     static constexpr int kPubFloats = 3 * 64 * EPT;                   // P, h_loc, G_loc
+    // Idle lanes' offset, to which the distance of later tokens is added: past the end
+    // of the rows of a tile, and within an int after the additions.
+    static constexpr int IDLE = 1 << 30;
+    static_assert(NW * L * kMostTileStride * 4 <= IDLE, "rows of a tile");
+    static_assert(IDLE + (L / 4 - 1) * 4 * kMostTileStride * 4 <= 0x7fffffff, "offsets of the tokens of an idle lane");
     static constexpr size_t lds(int nw) { return 4 * ((size_t)nw * (kWaveFloats + 2 * kPubFloats) + 2 * 64 * EPT); }
 };
 
@@ -235,11 +240,11 @@ __global__ __launch_bounds__(64 * Bwd<SPL>::NW, SPL == 16 ? 1 : 2) void k_scan_b
     int ox[J], odt[J], oz[J], ody[J], og[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        ox[j] = act[j] ? (int)((r0 * a.p.x_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
-        odt[j] = act[j] ? (int)((r0 * a.p.dt_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
-        oz[j] = act[j] ? (int)((r0 * a.p.z_stride + ch[j]) * (int)sizeof(T)) : kNowhere;
-        ody[j] = act[j] ? (int)((r0 * D + ch[j]) * dyb) : kNowhere;
-        og[j] = act[j] ? (int)((r0 * D + ch[j]) * gb) : kNowhere;
+        ox[j] = act[j] ? (int)((r0 * a.p.x_stride + ch[j]) * (int)sizeof(T)) : V::IDLE;
+        odt[j] = act[j] ? (int)((r0 * a.p.dt_stride + ch[j]) * (int)sizeof(T)) : V::IDLE;
+        oz[j] = act[j] ? (int)((r0 * a.p.z_stride + ch[j]) * (int)sizeof(T)) : V::IDLE;
+        ody[j] = act[j] ? (int)((r0 * D + ch[j]) * dyb) : V::IDLE;
+        og[j] = act[j] ? (int)((r0 * D + ch[j]) * gb) : V::IDLE;
     }
     const int kx = (int)(4 * a.p.x_stride * (int)sizeof(T)), kdt = (int)(4 * a.p.dt_stride * (int)sizeof(T));
     const int kz = (int)(4 * a.p.z_stride * (int)sizeof(T)), kdy = 4 * D * dyb, kg = 4 * D * gb;

@@ -68,3 +68,27 @@ def test_norm_of_more_rows_than_threads_of_a_launch():
         assert torch.equal(y[s], ys) and torch.equal(mean[s], ms) and torch.equal(rstd[s], rs), i
         assert torch.equal(dx[s], gdr.layer_norm_bwd(x[s], ys, ms, rs, w, grad_dtype=x.dtype)["dx"]), i
     assert float(rstd.max()) <= 1e-5 ** -0.5 * 1.001 and bool((mean[-37:] > 0).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,G,S", [(40, 2, 16), (19, 1, 5), (16, 1, 40)])
+def test_scan_of_the_widest_rows(dtype, D, G, S):
+    """Tokens 2^22 - 1 elements apart, the most that the tiles' 31-bit offsets take, with channels that leave lanes idle:
+    the bits of dense inputs, forward and backward."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    T, width = 300, (1 << 22) - 1
+    wide = torch.empty(1, T, width, device="cuda", dtype=dtype)
+    ends = (0, D, width - D)                                # slices at both ends of a row
+    x, dt, z = (wide[..., i:i + D] for i in ends)
+    B, C = (wide[..., i:i + G * S].unflatten(-1, (G, S)) for i in (2 * D, width // 2))
+    for t in (x, dt, z, B, C):
+        t.copy_(normal(gen, *t.shape, dtype=dtype))
+    A, h0 = -torch.rand(D, S, device="cuda"), normal(gen, 1, D, S)
+    d_y = normal(gen, 1, T, D, dtype=dtype)
+
+    def all_of(f):
+        a = [f(x), f(dt), A, f(B), f(C)]
+        kw = dict(z=f(z), dt_softplus=True, initial_state=h0)
+        return [*gdr.scan_fwd(*a, **kw), *gdr.scan_bwd(*a, d_y, grad_dtype=dtype, **kw).values()]
+    for i, (a, b) in enumerate(zip(all_of(lambda t: t), all_of(lambda t: t.contiguous()))):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
