@@ -98,6 +98,8 @@ gdr_status_t done(hipError_t e) {
 gdr_status_t check_conv(const gdr_conv_problem_t* p) {
     if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
     GDR_TRY(check_tokens(p->batch, p->seq_len, p->num_seqs, p->channels));
+    // the kernels count channels in an int, past the last one by a workgroup's
+    if (p->channels > (1 << 30)) return fail(GDR_ERR_SHAPE, "channels must be at most 2^30 (got %d)", p->channels);
     if (!is_dtype(p->io_dtype)) return fail(GDR_ERR_DTYPE, "unknown io_dtype %d", p->io_dtype);
     if (!io_or_f32(p->param_dtype, p->io_dtype))
         return fail(GDR_ERR_DTYPE, "param_dtype must equal io_dtype or be GDR_F32");

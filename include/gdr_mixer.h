@@ -48,7 +48,7 @@ typedef struct {
     int64_t batch, seq_len;
     int64_t x_stride;       /* elements between tokens of x, >= channels                 */
     int32_t num_seqs;       /* batch, or len(cu_seqlens) - 1                             */
-    int32_t channels;       /* D >= 1                                                    */
+    int32_t channels;       /* D: 1 to 2^30                                              */
     int32_t width;          /* W: 2, 3 or 4                                              */
     int32_t activation;     /* gdr_activation_t                                          */
     int32_t io_dtype;       /* x, y and states                                           */
@@ -97,7 +97,7 @@ typedef struct {
     int64_t batch, seq_len;
     int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;   /* elements between tokens; fwd, bwd: below 2^22 */
     int32_t num_seqs;
-    int32_t channels;       /* >= 1                                                      */
+    int32_t channels;       /* 1 to 2^22 - 1                                             */
     int32_t groups;         /* >= 1, divides channels                                    */
     int32_t state_dim;      /* 1 to 64                                                   */
     int32_t dt_softplus;    /* 0 or 1                                                    */

@@ -87,3 +87,18 @@ def test_norm_rows(launches):
     for (op, kw), (status, message, found) in zip(calls, launches(calls)):
         assert status == 0, (op, kw, message)
         assert found and all(0 < g * b < 1 << 32 for g, b, _ in found), (op, kw, found)
+
+
+def test_conv_channels(launches):
+    """Channels are counted in an int, several to a lane: more than 2^30 of them are refused."""
+    calls = [(op, dict(batch=1, num_seqs=1, seq_len=1, channels=D, x_stride=D, width=W))
+             for op in ("conv_fwd", "conv_step", "conv_bwd") for W in (2, 4)
+             for D in (1, 5, 8192, (1 << 22) + 3, 1 << 30, (1 << 30) + 1, (1 << 31) - 512, (1 << 31) - 2, (1 << 31) - 1)]
+    for (op, kw), (status, message, found) in zip(calls, launches(calls)):
+        D = kw["channels"]
+        assert status == (2 if D > 1 << 30 else 0), (op, kw, message)
+        if status:
+            assert not found and "channels" in message, (op, kw, message, found)
+        else:
+            assert found and all(0 < b <= 1024 and 0 < g * b < 1 << 32 for g, b, _ in found), (op, kw, found)
+            assert found[0][0] * found[0][1] * 8 >= D, (op, kw, found)     # a lane takes 8 channels at most
