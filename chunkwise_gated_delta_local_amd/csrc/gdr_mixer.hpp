@@ -167,20 +167,6 @@ __device__ __forceinline__ void load_vec_as(const void* p, int64_t idx, int f32,
         unpack<T, V>(load_raw<T, V>(reinterpret_cast<const T*>(p) + idx), f);
     }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_vec_as(void* p, int64_t idx, const float (&f)[V], int f32) {
-    if (f32) {
-        float* q = reinterpret_cast<float*>(p) + idx;
-        if constexpr (V == 1) {
-            q[0] = f[0];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i += 4) *reinterpret_cast<f32x4*>(q + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
-        }
-    } else {
-        store_vec<T, V>(reinterpret_cast<T*>(p) + idx, f);
-    }
-}
 
 // Token range of sequence n, clamped to the token axis whatever cu holds.
 __device__ __forceinline__ void seq_range(const int32_t* cu, int n, int64_t T_row, int64_t Ttot, int64_t* s,
