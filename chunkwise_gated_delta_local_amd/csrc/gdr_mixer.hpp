@@ -158,7 +158,7 @@ __device__ __forceinline__ void load_vec_as(const void* p, int64_t idx, int f32,
         } else {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(q + i);
+                const auto v = load_raw<float, 4>(q + i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[i + j] = v[j];
             }

@@ -92,3 +92,41 @@ def test_scan_of_the_widest_rows(dtype, D, G, S):
         return [*gdr.scan_fwd(*a, **kw), *gdr.scan_bwd(*a, d_y, grad_dtype=dtype, **kw).values()]
     for i, (a, b) in enumerate(zip(all_of(lambda t: t), all_of(lambda t: t.contiguous()))):
         assert torch.isfinite(a).all() and torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_bases_aligned_to_an_element_only(dtype):
+    """Every tensor one element behind an aligned address: the bits of aligned ones."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    N, T, D, G, S = 2, 70, 72, 2, 16
+
+    def odd(t):
+        buf = torch.empty(t.numel() + 1, device="cuda", dtype=t.dtype)
+        out = buf[1:].view(t.shape)
+        assert out.data_ptr() % 16 and out.is_contiguous()
+        return out.copy_(t)
+    io = lambda *s: normal(gen, *s, dtype=dtype)
+    x, dt, z, d_y, B, C = io(N, T, D), io(N, T, D), io(N, T, D), io(N, T, D), io(N, T, G, S), io(N, T, G, S)
+    f32 = [normal(gen, *s) for s in ((D, 4), (D, 3), (D,), (D, S), (N, D, S))]
+    w4, w3, b, A, h0 = f32[0], f32[1], f32[2], -f32[3].abs(), f32[4]
+    rows = io(N, 3, D)
+
+    def all_of(f):
+        out = []
+        for w, r in ((f(w4), f(rows)), (f(w3), f(rows[:, :2].contiguous()))):
+            out += gdr.conv_fwd(f(x), w, f(b), initial_state=r)
+            out += gdr.conv_bwd(f(x), w, f(d_y), f(b), initial_state=r, d_final_state=r, grad_dtype=dtype).values()
+            out += [gdr.conv_step(f(x[:, 0].contiguous()), r, w, f(b)), r]
+        kw = dict(D=f(b), z=f(z), dt_bias=f(b), dt_softplus=True)
+        a = [f(x), f(dt), f(A), f(B), f(C)]
+        out += gdr.scan_fwd(*a, initial_state=f(h0), **kw)
+        out += gdr.scan_bwd(*a, f(d_y), initial_state=f(h0), d_final_state=f(h0), grad_dtype=dtype, **kw).values()
+        st, one = f(h0.clone()), lambda t: f(t[:, 0].contiguous())
+        kw["z"] = one(z)
+        out += [gdr.scan_step(one(x), one(dt), a[2], one(B), one(C), st, **kw), st]
+        out += gdr.layer_norm_fwd(f(x), f(b), f(b))
+        _, mean, rstd = gdr.layer_norm_fwd(x)
+        out += gdr.layer_norm_bwd(f(x), f(d_y), f(mean), f(rstd), f(b), grad_dtype=dtype).values()
+        return out
+    for i, (p, q) in enumerate(zip(all_of(odd), all_of(lambda t: t.clone()))):
+        assert torch.isfinite(p).all() and torch.equal(p, q), i
