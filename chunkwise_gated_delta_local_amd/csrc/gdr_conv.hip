@@ -8,7 +8,8 @@
 // moves once, 8 or 16 bytes a lane, and a wavefront walks a run of tokens with
 // the last W - 1 rows of its channels in registers; only the W - 1 rows before
 // a run (and, backward, behind it) are read again. 65,536 tokens of 8,192 bf16
-// channels: 386 us, 5.6 TB/s (a copy of 1 GiB: 5.2).
+// channels: 385 to 400 us by the run, 5.4 to 5.6 TB/s (copies of 1 GiB: torch's
+// 5.2, one past the caches 5.9).
 #include <type_traits>
 
 #include "gdr_mixer.hpp"
@@ -18,16 +19,16 @@ namespace gdr {
 namespace {
 
 constexpr int kWaves = 4;      // wavefronts of a workgroup
-constexpr int kGroup = 4;      // rows loaded together (8: 431 us instead of 412; 2: 426)
-// Elements of a bf16 row a lane moves at once. Forward 8 (4: 575 us instead of
-// 422). Backward 4: with 8 the registers of taps, their sums and two histories
-// leave one wavefront on a SIMD (208 us instead of 165 on 16,384 tokens of 6,144
-// channels).
+constexpr int kGroup = 4;      // rows loaded together (8: 405 us instead of 385; 2: 396)
+// Elements of a bf16 row a lane moves at once. Forward 8 (4: 401 us instead of
+// 385). Backward 4: with 8 the registers of taps, their sums and two histories
+// leave one wavefront on a SIMD instead of three (150 us instead of 130 on 16,384
+// tokens of 6,144 channels).
 constexpr int kFwdV = 8, kBwdV = 4;
 
 // Tokens a wavefront walks: the longest run, up to `most`, that still makes 2048
 // wavefronts (two a SIMD); one group where there is too little work for that. Longest:
-// forward 64 (32: 422 us, 128: 422, 64: 412), backward 128 (64: 143 us, 128: 140).
+// forward 64 (32: 411 us, 128: 405, 64: 385), backward 128 (64: 133 us, 128: 130).
 int run_length(int64_t Ttot, int wavefronts, int most) {
     int run = most;
     while (run > kGroup && (Ttot + run - 1) / run * wavefronts < 2048) run /= 2;
@@ -401,7 +402,7 @@ hipError_t launch_conv_fwd(const ConvArgs& a) {
         if (!grid_fits(all * ncb, 256)) return hipErrorInvalidConfiguration;
         if (all == 0) return hipSuccess;
         const dim3 grid((unsigned)(all * ncb));
-        // (65,536 x 8,192 bf16: 386 us, 5.6 TB/s, against 413; x alone 438, y alone 404)
+        // (65,536 x 8,192 bf16: 387 us against 417; x alone 438, y alone 404)
         if (beyond_caches(2 * a.Ttot * a.p.channels * size_of(a.p.io_dtype)))
             k_conv_fwd<T, V, W, true><<<grid, 256, 0, a.stream>>>(a, ncb, ntiles, run);
         else k_conv_fwd<T, V, W, false><<<grid, 256, 0, a.stream>>>(a, ncb, ntiles, run);

@@ -200,7 +200,11 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int N, int64_t T_
 }
 
 // Whether a call moves more bytes than the last cache holds (256 MB): its rows then
-// go past the caches where that was faster.
+// go past the caches. Below, the next operator finds them there; above, hardly any
+// (us from the caches and past them, 4,096 bf16 columns):
+//   a convolution and the norm of its output    192 MB each 76, 82; 272: 125, 123; 320: 147, 135; 512: 215, 208
+//   backward, the norm and then the convolution 192 MB each 92, 97; 288: 128, 138; 408: 195, 189; 768: 308, 288
+// Rows that nothing left in the caches are 3 to 6 % faster past them from 150 MB on.
 inline bool beyond_caches(int64_t bytes) { return bytes > ((int64_t)256 << 20); }
 inline int64_t size_of(int32_t dtype) { return dtype == GDR_BF16 ? 2 : 4; }
 
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(64 * NW) void k_sum_partials(const float* __restric
 }
 
 // 16 wavefronts share the partials where there are many of them for few sums
-// (512 for 5,122, in a layer norm's backward pass of 4,001 rows: 32.8 us in all; with 4: 36.4), else 4.
+// (512 for 5,122, in a layer norm's backward pass of 4,001 rows: 33.2 us in all; with 4: 36.6), else 4.
 template <typename Out>
 hipError_t sum_partials(const float* part, int64_t P, int64_t n, Out out, hipStream_t stream) {
     if (n == 0) return hipSuccess;

@@ -1,6 +1,9 @@
 // Layer norm over rows, forward and backward (include/gdr_mixer.h). A few
 // operations an element: HBM bounds both, so a row is read once and stays in
-// registers between the statistics and the output. TPR threads share a row,
+// registers between the statistics and the output (but for the backward pass of
+// more than 12,288 columns, whose sums overflow into scratch: 208 to 584 bytes a
+// lane in bf16, 928 in fp32; 4,096 rows of 16,384 take 176 and 414 us, of 12,288
+// 104 and 127). TPR threads share a row,
 // each holding NV pieces of V = 16 bytes; rows go round the grid, the weights
 // stay in registers meanwhile, and the next row is on its way while one is
 // worked on.
@@ -302,8 +305,8 @@ hipError_t by_shape(const NormArgs& a, F f) {
 int64_t row_blocks(int64_t rows, int TPR) { return (rows + kThreads / TPR - 1) / (kThreads / TPR); }
 
 // Workgroups of the forward pass, for n that one trip each would take: four trips a
-// workgroup (2,097,152 rows of 128: 206 us, with 16 trips 223, one 249; 65,536 of
-// 4,096: 189, eight 198, one 240), and more where a launch's threads would pass 32 bits.
+// workgroup (2,097,152 rows of 128: 192 us, with 8 trips 198, 16 205, one 249; 65,536
+// of 4,096: 180, 187, 187 and 234), and more where a launch's threads would pass 32 bits.
 int64_t norm_fwd_blocks(int64_t n) {
     constexpr int64_t least = 8192, most = (int64_t)1 << 22;
     static_assert(most * kThreads < ((int64_t)1 << 32), "threads of a launch");
@@ -314,7 +317,8 @@ int64_t norm_fwd_blocks(int64_t n) {
 }  // namespace
 
 // Workgroups of the backward pass, whose partial sums are written and read once
-// more: 512, two a compute unit (16,384 x 4,096 bf16: 92 us; 256: 107, 1024: 104).
+// more: 512, two a compute unit (16,384 x 4,096 bf16: 85 us; 256: 104, 1024: 98;
+// 4,001 x 2,561 fp32: 34, 41 and 38).
 int norm_bwd_blocks(const gdr_norm_problem_t& p) {
     const int64_t n = row_blocks(p.rows, shape_of(p.io_dtype == GDR_BF16, p.cols).TPR), most = 512;
     return (int)(n < most ? n : most);

@@ -251,9 +251,11 @@ hipError_t fwd(const ScanArgs& a) {
     const int64_t whole = units_of(a.p);
     Segments sg = segments_for(whole, most, a.max_len);
     const int64_t units = whole * sg.most;
-    // 2048 wavefronts fill the card at two a SIMD (16 sequences of 512 tokens and 2,048 channels: 93 us, with twice as
-    // many 104); ragged sequences take 4096, for the longest one is a chain that the others do not shorten (13 of 4,099
-    // tokens, the longest 1,272, fp32: 90 us, with 2048 143).
+    // 2048 wavefronts fill the card at two a SIMD (16 sequences of 512 tokens and 2,048 channels: 95 us, with twice as
+    // many 105; 4 of 1,024 tokens and 32 states: 90 and 104); ragged sequences take 4096, for the longest one is a chain
+    // that the others do not shorten (13 of 4,099 tokens, the longest 1,272, fp32: 88 us, with 2048 143; 20 of 16,384,
+    // the longest 2,523: 108 and 160). Many of few states are the exception (24 of 6,000 tokens, 640 channels and 8
+    // states: 37 and 27).
     const int fill = a.max_len * a.p.num_seqs > 2 * a.Ttot ? 4096 : 2048;
     const int nw = waves_for(units, sg.most > 1 ? sg.len : a.max_len, kPiece<SPL>, fill, 1, most);
     const int64_t lines = line_units((int64_t)a.p.num_seqs * a.p.groups * sg.most, cbg), blocks = unit_blocks(lines);
@@ -288,7 +290,7 @@ hipError_t step(const ScanArgs& a) {
         const int64_t blocks = (nch + 256 / LC - 1) / (256 / LC);
         if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
         if (blocks == 0) return hipSuccess;
-        // (1,024 x 4,096 x 16: 124 us against 139; 256 x 4,096 x 16, which the caches hold: 33 against 30)
+        // (1,024 x 4,096 x 16: 126 us against 144, 520: 64 against 73; 256 of them, which the caches hold: 33 against 30)
         if (beyond_caches(8 * nch * a.p.state_dim)) k_scan_step<T, LC, WIDE, true><<<dim3((unsigned)blocks), 256, 0, a.stream>>>(a, nch);
         else k_scan_step<T, LC, WIDE, false><<<dim3((unsigned)blocks), 256, 0, a.stream>>>(a, nch);
         return hipGetLastError();

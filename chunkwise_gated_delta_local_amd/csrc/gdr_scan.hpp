@@ -64,9 +64,10 @@ __device__ __forceinline__ int by_length(const int32_t* cu, int N, int r) {
 
 // Workgroup -> (sequence, segment, group, channel block). Workgroups are dealt to
 // the eight XCDs in turn; kLine consecutive channel blocks, whose rows share
-// 128-byte lines, go to the same one, so that the lines meet in one L2. Long
-// sequences start first: 13 of 4,099 tokens, the longest 1,272, take 89 us instead
-// of 130 in their order, a run of them an XCD.
+// 128-byte lines, go to the same one, so that the lines meet in one L2 (8,192 tokens
+// of 4,096 channels and 16 states: 198 us, dealt one by one 213). Long sequences
+// start first: 13 of 4,099 tokens, the longest 1,272, take 82 us instead of 130 in
+// their order.
 constexpr int kLine = 4;
 inline int64_t line_units(int64_t seqs_segments_groups, int cbg) { return seqs_segments_groups * ((cbg + kLine - 1) / kLine); }
 inline int64_t unit_blocks(int64_t lines) { return (lines + 7) / 8 * 8 * kLine; }
@@ -360,8 +361,10 @@ __global__ __launch_bounds__(512) void k_scan_states(ScanArgs a, Segments sg, fl
 // ---------------------------------------------------------------- host
 // Segments where whole sequences leave more than half of 2048 wavefronts idle: as
 // many as fill them, of 256 tokens or more. The work of the recurrence is done
-// twice then: 16,384 tokens of 512 channels and 16 states take 94 us instead of
-// 343, 8,192 of them backward 180 instead of 749.
+// twice then: 16,384 tokens of 512 channels and 16 states take 93 us instead of
+// 345, 8,192 of them backward 175 instead of 725. Two segments: 8,192 tokens of
+// 2,048 channels 170 instead of 184, backward 654 instead of 746; near the least
+// length they cost a little forward (512 tokens 19 instead of 17, backward 64).
 constexpr int kMostSegments = 64;
 inline int most_segments(int64_t units, int nw) {
     const int64_t want = units > 0 ? 2048 / (units * nw) : 0;
@@ -395,8 +398,8 @@ template <int SPL> constexpr size_t states_lds(int nw) {
     return 4 * ((size_t)nw * (kPiece<SPL> * (kCh * 2 + 4 * SPL) + 2 * 128 * SPL) + 2 * 64 * SPL);
 }
 
-// f(states a lane). Six of them for 17 to 24 states: 4,099 tokens of 1,540 channels and 24 states take 80 us, padded to
-// 32 states 89.
+// f(states a lane). Six of them for 17 to 24 states: 4,099 tokens of 1,540 channels and 24 states take 82 us, padded to
+// 32 states 91; 4 x 2,048 tokens of 1,365 channels backward 649 and 1,202.
 template <typename F>
 auto by_state_dim(int S, F f) {
     if (S <= 8) return f(std::integral_constant<int, 2>{});

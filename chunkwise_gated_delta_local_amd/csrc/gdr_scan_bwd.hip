@@ -31,10 +31,13 @@ namespace {
 // Variants by states a lane: J channels a lane, L tokens a piece, at most NW
 // wavefronts, and at least LEAST of them where a sequence has the pieces (the
 // states before the tiles are written and read once more). The exponentials and
-// states of a piece take 2 SPL J L registers: pieces of 8 tokens at 32 states, and
-// 64 states at two wavefronts a SIMD, went to scratch (1.20 and 4.47 ms against
-// 0.61 and 1.44 with as many elements as 4 x 2,048 tokens of 2,048 channels and 16
-// states, where two channels a lane took 446 us against 427).
+// states of a piece take 2 SPL J L registers, and what does not fit goes to
+// scratch. 4 x 2,048 tokens, gated, bf16, of 4,096 channels and 8 states, 2,048 and
+// 16, 1,365 and 24, 1,024 and 32, 512 and 64: 427, 371, 649, 630 and 897 us. With one
+// channel a lane at 8 states 480, two at 16 983; pieces of 8 tokens at 24 and 32
+// states 1,112 and 1,178; 64 states at two wavefronts a SIMD 2,743. Still in scratch,
+// with a gate: 28 to 36 bytes a lane at up to 8 states (with softplus), 156 to 168 at
+// 25 to 32, 52 to 72 at 33 to 64.
 template <int SPL> struct Bwd {
     static constexpr int J = SPL <= 2 ? 2 : 1, L = SPL <= 4 ? 8 : 4, NW = SPL <= 8 ? 8 : 4, LEAST = 4;
     static constexpr int EPT = SPL * J, SP = 4 * SPL, CHB = kCh * J;

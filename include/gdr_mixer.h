@@ -91,7 +91,8 @@ gdr_status_t gdr_conv_bwd(const gdr_conv_problem_t* problem, const void* x, cons
  * exp(delta A) is meant to be at most one; a growing state may overflow where
  * pieces of a sequence are joined although its running value does not, and an
  * infinite one become NaN there. A may be -inf: a step size above zero then
- * forgets the state, one of zero keeps it.
+ * forgets the state, one of zero keeps it. An infinite delta x may give NaN in
+ * y where the sum over the state would be infinite.
  */
 typedef struct {
     int64_t batch, seq_len;
