@@ -290,7 +290,9 @@ hipError_t step(const ScanArgs& a) {
         const int64_t blocks = (nch + 256 / LC - 1) / (256 / LC);
         if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
         if (blocks == 0) return hipSuccess;
-        // (1,024 x 4,096 x 16: 126 us against 144, 520: 64 against 73; 256 of them, which the caches hold: 33 against 30)
+        // A state counts twice, read and written, since a model steps several in turn: three of 256 sequences (64 MB each)
+        // 30 us from the caches, past them 33, of 520 62 and 58, of 1,024 122 and 113. (One alone would stay in the caches
+        // up to 256 MB: 520 sequences 50 and 59, 1,024 123 and 112.)
         if (beyond_caches(8 * nch * a.p.state_dim)) k_scan_step<T, LC, WIDE, true><<<dim3((unsigned)blocks), 256, 0, a.stream>>>(a, nch);
         else k_scan_step<T, LC, WIDE, false><<<dim3((unsigned)blocks), 256, 0, a.stream>>>(a, nch);
         return hipGetLastError();
