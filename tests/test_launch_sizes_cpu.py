@@ -102,3 +102,28 @@ def test_conv_channels(launches):
         else:
             assert found and all(0 < b <= 1024 and 0 < g * b < 1 << 32 for g, b, _ in found), (op, kw, found)
             assert found[0][0] * found[0][1] * 8 >= D, (op, kw, found)     # a lane takes 8 channels at most
+
+
+def test_scan_sizes(launches):
+    """From one token to 2^30 sequences and the widest rows: a launch within HIP's limits and a compute unit's LDS, or a
+    refusal."""
+    most = (1 << 22) - 1
+    shapes = [(1, 1, 1, 1), (1, 1, most, 1), (1, 300, most, 1), (1, 1, 1 << 21, 1 << 21), (1, 65536, 4096, 1),
+              (1, (1 << 31) - 65, 16, 1), (1 << 22, 100, 64, 4), (1 << 30, 1, 1, 1), (1 << 20, 1, 4096, 2), (3, 0, 64, 1),
+              (13, 4099, 1540, 4), (2, 700, 1536, 1)]
+    calls = [(op, dict(batch=b, num_seqs=b, seq_len=1 if op == "scan_step" else t, channels=D, groups=G, state_dim=S,
+                       x_stride=D, dt_stride=D, z_stride=D, b_stride=G * S, c_stride=G * S))
+             for op in ("scan_step", "scan_bwd") for b, t, D, G in shapes for S in (1, 8, 16, 24, 32, 64) if G * S <= most]
+    refused = 0
+    for (op, kw), (status, message, found) in zip(calls, launches(calls)):
+        if status:
+            refused += 1
+            N, D, G, S = (kw[k] for k in ("batch", "channels", "groups", "state_dim"))
+            assert status == 2 and "too large" in message and not found, (op, kw, status, message)
+            # lanes of the single tokens: 4 states each, a power of two to a channel; of the tiles: at most 8 wavefronts to
+            # 16 channels, whose workgroups come in fours
+            lanes = N * D * 2 * -(-S // 4) if op == "scan_step" else N * G * -(-(D // G) // 64) * 4 * 512
+            assert lanes >= 1 << 32, (op, kw)
+        else:
+            assert found and all(0 < b <= 1024 and 0 < g * b < 1 << 32 and lds <= 160 * 1024 for g, b, lds in found), (op, kw)
+    assert 0 < refused < len(calls) / 2
