@@ -10,3 +10,4 @@ call does, and fails loudly if the library is missing.
 from .api import Forward, chunk_fwd, chunk_fwd_debug, recurrent_fwd, workspace_size, validate  # noqa: F401
 from .mixer import (conv_bwd, conv_fwd, conv_step, layer_norm_bwd, layer_norm_fwd, scan_bwd, scan_fwd,  # noqa: F401
                     scan_step)
+from .attn import window_attn_bwd, window_attn_fwd, window_attn_step  # noqa: F401

@@ -36,7 +36,9 @@ EXPORTED = ("gdr_validate", "gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd_debug
             "gdr_conv_fwd", "gdr_conv_step", "gdr_conv_bwd", "gdr_conv_bwd_workspace_size",
             "gdr_scan_fwd", "gdr_scan_fwd_workspace_size", "gdr_scan_step", "gdr_scan_bwd",
             "gdr_scan_bwd_workspace_size", "gdr_layer_norm_fwd", "gdr_layer_norm_bwd",
-            "gdr_layer_norm_bwd_workspace_size")
+            "gdr_layer_norm_bwd_workspace_size",
+            "gdr_window_attn_fwd", "gdr_window_attn_fwd_workspace_size", "gdr_window_attn_step",
+            "gdr_window_attn_step_workspace_size", "gdr_window_attn_bwd", "gdr_window_attn_bwd_workspace_size")
 
 
 class Problem(ctypes.Structure):
@@ -76,6 +78,15 @@ class NormProblem(ctypes.Structure):
                 ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class AttnProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seq_len", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim_qk", ctypes.c_int32),
+                ("head_dim_v", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("do_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
 
 
 class GdrError(RuntimeError):
@@ -129,6 +140,7 @@ def load_library():
     lib.gdr_peak_mfma_flops.argtypes = [ctypes.c_int32, ctypes.c_int32]
     lib.gdr_peak_mfma_flops.restype = ctypes.c_double
     CP, SP, NP = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(NormProblem)
+    AP = ctypes.POINTER(AttnProblem)
     Z, PZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     for name, types in (("gdr_conv_fwd", [CP] + [P] * 9), ("gdr_conv_step", [CP] + [P] * 6),
                         ("gdr_conv_bwd", [CP] + [P] * 13 + [Z, P]), ("gdr_conv_bwd_workspace_size", [CP, PZ]),
@@ -136,7 +148,10 @@ def load_library():
                         ("gdr_scan_step", [SP] + [P] * 11), ("gdr_scan_bwd", [SP] + [P] * 23 + [Z, P]),
                         ("gdr_scan_bwd_workspace_size", [SP, PZ]), ("gdr_layer_norm_fwd", [NP] + [P] * 7),
                         ("gdr_layer_norm_bwd", [NP] + [P] * 9 + [Z, P]),
-                        ("gdr_layer_norm_bwd_workspace_size", [NP, PZ])):
+                        ("gdr_layer_norm_bwd_workspace_size", [NP, PZ]),
+                        ("gdr_window_attn_fwd", [AP] + [P] * 11 + [Z, P]), ("gdr_window_attn_fwd_workspace_size", [AP, PZ]),
+                        ("gdr_window_attn_step", [AP] + [P] * 8 + [Z, P]), ("gdr_window_attn_step_workspace_size", [AP, PZ]),
+                        ("gdr_window_attn_bwd", [AP] + [P] * 12 + [Z, P]), ("gdr_window_attn_bwd_workspace_size", [AP, PZ])):
         getattr(lib, name).argtypes = types
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib

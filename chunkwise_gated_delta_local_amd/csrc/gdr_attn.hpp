@@ -1,0 +1,442 @@
+// Internal interface of the window attention (include/gdr_attn.h): launch
+// arguments, and the device building blocks that its kernels share.
+//
+// Products run on 32x32 matrix-core tiles. For lane l = 32 h + r of a wavefront
+// the operand of 32 rows holds row r, and the accumulator holds column r with
+// the rows 8 i + 4 h + j in register 4 i + j. Operand and accumulator then fit
+// without moving data between lanes: the scores are formed transposed (keys in
+// the accumulator's rows, a query in each lane's column), so that
+//  - a query's maximum and sum are a lane's own but for one exchange of halves;
+//  - the weights are the operand of the product with v as they lie, contracted
+//    over keys in the order 8 i + 4 h + j;
+//  - v enters that product by transposing LDS reads of 4 keys at a time (bf16),
+//    or by plain ones (fp32).
+// The contraction over the head dimension may run in any order that both
+// operands share: a step takes 16 bytes of each row, the half h its unit 2 t + h.
+#pragma once
+
+#include <type_traits>
+
+#include "gdr_attn.h"
+#include "gdr_mixer.hpp"
+
+namespace gdr {
+
+struct AttnArgs {
+    gdr_attn_problem_t p;
+    int64_t Ttot, max_len;     // total tokens, longest sequence (host)
+    int32_t q_ld, k_ld, v_ld;  // elements between tokens of one sequence (a single token: any)
+    const void *q, *k, *v;
+    void *kc, *vc;             // caches or NULL
+    const int32_t *lens, *cu;  // NULL: zeros; NULL: batch rows
+    void* o;
+    float* lse;
+    bool one;                  // single tokens: negative lens pass, the caches are written by the same kernel
+    bool vec;                  // rows of q, k, v and the caches in 16-byte pieces at 16-byte addresses
+    float* ws;
+    // backward
+    const void *oin, *d_o;     // d_o: as given, then in the io type
+    const float* lse_in;
+    void *dq, *dk, *dv;
+    float* rows;               // [Ttot][Nq][2]: lse log2(e), sum of d_o o
+    void* d_o16;               // d_o rounded to the io type, where it comes in fp32
+    int32_t* slots;            // [num_seqs + 1]: first slot of each sequence
+    float* sink_part;          // [slots][sinks][Nk][dk + dv]
+    int32_t max_slots, sink_run;
+    hipStream_t stream;
+};
+
+size_t attn_fwd_workspace(const gdr_attn_problem_t& p);
+hipError_t launch_attn_fwd(const AttnArgs& a);
+size_t attn_bwd_workspace(const gdr_attn_problem_t& p);
+hipError_t launch_attn_bwd(const AttnArgs& a);
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+// elements in 16 bytes
+template <typename T> constexpr int kUnit = 16 / (int)sizeof(T);
+
+// ---------------------------------------------------------------- rows of queries
+// A block of queries is TPB tokens of one sequence times HPB of the G heads that
+// share a key head: row r is token r / HPB, head r % HPB. The keys of a block are
+// read once for all its heads, and its window is little longer than one token's.
+struct RowBlock {
+    int HPB, TPB, HC;          // heads and tokens of a block, blocks to a key head's group
+};
+__host__ __device__ inline RowBlock row_block(int rows, int G) {
+    RowBlock b;
+    b.HPB = G < rows ? G : rows;
+    b.TPB = rows / b.HPB;
+    b.HC = (G + b.HPB - 1) / b.HPB;
+    return b;
+}
+// Blocks of TPB tokens: sequence n has the numbers from start / TPB + n (packed
+// sequences; some numbers stay unused) or n ceil(T / TPB) on.
+__host__ __device__ inline int64_t token_blocks(int64_t batch, int64_t T, int N, bool packed, int TPB) {
+    return packed ? T / TPB + N : batch * ((T + TPB - 1) / TPB);
+}
+
+struct Block {
+    int n, t0, tn;             // sequence, first token in it, tokens
+    int64_t start;             // the sequence's first row of q, k, v
+    int len;                   // its tokens
+};
+// Block number b of tokens; false: unused. All lanes call it alike.
+__device__ inline bool find_block(const int32_t* cu, int N, int64_t T, int64_t Ttot, int TPB, int b, Block* x) {
+    if (!cu) {
+        const int per = (int)((T + TPB - 1) / TPB);
+        x->n = b / per;
+        x->t0 = (b - x->n * per) * TPB;
+        x->start = (int64_t)x->n * T;
+        x->len = (int)T;
+    } else {
+        // the last n with cu[n] / TPB + n <= b; each lane looks at a 64th of what is left
+        int lo = 0, len = N;
+        while (len > 1) {
+            const int step = (len + 63) / 64, i = lo + (int)(threadIdx.x & 63) * step;
+            const bool before = i < lo + len && cu[i] / TPB + i <= b;
+            const int k = __popcll(__ballot(before));
+            const int at = k > 0 ? (k - 1) * step : 0;
+            len = len - at < step ? len - at : step;
+            lo += at;
+        }
+        x->n = __builtin_amdgcn_readfirstlane(lo);
+        int64_t s, e;
+        seq_range(cu, x->n, 0, Ttot, &s, &e);
+        s = __builtin_amdgcn_readfirstlane((int)s);
+        e = __builtin_amdgcn_readfirstlane((int)e);
+        x->start = s;
+        x->len = (int)(e - s);
+        const int first = (int)s / TPB + x->n;
+        if (b < first || b - first > x->len / TPB) return false;
+        x->t0 = (b - first) * TPB;
+    }
+    x->tn = x->len - x->t0 < TPB ? x->len - x->t0 : TPB;
+    return x->tn > 0;
+}
+
+// The keys that queries at positions p0 .. p1 see (behind len cached tokens), as
+// at most five runs of consecutive rows: cached sinks, two pieces of the ring, new
+// sinks, new tokens. All members are the same in every lane.
+struct Keys {
+    int n0, n1, n2, n3, n4;    // keys of the runs that are left, the present one first
+    int p0, p1, p2, p3, p4;    // their first positions
+    int r0, r1, r2, r3, r4;    // and rows
+    int old;                   // runs among them that lie in the cache
+
+    __device__ Keys(int first, int last, int len, int W, int S) : old(3) {
+        const int end = last + 1, lo = first - W + 1 > S ? first - W + 1 : S;
+        p0 = r0 = 0;
+        n0 = len < S ? len : S;
+        p1 = lo;
+        n1 = n2 = 0;
+        r1 = r2 = S;
+        if (lo < len) {
+            const int n = len - lo, w = (lo - S) % W;
+            n1 = n < W - w ? n : W - w;
+            n2 = n - n1;
+            r1 = S + w;
+            if (lo == S) {                       // the ring goes on behind the sinks (and has not turned)
+                n0 += n1;
+                n1 = 0;
+            }
+        }
+        p2 = p1 + n1;
+        const int sink_end = S < end ? S : end;
+        p3 = len;
+        n3 = len < sink_end ? sink_end - len : 0;
+        p4 = lo > len ? lo : len;
+        n4 = end > p4 ? end - p4 : 0;
+        if (n3 > 0 && p4 == len + n3) {
+            n3 += n4;
+            n4 = 0;
+        }
+        r3 = 0;
+        r4 = p4 - len;
+    }
+    __device__ int total() const { return n0 + n1 + n2 + n3 + n4; }
+    __device__ void drop() {
+        n0 = n1; n1 = n2; n2 = n3; n3 = n4; n4 = 0;
+        p0 = p1; p1 = p2; p2 = p3; p3 = p4;
+        r0 = r1; r1 = r2; r2 = r3; r3 = r4;
+        --old;
+    }
+    __device__ void cut(int n) {
+        n0 -= n;
+        p0 += n;
+        r0 += n;
+    }
+    // moves n <= total() keys on
+    __device__ void skip(int n) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            if (n >= n0) {
+                n -= n0;
+                drop();
+            }
+        cut(n);
+    }
+    // the next tile of at most n keys: its first position, keys, first row, whether cached; 0 keys: the end
+    __device__ void next(int n, int* pos, int* cnt, int* row, bool* cached) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 == 0) drop();
+        *cnt = n0 < n ? n0 : n;
+        *pos = p0;
+        *row = r0;
+        *cached = old > 0;
+        cut(*cnt);
+    }
+};
+
+// ---------------------------------------------------------------- tiles
+// Rows of D elements in LDS, in 16-byte units; unit u of row lies at u ^ swz(row),
+// so that neither 8 rows' reads of one unit nor a transposing read of 4 rows meet
+// in the banks.
+__device__ __forceinline__ int swz(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
+
+// A row's operand for a contraction over the head dimension
+template <typename T> struct Frag;
+template <> struct Frag<bf16> {
+    typedef Vec<bf16>::v8 type;
+};
+template <> struct Frag<float> {
+    typedef f32x4 type;
+};
+template <typename T> using frag_t = typename Frag<T>::type;
+
+__device__ __forceinline__ f32x16 mma(const Vec<bf16>::v8& a, const Vec<bf16>::v8& b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(const f32x4& a, const f32x4& b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+
+// row r0 + lane % 32, step t
+template <typename T, int D>
+__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t) {
+    const int lane = threadIdx.x & 63, row = r0 + (lane & 31);
+    return *reinterpret_cast<const frag_t<T>*>(tile + row * D + ((2 * t + (lane >> 5)) ^ swz(row)) * kUnit<T>);
+}
+// Operand of the transpose: row d0 + lane % 32 (a column of the tile), contracted
+// over the 16 tile rows r0 + 8 i + 4 h + j, i < 2
+template <int D>
+__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int d0) {
+    typedef __attribute__((address_space(3))) s16x4* lds_p;
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    const int unit = (d0 + (lane & 16)) / 8 + (l >> 1 & 1);
+    s16x4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = r0 + 8 * i + 4 * (lane >> 5) + (l >> 2);
+        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(tile + row * D + (unit ^ swz(row)) * 8 + 4 * (l & 1)));
+    }
+    return __builtin_bit_cast(Vec<bf16>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int D>
+__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int d0) {
+    const int lane = threadIdx.x & 63, d = d0 + (lane & 31);
+    Vec<float>::v8 x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = r0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+        x[i] = tile[row * D + ((d >> 2) ^ swz(row)) * 4 + (d & 3)];
+    }
+    return x;
+}
+__device__ __forceinline__ f32x16 mma(const Vec<float>::v8& a, const Vec<float>::v8& b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+// rows 16 q .. 16 q + 15 of an accumulator as the other operand of that contraction
+template <typename T>
+__device__ __forceinline__ typename Vec<T>::v8 acc_frag(const f32x16& s, int q) {
+    typename Vec<T>::v8 x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_t<T>(s[8 * q + e]);
+    return x;
+}
+
+// 16 bytes of a row through a range-checked buffer, zero from element d on; VEC:
+// rows begin and end at 16-byte addresses
+template <typename T, bool VEC>
+__device__ __forceinline__ u32x4 load_unit(__amdgpu_buffer_rsrc_t rs, int row_bytes, int unit, int d) {
+    constexpr int out = 0x7ffffff0;                          // behind every buffer
+    if constexpr (VEC) {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rs, unit * kUnit<T> < d ? row_bytes + unit * 16 : out, 0, 0));
+    } else if constexpr (sizeof(T) == 4) {
+        u32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, unit * 4 + e < d ? row_bytes + unit * 16 + 4 * e : out, 0, 0);
+        return x;
+    } else {
+        u32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                    rs, unit * 8 + 2 * e + i < d ? row_bytes + unit * 16 + 4 * e + 2 * i : out, 0, 0);
+            x[e] = v[0] | v[1] << 16;
+        }
+        return x;
+    }
+}
+// the same of a row in memory (`live`: its address is valid)
+template <typename T, bool VEC>
+__device__ __forceinline__ frag_t<T> load_frag_row(const T* row, int unit, int d, bool live) {
+    frag_t<T> x;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; ++e) x[e] = to_t<T>(0.f);
+        if (live && unit * kUnit<T> < d) x = *reinterpret_cast<const frag_t<T>*>(row + unit * kUnit<T>);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; ++e) {
+            const int c = unit * kUnit<T> + e;
+            x[e] = live && c < d ? row[c] : to_t<T>(0.f);
+        }
+    }
+    return x;
+}
+
+// `rows` rows of a tile on their way from memory to LDS through the registers of NT
+// threads; the copy is not waited for before it is stored.
+template <typename T, int D, int ROWS, int NT, bool VEC>
+struct Stage {
+    static constexpr int UN = D / kUnit<T>, N = ROWS * UN / NT;
+    static_assert(ROWS * UN % NT == 0, "whole units a thread");
+    u32x4 x[N];
+    // row_at(row): its bytes behind base, of which `bytes` are valid
+    template <typename F>
+    __device__ __forceinline__ void load(const T* base, uint32_t bytes, F row_at, int d, int tid) {
+        const auto rs = buf_rsrc(base, bytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz(row);
+            x[i] = load_unit<T, VEC>(rs, row_at(row), unit, d);
+        }
+    }
+    __device__ __forceinline__ void load(const T* base, int ld, int rows, int d, int tid) {
+        const uint32_t row_bytes = (uint32_t)ld * sizeof(T);
+        load(base, rows > 0 ? (rows - 1) * row_bytes + d * (uint32_t)sizeof(T) : 0,
+             [&](int row) { return row * (int)row_bytes; }, d, tid);
+    }
+    __device__ __forceinline__ void store(T* tile, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (tid + i * NT) * kUnit<T>) = x[i];
+    }
+};
+
+// over the two lanes of a column
+__device__ __forceinline__ float pair_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Which of a tile's keys a lane's query sees.
+struct Sight {
+    int pos0, cnt, p, W, S;
+    __device__ bool operator()(int key) const {
+        const int pos = pos0 + key;
+        return key < cnt && pos <= p && (pos < S || pos > p - W);
+    }
+};
+
+// ---------------------------------------------------------------- shared set-up
+// A wavefront's 32 rows of a block: the lane's row, its query's place and position.
+struct Query {
+    bool live;
+    int64_t token;             // row of q and o
+    int head, p;               // head of q; position in the sequence
+};
+__device__ __forceinline__ Query query_of(const Block& b, const RowBlock& rb, int G, int hk, int hc, int r, int len) {
+    const int t = r / rb.HPB, g = hc * rb.HPB + r % rb.HPB;
+    Query q;
+    q.live = t < b.tn && t < rb.TPB && g < G;
+    const int tc = t < b.tn ? t : b.tn - 1;            // rows behind the block follow its last token
+    q.token = b.start + b.t0 + tc;
+    q.head = hk * G + (g < G ? g : G - 1);
+    q.p = len + b.t0 + tc;
+    return q;
+}
+__device__ __forceinline__ int past_len(const AttnArgs& a, int n) {
+    if (!a.lens) return 0;
+    const int len = __builtin_amdgcn_readfirstlane(a.lens[n]), most = 0x7fffffff - 64 - (int)a.p.seq_len;
+    return len < 0 ? 0 : len < most ? len : most;
+}
+
+template <typename T>
+struct Source {                // where a tile's keys and values begin
+    const T *k, *v;
+    int kld, vld;
+};
+template <typename T>
+__device__ __forceinline__ Source<T> source(const AttnArgs& a, const Block& b, int hk, int row, bool cached) {
+    const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v, Nk = a.p.num_kv_heads;
+    Source<T> s;
+    if (cached) {
+        const int64_t at = (int64_t)b.n * ((int64_t)a.p.sinks + a.p.window) + row;
+        s.k = (const T*)a.kc + (at * Nk + hk) * dk;
+        s.v = (const T*)a.vc + (at * Nk + hk) * dv;
+        s.kld = Nk * dk;
+        s.vld = Nk * dv;
+    } else {
+        const int64_t at = b.start * (a.one ? 0 : 1);
+        s.k = (const T*)a.k + (a.one ? b.n * a.p.k_stride : (at + row) * a.p.k_stride) + hk * dk;
+        s.v = (const T*)a.v + (a.one ? b.n * a.p.v_stride : (at + row) * a.p.v_stride) + hk * dv;
+        s.kld = a.k_ld;
+        s.vld = a.v_ld;
+    }
+    return s;
+}
+
+// Four consecutive outputs d .. d + 3 of a row
+template <typename OT>
+__device__ __forceinline__ void store4(OT* row, int d, int dv, const float (&y)[4]) {
+    if (d + 4 <= dv) {
+        store_vec<OT, 4>(row + d, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (d + j < dv) row[d + j] = to_t<OT>(y[j]);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+inline int group(const gdr_attn_problem_t& p) { return p.num_q_heads / p.num_kv_heads; }
+
+// f(io type, DK, DV)
+template <typename F>
+void by_dims(const gdr_attn_problem_t& p, F f) {
+    auto go = [&](auto type) {
+        typedef std::integral_constant<int, 64> d64;
+        typedef std::integral_constant<int, 128> d128;
+        if (p.head_dim_qk <= 64) p.head_dim_v <= 64 ? f(type, d64{}, d64{}) : f(type, d64{}, d128{});
+        else p.head_dim_v <= 64 ? f(type, d128{}, d64{}) : f(type, d128{}, d128{});
+    };
+    p.io_dtype == GDR_BF16 ? go(bf16{}) : go(float{});
+}
+
+}  // namespace gdr

@@ -1,0 +1,471 @@
+// Window attention, backward (include/gdr_attn.h; tile conventions in gdr_attn.hpp).
+//
+//   P_pj = exp(s_pj - lse_p),  dP = d_o v^T,  dS = P (dP - delta),  delta_p = d_o_p . o_p
+//   dq = scale dS k,  dk = scale dS^T q,  dv = P^T d_o
+//
+// The scores are formed again, twice: k_window_dq walks the keys of a block of
+// queries, k_window_dkv the queries of a block of keys, each summing what it
+// owns in registers, so that no sum crosses workgroups and its order is fixed.
+// The first tokens alone are seen by queries of the whole sequence: those behind
+// the ones that a key block meets anyway are shared out in runs of sink_run tokens,
+// whose sums go to slots in memory and are added up by k_window_sinks.
+#include "gdr_attn.hpp"
+
+namespace gdr {
+
+namespace {
+
+// ---------------------------------------------------------------- per row: lse and delta
+// 16 lanes a row of up to 128 elements. The last workgroup counts the slots instead.
+template <typename T>
+__global__ __launch_bounds__(256) void k_window_rows_prep(AttnArgs a, int key_block) {
+    if (blockIdx.x == gridDim.x - 1) {
+        if (threadIdx.x >= 64 || !a.slots) return;
+        int base = 0;
+        for (int n0 = 0; n0 <= a.p.num_seqs; n0 += 64) {
+            const int n = n0 + (int)threadIdx.x;
+            int m = 0;
+            if (n < a.p.num_seqs) {
+                int64_t s, e;
+                seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+                // tokens behind all that the sinks' key blocks meet, in runs; and a slot for those blocks' own sums
+                const int64_t behind = e - s - a.p.window;
+                if (behind > 0) m = (int)((behind + a.sink_run - 1) / a.sink_run) + 1;
+            }
+            int sum = m;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int x = __shfl_up(sum, d, 64);
+                if ((int)threadIdx.x >= d) sum += x;
+            }
+            const int first = base + sum - m;
+            if (n <= a.p.num_seqs) a.slots[n] = first < a.max_slots ? first : a.max_slots;
+            base += __shfl(sum, 63, 64);
+        }
+        return;
+    }
+    const int l = threadIdx.x & 15, dv = a.p.head_dim_v;
+    const int64_t rows = a.Ttot * a.p.num_q_heads, step = (int64_t)(gridDim.x - 1) * 16;
+    for (int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); r < rows; r += step) {
+        const int o32 = a.p.out_dtype == GDR_F32, g32 = a.p.do_dtype == GDR_F32;
+        float s = 0.f;
+        if (8 * l + 8 <= dv) {
+            float o[8], g[8];
+            load_vec_as<T, 8>(a.oin, r * dv + 8 * l, o32, o);
+            load_vec_as<T, 8>(a.d_o, r * dv + 8 * l, g32, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(o[i], g[i], s);
+            if (a.d_o16) store_vec<T, 8>((T*)a.d_o16 + r * dv + 8 * l, g);
+        } else {
+            for (int i = 8 * l; i < dv; ++i) {
+                const float g = load_as<T>(a.d_o, r * dv + i, g32);
+                s = __builtin_fmaf(load_as<T>(a.oin, r * dv + i, o32), g, s);
+                if (a.d_o16) ((T*)a.d_o16)[r * dv + i] = to_t<T>(g);
+            }
+        }
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m, 64);
+        if (l == 0) {
+            a.rows[2 * r] = a.lse_in[r] * kLog2e;
+            a.rows[2 * r + 1] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dq
+template <typename T, int DK, int DV, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
+    constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = KT / 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
+    __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK];
+    __shared__ __attribute__((aligned(16))) T Vs[2][KT * DV];
+    const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
+    const int hh = id / nblk, G = a.p.num_q_heads / a.p.num_kv_heads, hk = hh / rb.HC, hc = hh % rb.HC;
+    Block b;
+    if (!find_block(a.cu, a.p.num_seqs, a.p.seq_len, a.Ttot, rb.TPB, id % nblk, &b)) return;
+    const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, h = lane >> 5;
+    const int W = a.p.window, S = a.p.sinks, dk = a.p.head_dim_qk, dv = a.p.head_dim_v;
+    const Query q = query_of(b, rb, G, hk, hc, 32 * w + (lane & 31), 0);
+    const int pa = __builtin_amdgcn_readlane(q.p, 0), pb = __builtin_amdgcn_readlane(q.p, 31);
+    const int64_t row = q.token * a.p.num_q_heads + q.head;
+    frag_t<T> qf[KF], gf[VF];
+#pragma unroll
+    for (int t = 0; t < KF; ++t)
+        qf[t] = load_frag_row<T, VEC>((const T*)a.q + q.token * a.p.q_stride + (int64_t)q.head * dk, 2 * t + h, dk, q.live);
+#pragma unroll
+    for (int t = 0; t < VF; ++t) gf[t] = load_frag_row<T, VEC>((const T*)a.d_o + row * dv, 2 * t + h, dv, q.live);
+    const float lse = a.rows[2 * row], delta = a.rows[2 * row + 1], c = a.p.scale * kLog2e;
+    f32x16 acc[DK / 32];
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t) acc[t] = zero16();
+
+    Keys keys(b.t0, b.t0 + b.tn - 1, 0, W, S);
+    Stage<T, DK, KT, 64 * NW, VEC> sk;
+    Stage<T, DV, KT, 64 * NW, VEC> sv;
+    int pos, cnt, at;
+    bool cached;
+    auto fetch = [&] {
+        keys.next(KT, &pos, &cnt, &at, &cached);
+        if (cnt == 0) return;
+        const Source<T> s = source<T>(a, b, hk, at, false);
+        sk.load(s.k, s.kld, cnt, dk, tid);
+        sv.load(s.v, s.vld, cnt, dv, tid);
+    };
+    fetch();
+    sk.store(Ks[0], tid);
+    sv.store(Vs[0], tid);
+    __syncthreads();
+    for (int cur = 0; cnt > 0; cur ^= 1) {
+        const int pos0 = pos, n = cnt;
+        fetch();
+        if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
+            const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
+            const Sight sees{pos0, n, q.p, W, S};
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                f32x16 s = zero16(), g = zero16();
+#pragma unroll
+                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(Ks[cur], 32 * k, t), qf[t], s);
+#pragma unroll
+                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(Vs[cur], 32 * k, t), gf[t], g);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
+                if (partial) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = sees(32 * k + 8 * (i >> 2) + 4 * h + (i & 3)) ? s[i] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const auto x = acc_frag<T>(s, e);
+#pragma unroll
+                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(Ks[cur], 32 * k + 16 * e, 32 * t), x, acc[t]);
+                }
+            }
+        }
+        if (cnt > 0) {
+            sk.store(Ks[cur ^ 1], tid);
+            sv.store(Vs[cur ^ 1], tid);
+        }
+        __syncthreads();
+    }
+    if (!q.live) return;
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = acc[t][4 * i + j] * a.p.scale;
+            const int d = 32 * t + 8 * i + 4 * h;
+            if (a.p.grad_dtype == GDR_F32) store4((float*)a.dq + row * dk, d, dk, y);
+            else store4((T*)a.dq + row * dk, d, dk, y);
+        }
+}
+
+// ---------------------------------------------------------------- dk, dv
+// A wavefront owns 32 keys (a lane a key), with their k and v as operands and the
+// sums of dk and dv in registers; the queries' tiles go through LDS. Work numbers
+// from `main` on are the runs of queries that see sinks alone.
+template <typename T, int DK, int DV, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, 1) void k_window_dkv(AttnArgs a, RowBlock rb, int nblk, int main, int nwork) {
+    constexpr int QT = sizeof(T) == 2 ? 64 : 32, KB = 32 * NW, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
+    __shared__ __attribute__((aligned(16))) T Qs[2][QT * DK];
+    __shared__ __attribute__((aligned(16))) T Gs[2][QT * DV];
+    __shared__ __attribute__((aligned(16))) float Rs[2][2][QT];
+    const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
+    const int Nk = a.p.num_kv_heads, G = a.p.num_q_heads / Nk, W = a.p.window, S = a.p.sinks;
+    const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
+    Block b;
+    int hk, slot, ta, te, keys;                // tokens [ta, te) of the sequence, keys from b.t0 on
+    if (id < main) {
+        hk = id / nblk;
+        if (!find_block(a.cu, a.p.num_seqs, a.p.seq_len, a.Ttot, KB, id % nblk, &b)) return;
+        keys = b.tn;
+        ta = b.t0;
+        const int64_t end = (int64_t)b.t0 + b.tn - 1 + W;
+        te = end < b.len ? (int)end : b.len;
+        slot = b.t0 < S && a.slots && a.slots[b.n + 1] > a.slots[b.n] ? a.slots[b.n] : -1;
+    } else {
+        const int sb = (S + KB - 1) / KB, i = id - main, u = i / (Nk * sb);
+        hk = i / sb % Nk;
+        // the sequence whose slots hold u
+        int lo = 0, len = a.p.num_seqs;
+        while (len > 1) {
+            const int step = (len + 63) / 64, at = lo + lane * step;
+            const bool before = at < lo + len && a.slots[at] <= u;
+            const int k = __popcll(__ballot(before)), x = k > 0 ? (k - 1) * step : 0;
+            len = len - x < step ? len - x : step;
+            lo += x;
+        }
+        b.n = __builtin_amdgcn_readfirstlane(lo);
+        const int run = u - a.slots[b.n];
+        if (run < 1 || u >= a.slots[b.n + 1]) return;
+        int64_t s, e;
+        seq_range(a.cu, b.n, a.p.seq_len, a.Ttot, &s, &e);
+        b.start = s;
+        b.len = (int)(e - s);
+        b.t0 = i % sb * KB;
+        keys = S - b.t0 < KB ? S - b.t0 : KB;
+        keys = b.len - b.t0 < keys ? b.len - b.t0 : keys;
+        // the key block's own run ends where its last key's window does
+        const int own = (b.len - b.t0 < KB ? b.len - b.t0 : KB);
+        const int64_t from = (int64_t)b.t0 + own - 1 + W, first = W + (int64_t)(run - 1) * a.sink_run;
+        int64_t x = first > from ? first : from, y = first + a.sink_run;
+        // the last run takes what is left; all runs begin behind the first window
+        x = x < b.len ? x : b.len;
+        y = y < b.len ? y : b.len;
+        ta = (int)x;
+        te = y > x ? (int)y : (int)x;
+        slot = u;
+    }
+    const int mine = b.t0 + 32 * w + (lane & 31);                  // the lane's key
+    const int ja = b.t0 + 32 * w, jb = ja + 31 < b.t0 + keys - 1 ? ja + 31 : b.t0 + keys - 1;
+    const bool live = mine < b.t0 + keys;
+    const float c = a.p.scale * kLog2e;
+    frag_t<T> kf[KF], vf[VF];
+    {
+        const int64_t tok = b.start + (live ? mine : b.t0);
+#pragma unroll
+        for (int t = 0; t < KF; ++t)
+            kf[t] = load_frag_row<T, VEC>((const T*)a.k + tok * a.p.k_stride + (int64_t)hk * dk, 2 * t + h, dk, live);
+#pragma unroll
+        for (int t = 0; t < VF; ++t)
+            vf[t] = load_frag_row<T, VEC>((const T*)a.v + tok * a.p.v_stride + (int64_t)hk * dv, 2 * t + h, dv, live);
+    }
+    f32x16 dK[DK / 32], dV[DV / 32];
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t) dK[t] = zero16();
+#pragma unroll
+    for (int t = 0; t < DV / 32; ++t) dV[t] = zero16();
+
+    // row r of a tile: token r / HPB, head r % HPB
+    const int magic = (65536 + rb.HPB - 1) / rb.HPB;               // r / HPB = r magic / 65536 for r < 256
+    const int span = rb.HPB * rb.TPB;
+    Stage<T, DK, QT, 64 * NW, VEC> sq;
+    Stage<T, DV, QT, 64 * NW, VEC> sg;
+    float r0 = 0.f, r1 = 0.f;
+    int t = ta, hc = 0, t_now = ta, n_now = 0;
+    bool more = true;
+    auto fetch = [&] {
+        more = t < te;
+        if (!more) return;
+        const int n = te - t < rb.TPB ? te - t : rb.TPB, heads = G - hc * rb.HPB < rb.HPB ? G - hc * rb.HPB : rb.HPB;
+        const int64_t tok = b.start + t;
+        const int head = hk * G + hc * rb.HPB;
+        constexpr int out = 0x7ffffff0;
+        const int q_ld = a.q_ld, g_ld = a.p.num_q_heads * dv;
+        sq.load((const T*)a.q + tok * a.p.q_stride + (int64_t)head * dk,
+                (uint32_t)((n - 1) * q_ld + heads * dk) * sizeof(T), [&](int r) {
+                    const int x = (r * magic) >> 16, g = r - x * rb.HPB;
+                    return r < span && x < n && g < heads ? (x * q_ld + g * dk) * (int)sizeof(T) : out;
+                }, dk, tid);
+        sg.load((const T*)a.d_o + (tok * a.p.num_q_heads + head) * dv,
+                (uint32_t)((n - 1) * g_ld + heads * dv) * sizeof(T), [&](int r) {
+                    const int x = (r * magic) >> 16, g = r - x * rb.HPB;
+                    return r < span && x < n && g < heads ? (x * g_ld + g * dv) * (int)sizeof(T) : out;
+                }, dv, tid);
+        if (tid < QT) {
+            const int x = (tid * magic) >> 16, g = tid - x * rb.HPB;
+            const bool in = tid < span && x < n && g < heads;
+            const float* p = a.rows + 2 * ((tok + (in ? x : 0)) * a.p.num_q_heads + head + (in ? g : 0));
+            r0 = in ? p[0] : __builtin_inff();                     // a row that is not there weighs nothing
+            r1 = in ? p[1] : 0.f;
+        }
+        t_now = t;
+        n_now = n;
+        if (++hc == rb.HC) {
+            hc = 0;
+            t += rb.TPB;
+        }
+    };
+    auto put = [&](int buf) {
+        sq.store(Qs[buf], tid);
+        sg.store(Gs[buf], tid);
+        if (tid < QT) {
+            Rs[buf][0][tid] = r0;
+            Rs[buf][1][tid] = r1;
+        }
+    };
+    fetch();
+    if (more) put(0);
+    __syncthreads();
+    for (int cur = 0; more; cur ^= 1) {
+        const int p0 = t_now, p1 = t_now + n_now - 1;
+        fetch();
+        if (ja <= jb && p1 >= ja && (ja < S || p0 <= jb + (int64_t)W - 1)) {
+            const bool partial = p0 < jb || (p1 - W >= ja && jb >= S);
+#pragma unroll
+            for (int k = 0; k < QT / 32; ++k) {
+                f32x16 s = zero16(), g = zero16();
+#pragma unroll
+                for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Qs[cur], 32 * k, u), kf[u], s);
+#pragma unroll
+                for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gs[cur], 32 * k, u), vf[u], g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 L = *reinterpret_cast<const f32x4*>(&Rs[cur][0][32 * k + 8 * i + 4 * h]);
+                    const f32x4 D = *reinterpret_cast<const f32x4*>(&Rs[cur][1][32 * k + 8 * i + 4 * h]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
+                        s[4 * i + j] = p;
+                        g[4 * i + j] = p * (g[4 * i + j] - D[j]);
+                    }
+                }
+                if (partial) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 32 * k + 8 * (i >> 2) + 4 * h + (i & 3), p = p0 + ((r * magic) >> 16);
+                        const bool see = p >= mine && (mine < S || p - mine < W);
+                        s[i] = see ? s[i] : 0.f;
+                        g[i] = see ? g[i] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const auto x = acc_frag<T>(s, e), y = acc_frag<T>(g, e);
+#pragma unroll
+                    for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gs[cur], 32 * k + 16 * e, 32 * u), x, dV[u]);
+#pragma unroll
+                    for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Qs[cur], 32 * k + 16 * e, 32 * u), y, dK[u]);
+                }
+            }
+        }
+        if (more) put(cur ^ 1);
+        __syncthreads();
+    }
+    if (!live) return;
+    const bool to_slot = slot >= 0 && mine < S;
+    float* part = to_slot ? a.sink_part + (((int64_t)slot * S + mine) * Nk + hk) * (dk + dv) : nullptr;
+    const int64_t row = (b.start + mine) * Nk + hk;
+#pragma unroll
+    for (int u = 0; u < DK / 32; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = dK[u][4 * i + j] * a.p.scale;
+            const int d = 32 * u + 8 * i + 4 * h;
+            if (to_slot) store4(part, d, dk, y);
+            else if (a.p.grad_dtype == GDR_F32) store4((float*)a.dk + row * dk, d, dk, y);
+            else store4((T*)a.dk + row * dk, d, dk, y);
+        }
+#pragma unroll
+    for (int u = 0; u < DV / 32; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = dV[u][4 * i + j];
+            const int d = 32 * u + 8 * i + 4 * h;
+            if (to_slot) store4(part + dk, d, dv, y);
+            else if (a.p.grad_dtype == GDR_F32) store4((float*)a.dv + row * dv, d, dv, y);
+            else store4((T*)a.dv + row * dv, d, dv, y);
+        }
+}
+
+// ---------------------------------------------------------------- sums of the sinks' slots
+// Workgroups (slot, key head); those of a sequence's first slot add up its slots in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_window_sinks(AttnArgs a) {
+    const int Nk = a.p.num_kv_heads, u = blockIdx.x / Nk, hk = blockIdx.x % Nk, S = a.p.sinks;
+    int lo = 0, len = a.p.num_seqs;
+    while (len > 1) {
+        const int step = (len + 63) / 64, at = lo + (int)(threadIdx.x & 63) * step;
+        const bool before = at < lo + len && a.slots[at] <= u;
+        const int k = __popcll(__ballot(before)), x = k > 0 ? (k - 1) * step : 0;
+        len = len - x < step ? len - x : step;
+        lo += x;
+    }
+    const int n = __builtin_amdgcn_readfirstlane(lo), first = a.slots[n], end = a.slots[n + 1];
+    if (u != first || u >= end) return;
+    int64_t s, e;
+    seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+    const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v, d = dk + dv;
+    const int rows = S < e - s ? S : (int)(e - s);
+    const int64_t step = (int64_t)S * Nk * d;
+    for (int64_t i = threadIdx.x; i < (int64_t)rows * d; i += 256) {
+        const int j = (int)(i / d), x = (int)(i % d);
+        const float* p = a.sink_part + (((int64_t)first * S + j) * Nk + hk) * d + x;
+        float sum = 0.f;
+        for (int k = first; k < end; ++k, p += step) sum += *p;
+        const int64_t row = (s + j) * Nk + hk;
+        if (x < dk) store_as<T>(a.dk, row * dk + x, sum, a.p.grad_dtype == GDR_F32);
+        else store_as<T>(a.dv, row * dv + x - dk, sum, a.p.grad_dtype == GDR_F32);
+    }
+}
+
+struct Plan {
+    int run;                   // queries of a slot
+    int64_t slots;
+    size_t rows, d_o16, table, part;   // bytes
+};
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+Plan plan_of(const gdr_attn_problem_t& p) {
+    Plan x{};
+    const int64_t T = p.batch * p.seq_len, W = p.window;
+    x.rows = up((size_t)T * p.num_q_heads * 8);
+    if (p.do_dtype != p.io_dtype) x.d_o16 = up((size_t)T * p.num_q_heads * p.head_dim_v * size_of(p.io_dtype));
+    x.run = (int)(W < 512 ? 512 : W < 4096 ? W : 4096);
+    if (p.sinks > 0 && T > W) {
+        const int64_t longer = T / (W + 1);                        // sequences that can be longer than a window
+        x.slots = T / x.run + 2 * (longer < p.num_seqs ? longer : p.num_seqs) + 1;
+        x.table = up(((size_t)p.num_seqs + 1) * 4);
+        x.part = up((size_t)x.slots * p.sinks * p.num_kv_heads * (p.head_dim_qk + p.head_dim_v) * 4);
+    }
+    return x;
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace(const gdr_attn_problem_t& p) {
+    const Plan x = plan_of(p);
+    return x.rows + x.d_o16 + x.table + x.part;
+}
+
+hipError_t launch_attn_bwd(const AttnArgs& in) {
+    AttnArgs a = in;
+    if (a.Ttot == 0) return hipSuccess;
+    const Plan x = plan_of(a.p);
+    char* ws = reinterpret_cast<char*>(a.ws);
+    a.rows = reinterpret_cast<float*>(ws);
+    a.d_o16 = x.d_o16 ? ws + x.rows : nullptr;
+    a.slots = x.slots ? reinterpret_cast<int32_t*>(ws + x.rows + x.d_o16) : nullptr;
+    a.sink_part = x.slots ? reinterpret_cast<float*>(ws + x.rows + x.d_o16 + x.table) : nullptr;
+    a.max_slots = (int32_t)x.slots;
+    a.sink_run = x.run;
+    const int G = group(a.p), Nk = a.p.num_kv_heads;
+    const bool packed = a.cu != nullptr;
+    hipError_t e = hipSuccess;
+    by_dims(a.p, [&](auto type, auto dk, auto dv) {
+        typedef decltype(type) T;
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NQ = 8, NK = 4, KB = 32 * NK;
+        constexpr int QT = sizeof(T) == 2 ? 64 : 32;
+        const RowBlock rq = row_block(32 * NQ, G), rk = row_block(QT, G);
+        const int64_t bq = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, rq.TPB), wq = bq * Nk * rq.HC;
+        const int64_t bk = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, KB), wm = bk * Nk;
+        const int64_t wk = wm + x.slots * Nk * ((a.p.sinks + KB - 1) / KB);
+        if (wq >= (int64_t)1 << 31 || wk >= (int64_t)1 << 31 || !grid_fits(wq + 8, 64 * NQ) || !grid_fits(wk + 8, 64 * NK)) {
+            e = hipErrorInvalidConfiguration;
+            return;
+        }
+        const int64_t rows = (a.Ttot * a.p.num_q_heads + 15) / 16, most = 8192;
+        k_window_rows_prep<T><<<dim3((unsigned)((rows < most ? rows : most) + 1)), 256, 0, a.stream>>>(a, KB);
+        if (a.d_o16) a.d_o = a.d_o16;
+        const dim3 gq((unsigned)((wq + 7) / 8 * 8)), gk((unsigned)((wk + 7) / 8 * 8));
+        auto go = [&](auto vec) {
+            constexpr bool VEC = decltype(vec)::value;
+            k_window_dkv<T, DK, DV, NK, VEC><<<gk, 64 * NK, 0, a.stream>>>(a, rk, (int)bk, (int)wm, (int)wk);
+            k_window_dq<T, DK, DV, NQ, VEC><<<gq, 64 * NQ, 0, a.stream>>>(a, rq, (int)bq, (int)wq);
+        };
+        a.vec ? go(std::true_type{}) : go(std::false_type{});
+        if (x.slots) k_window_sinks<T><<<dim3((unsigned)(x.slots * Nk)), 256, 0, a.stream>>>(a);
+        e = hipGetLastError();
+    });
+    return e;
+}
+
+}  // namespace gdr
