@@ -37,6 +37,8 @@ EXPORTED = ("gdr_validate", "gdr_chunk_fwd_workspace_size", "gdr_chunk_fwd_debug
             "gdr_scan_fwd", "gdr_scan_fwd_workspace_size", "gdr_scan_step", "gdr_scan_bwd",
             "gdr_scan_bwd_workspace_size", "gdr_layer_norm_fwd", "gdr_layer_norm_bwd",
             "gdr_layer_norm_bwd_workspace_size",
+            "gdr_gated_norm_fwd", "gdr_gated_norm_bwd", "gdr_gated_norm_bwd_workspace_size", "gdr_residual_norm_fwd",
+            "gdr_residual_norm_bwd", "gdr_residual_norm_bwd_workspace_size",
             "gdr_window_attn_fwd", "gdr_window_attn_fwd_workspace_size", "gdr_window_attn_step",
             "gdr_window_attn_step_workspace_size", "gdr_window_attn_bwd", "gdr_window_attn_bwd_workspace_size")
 
@@ -78,6 +80,22 @@ class NormProblem(ctypes.Structure):
                 ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class GatedNormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("cols", ctypes.c_int32), ("eps", ctypes.c_float), ("activation", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("dy_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class ResidualNormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("cols", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("gate", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("dy_dtype", ctypes.c_int32), ("dh_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("dres_dtype", ctypes.c_int32)]
 
 
 class AttnProblem(ctypes.Structure):
@@ -140,7 +158,7 @@ def load_library():
     lib.gdr_peak_mfma_flops.argtypes = [ctypes.c_int32, ctypes.c_int32]
     lib.gdr_peak_mfma_flops.restype = ctypes.c_double
     CP, SP, NP = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(NormProblem)
-    AP = ctypes.POINTER(AttnProblem)
+    AP, GP, RP = (ctypes.POINTER(t) for t in (AttnProblem, GatedNormProblem, ResidualNormProblem))
     Z, PZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     for name, types in (("gdr_conv_fwd", [CP] + [P] * 9), ("gdr_conv_step", [CP] + [P] * 6),
                         ("gdr_conv_bwd", [CP] + [P] * 13 + [Z, P]), ("gdr_conv_bwd_workspace_size", [CP, PZ]),
@@ -149,6 +167,10 @@ def load_library():
                         ("gdr_scan_bwd_workspace_size", [SP, PZ]), ("gdr_layer_norm_fwd", [NP] + [P] * 7),
                         ("gdr_layer_norm_bwd", [NP] + [P] * 9 + [Z, P]),
                         ("gdr_layer_norm_bwd_workspace_size", [NP, PZ]),
+                        ("gdr_gated_norm_fwd", [GP] + [P] * 6), ("gdr_gated_norm_bwd", [GP] + [P] * 9 + [Z, P]),
+                        ("gdr_gated_norm_bwd_workspace_size", [GP, PZ]), ("gdr_residual_norm_fwd", [RP] + [P] * 10),
+                        ("gdr_residual_norm_bwd", [RP] + [P] * 15 + [Z, P]),
+                        ("gdr_residual_norm_bwd_workspace_size", [RP, PZ]),
                         ("gdr_window_attn_fwd", [AP] + [P] * 11 + [Z, P]), ("gdr_window_attn_fwd_workspace_size", [AP, PZ]),
                         ("gdr_window_attn_step", [AP] + [P] * 8 + [Z, P]), ("gdr_window_attn_step_workspace_size", [AP, PZ]),
                         ("gdr_window_attn_bwd", [AP] + [P] * 12 + [Z, P]), ("gdr_window_attn_bwd_workspace_size", [AP, PZ])):

@@ -1,0 +1,562 @@
+// The RMS norm with a gate and the residual sum with its norms, forward and backward
+// (include/gdr_mixer.h). A few operations an element: HBM bounds them, so a row is
+// read once and stays in registers between its sums and its outputs. TPR threads share
+// a row, each holding NV pieces of V = 16 bytes of the io type; rows go round the
+// grid, and up to 256 threads a row the next row is on its way while one is worked on,
+// with the parameters in registers. Longer rows take 512 or 1,024 threads, whose
+// fewer registers hold one row and no parameters.
+#include <type_traits>
+
+#include "gdr_norm.hpp"
+
+namespace gdr {
+
+namespace {
+
+template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
+
+// Sum over the TPR threads of a row, as in gdr_norm.hip, for any number of wavefronts
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (*red)[kBlock<TPR> / 64], int& slot) {
+#pragma unroll
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) v += __shfl_xor(v, m, 64);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v += red[slot][i];
+        slot ^= 1;
+    }
+    return v;
+}
+
+// A parameter's pieces: kept in registers or read again for every row
+template <typename T, int V, int NV, int TPR>
+struct Param {
+    static constexpr bool KEEP = TPR <= 256;
+    const void* p;
+    int C, f32;
+    float none, kept[KEEP ? NV : 1][V];
+    __device__ __forceinline__ Param(const void* p_, int C_, int f32_, float none_) : p(p_), C(C_), f32(f32_), none(none_) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                load_param<T, V>(p, (i * TPR + (int)threadIdx.x % TPR) * V, C, f32, none, kept[i]);
+        }
+    }
+    __device__ __forceinline__ void get(int i, float (&f)[V]) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = kept[i][v];
+        } else {
+            load_param<T, V>(p, (i * TPR + (int)threadIdx.x % TPR) * V, C, f32, none, f);
+        }
+    }
+};
+
+// act(z) and its derivative; silu is z sigmoid(z)
+__device__ __forceinline__ float gate_of(float z, bool silu_) {
+    const float s = sigmoid(z);
+    return silu_ ? z * s : s;
+}
+__device__ __forceinline__ float gate_slope(float z, bool silu_) {
+    const float s = sigmoid(z);
+    return silu_ ? silu_slope(z, s) : s * (1.f - s);
+}
+
+// ---------------------------------------------------------------- gated norm
+template <typename T, int V, int NV, int TPR, bool ONCE>
+__global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_fwd(GatedNormArgs a) {
+    constexpr int RPB = kBlock<TPR> / TPR;
+    constexpr bool AHEAD = TPR <= 256;
+    __shared__ float red[2][kBlock<TPR> / 64];
+    int slot = 0;
+    const int C = a.p.cols, l = threadIdx.x % TPR;
+    const bool act = a.p.activation == GDR_ACT_SILU;
+    const Param<T, V, NV, TPR> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
+    const float inv = 1.f / (float)C;
+    typename Raw<T, V>::type rx[NV], rz[NV];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (r < a.p.rows && c < C) {
+                rx[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, c, C);
+                rz[i] = load_piece<T, V, ONCE>((const T*)a.z + r * a.p.z_stride, c, C);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (AHEAD) fetch(r);
+    // every thread of a workgroup makes the same trips (row_sum meets in barriers)
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.p.rows; r0 += step, r += step) {
+        const bool live = r < a.p.rows;
+        if (!AHEAD) fetch(r);
+        float x[NV][V], g[NV][V], sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = live && (i * TPR + l) * V + v < C;
+                x[i][v] = in ? to_f(rx[i][v]) : 0.f;
+                g[i][v] = in ? to_f(rz[i][v]) : 0.f;
+                sq = __builtin_fmaf(x[i][v], x[i][v], sq);
+            }
+        if (AHEAD) fetch(r + step);
+        const float rstd = 1.f / sqrtf(row_sum<TPR>(sq, red, slot) * inv + a.p.eps);
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            float y[V];
+            w.get(i, y);
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] *= x[i][v] * rstd * gate_of(g[i][v], act);
+            store_any<T, V, ONCE>(a.y, r * C, c, C, a.p.out_dtype == GDR_F32, y);
+        }
+        if (l == 0 && a.rstd) a.rstd[r] = rstd;
+    }
+}
+
+// A workgroup's sums of its rows to memory: in LDS over the rows that it takes at a
+// time, then a thread a column.
+template <int V, int NV, int TPR>
+__device__ __forceinline__ void put_sums(float* part, const float (&s)[NV][V], int C, float* cols) {
+    constexpr int RPB = kBlock<TPR> / TPR;
+    const int l = threadIdx.x % TPR, rr = threadIdx.x / TPR;
+    if constexpr (RPB > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) cols[rr * (NV * TPR * V) + (i * TPR + l) * V + v] = s[i][v];
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += kBlock<TPR>) {
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < RPB; ++j) x += cols[j * (NV * TPR * V) + c];
+            part[c] = x;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c < C) store_piece<float, V>(part, c, C, s[i]);
+        }
+    }
+}
+
+// With xhat = x rstd, da = d_y act(z) and c = da weight:
+//   dx = rstd (c - xhat mean(c xhat)),   dz = d_y xhat weight act'(z),   dweight = sum of da xhat
+template <typename T, int V, int NV, int TPR, bool ONCE>
+__global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a) {
+    constexpr int RPB = kBlock<TPR> / TPR;
+    constexpr bool AHEAD = TPR <= 256;
+    __shared__ float red[2][kBlock<TPR> / 64];
+    __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
+    int slot = 0;
+    const int C = a.p.cols, l = threadIdx.x % TPR;
+    const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
+    const bool act = a.p.activation == GDR_ACT_SILU;
+    const Param<T, V, NV, TPR> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
+    const float inv = 1.f / (float)C;
+    float dw[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[i][v] = 0.f;
+    typename Raw<T, V>::type rx[NV], rz[NV];
+    AnyPiece<V> rd[NV];
+    float rr = 0.f;
+    auto fetch = [&](int64_t r) {
+        if (r >= a.p.rows) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            rx[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, c, C);
+            rz[i] = load_piece<T, V, ONCE>((const T*)a.z + r * a.p.z_stride, c, C);
+            load_any<T, V, ONCE>(rd[i], a.d_y, r * C, c, C, dy32);
+        }
+        rr = a.rstd[r];
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (AHEAD) fetch(r);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.p.rows; r0 += step, r += step) {
+        const bool live = r < a.p.rows;
+        if (!AHEAD) fetch(r);
+        const float rstd = rr;
+        float x[NV][V], z[NV][V], g[NV][V], s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack_any<T, V>(rd[i], dy32, g[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = live && (i * TPR + l) * V + v < C;
+                x[i][v] = in ? to_f(rx[i][v]) * rstd : 0.f;
+                z[i][v] = in ? to_f(rz[i][v]) : 0.f;
+                g[i][v] = in ? g[i][v] : 0.f;
+            }
+        }
+        if (AHEAD) fetch(r + step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[V];
+            w.get(i, f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float sg = sigmoid(z[i][v]), ac = act ? z[i][v] * sg : sg;
+                const float slope = act ? silu_slope(z[i][v], sg) : sg * (1.f - sg);
+                const float da = g[i][v] * ac;
+                dw[i][v] = __builtin_fmaf(da, x[i][v], dw[i][v]);
+                z[i][v] = g[i][v] * x[i][v] * f[v] * slope;        // dz
+                g[i][v] = da * f[v];                               // c
+                s = __builtin_fmaf(g[i][v], x[i][v], s);
+            }
+        }
+        s = row_sum<TPR>(s, red, slot) * inv;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            float d[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = rstd * (g[i][v] - x[i][v] * s);
+            store_any<T, V, ONCE>(a.dx, r * C, c, C, g32, d);
+            store_any<T, V, ONCE>(a.dz, r * C, c, C, g32, z[i]);
+        }
+    }
+    if (a.dweight) put_sums<V, NV, TPR>(a.partial + (int64_t)blockIdx.x * C, dw, C, cols);
+}
+
+// ---------------------------------------------------------------- residual sum with norms
+template <typename T, int V, int NV, int TPR, bool ONCE>
+__global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_fwd(ResidualNormArgs a) {
+    constexpr int RPB = kBlock<TPR> / TPR;
+    constexpr bool AHEAD = TPR <= 256;
+    __shared__ float red[2][kBlock<TPR> / 64];
+    int slot = 0;
+    const int C = a.p.cols, l = threadIdx.x % TPR, p32 = a.p.param_dtype == GDR_F32, s32 = a.p.stream_dtype == GDR_F32;
+    const bool post = a.x_weight != nullptr, token = a.p.gate == GDR_GATE_TOKEN;
+    const Param<T, V, NV, TPR> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f);
+    const Param<T, V, NV, TPR> gc(a.p.gate == GDR_GATE_CHANNEL ? a.gate : nullptr, C, p32, 1.f);
+    const float inv = 1.f / (float)C;
+    typename Raw<T, V>::type rx[NV], rg[NV];
+    AnyPiece<V> rs[NV];
+    auto fetch = [&](int64_t r) {
+        if (r >= a.p.rows) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            rx[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, c, C);
+            load_any<T, V, ONCE>(rs[i], a.residual, r * a.p.residual_stride, c, C, s32);
+            if (token) rg[i] = load_piece<T, V, ONCE>((const T*)a.gate + r * a.p.gate_stride, c, C);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (AHEAD) fetch(r);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.p.rows; r0 += step, r += step) {
+        const bool live = r < a.p.rows;
+        if (!AHEAD) fetch(r);
+        float x[NV][V], h[NV][V], g[NV][V], sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack_any<T, V>(rs[i], s32, h[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = live && (i * TPR + l) * V + v < C;
+                x[i][v] = in ? to_f(rx[i][v]) : 0.f;
+                h[i][v] = in ? h[i][v] : 0.f;
+                g[i][v] = token ? (in ? to_f(rg[i][v]) : 0.f) : 1.f;
+                sq = __builtin_fmaf(x[i][v], x[i][v], sq);
+            }
+        }
+        if (AHEAD) fetch(r + step);
+        float xr = 1.f;
+        if (post) xr = 1.f / sqrtf(row_sum<TPR>(sq, red, slot) * inv + a.p.eps);
+        sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[V], k[V];
+            xw.get(i, f);
+            gc.get(i, k);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float m = a.p.scale * (k[v] * g[i][v]);
+                h[i][v] = __builtin_fmaf(m, x[i][v] * xr * f[v], h[i][v]);
+                sq = __builtin_fmaf(h[i][v], h[i][v], sq);
+            }
+        }
+        const float rstd = 1.f / sqrtf(row_sum<TPR>(sq, red, slot) * inv + a.p.eps);
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            float y[V];
+            w.get(i, y);
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] *= h[i][v] * rstd;
+            store_any<T, V, ONCE>(a.y, r * C, c, C, a.p.out_dtype == GDR_F32, y);
+            store_any<T, V, ONCE>(a.h, r * C, c, C, s32, h[i]);
+        }
+        if (l == 0) {
+            if (a.rstd) a.rstd[r] = rstd;
+            if (a.x_rstd && post) a.x_rstd[r] = xr;
+        }
+    }
+}
+
+// With hhat = h rstd, xhat = x x_rstd and m = scale gate:
+//   c = d_y weight,          dh = d_h + rstd (c - hhat mean(c hhat)),   dresidual = dh,   dweight = sum of d_y hhat
+//   e = m dh x_weight,       dx = x_rstd (e - xhat mean(e xhat)) (or m dh),   dx_weight = sum of m dh xhat
+//   dgate = scale dh xhat x_weight (or scale dh x), summed over the rows for a gate per channel
+template <typename T, int V, int NV, int TPR, bool ONCE>
+__global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_bwd(ResidualNormArgs a) {
+    constexpr int RPB = kBlock<TPR> / TPR;
+    constexpr bool AHEAD = TPR <= 256;
+    __shared__ float red[2][kBlock<TPR> / 64];
+    __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
+    int slot = 0;
+    const int C = a.p.cols, l = threadIdx.x % TPR, p32 = a.p.param_dtype == GDR_F32, s32 = a.p.stream_dtype == GDR_F32;
+    const int dy32 = a.p.dy_dtype == GDR_F32, dh32 = a.p.dh_dtype == GDR_F32;
+    const bool post = a.x_weight != nullptr, token = a.p.gate == GDR_GATE_TOKEN, chan = a.p.gate == GDR_GATE_CHANNEL;
+    const Param<T, V, NV, TPR> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f), gc(chan ? a.gate : nullptr, C, p32, 1.f);
+    const float inv = 1.f / (float)C;
+    float dw[NV][V], dxw[NV][V], dg[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[i][v] = dxw[i][v] = dg[i][v] = 0.f;
+    typename Raw<T, V>::type rx[NV], rg[NV];
+    AnyPiece<V> rh[NV], ry[NV], rd[NV];
+    float r1 = 0.f, r2 = 1.f;
+    auto fetch = [&](int64_t r) {
+        if (r >= a.p.rows) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            rx[i] = load_piece<T, V, ONCE>((const T*)a.x + r * a.p.x_stride, c, C);
+            load_any<T, V, ONCE>(rh[i], a.h_in, r * C, c, C, s32);
+            load_any<T, V, ONCE>(ry[i], a.d_y, r * C, c, C, dy32);
+            if (a.d_h) load_any<T, V, ONCE>(rd[i], a.d_h, r * C, c, C, dh32);
+            if (token) rg[i] = load_piece<T, V, ONCE>((const T*)a.gate + r * a.p.gate_stride, c, C);
+        }
+        r1 = a.rstd[r];
+        if (post) r2 = a.x_rstd[r];
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (AHEAD) fetch(r);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.p.rows; r0 += step, r += step) {
+        const bool live = r < a.p.rows;
+        if (!AHEAD) fetch(r);
+        const float rstd = r1, xr = r2;
+        float x[NV][V], h[NV][V], c1[NV][V], d[NV][V], g[NV][V], s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack_any<T, V>(rh[i], s32, h[i]);
+            unpack_any<T, V>(ry[i], dy32, c1[i]);
+            unpack_any<T, V>(rd[i], dh32, d[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool in = live && (i * TPR + l) * V + v < C;
+                x[i][v] = in ? to_f(rx[i][v]) * xr : 0.f;
+                h[i][v] = in ? h[i][v] * rstd : 0.f;
+                c1[i][v] = in ? c1[i][v] : 0.f;
+                d[i][v] = in && a.d_h ? d[i][v] : 0.f;
+                g[i][v] = token ? (in ? to_f(rg[i][v]) : 0.f) : 1.f;
+            }
+        }
+        if (AHEAD) fetch(r + step);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[V];
+            w.get(i, f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                dw[i][v] = __builtin_fmaf(c1[i][v], h[i][v], dw[i][v]);
+                c1[i][v] *= f[v];
+                s = __builtin_fmaf(c1[i][v], h[i][v], s);
+            }
+        }
+        s = row_sum<TPR>(s, red, slot) * inv;
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            float f[V], k[V];
+            xw.get(i, f);
+            gc.get(i, k);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                d[i][v] = __builtin_fmaf(rstd, c1[i][v] - h[i][v] * s, d[i][v]);       // dh
+                const float m = a.p.scale * (k[v] * g[i][v]) * d[i][v];
+                dxw[i][v] = __builtin_fmaf(m, x[i][v], dxw[i][v]);
+                g[i][v] = a.p.scale * d[i][v] * x[i][v] * f[v];                        // dgate
+                dg[i][v] += g[i][v];
+                h[i][v] = m * f[v];
+                t = __builtin_fmaf(h[i][v], x[i][v], t);
+            }
+            if (!live || c >= C) continue;
+            store_any<T, V, ONCE>(a.dresidual, r * C, c, C, a.p.dres_dtype == GDR_F32, d[i]);
+            if (token && a.dgate) store_any<T, V, ONCE>(a.dgate, r * C, c, C, a.p.grad_dtype == GDR_F32, g[i]);
+        }
+        if (post) t = row_sum<TPR>(t, red, slot) * inv;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + l) * V;
+            if (c >= C) continue;
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] = post ? xr * (h[i][v] - x[i][v] * t) : h[i][v];
+            store_any<T, V, ONCE>(a.dx, r * C, c, C, a.p.grad_dtype == GDR_F32, y);
+        }
+    }
+    float* part = a.partial + (int64_t)blockIdx.x * 3 * C;
+    put_sums<V, NV, TPR>(part, dw, C, cols);
+    if (post) put_sums<V, NV, TPR>(part + C, dxw, C, cols);
+    if (chan) put_sums<V, NV, TPR>(part + 2 * (int64_t)C, dg, C, cols);
+}
+
+struct OneSum {
+    float* out;
+    __device__ void operator()(int64_t i, float v) const { out[i] = v; }
+};
+struct ThreeSums {
+    float *a, *b, *c;
+    int C;
+    __device__ void operator()(int64_t i, float v) const {
+        float* p = i < C ? a : i < 2 * (int64_t)C ? b : c;
+        if (p) p[i % C] = v;
+    }
+};
+
+// The variant for a row of C elements: the fewest threads whose registers hold it
+struct Shape {
+    int NV, TPR;
+};
+Shape shape_of(bool bf, int C) {
+    const Shape b[] = {{1, 16}, {1, 64}, {2, 64}, {1, 256}, {2, 256}, {2, 512}, {2, 1024}};
+    const Shape f[] = {{1, 16}, {2, 16}, {1, 64}, {2, 64}, {4, 64}, {2, 256}, {4, 256}, {4, 512}, {4, 1024}};
+    const int V = bf ? 8 : 4;
+    if (bf) {
+        for (const Shape& s : b)
+            if (C <= V * s.NV * s.TPR) return s;
+    } else {
+        for (const Shape& s : f)
+            if (C <= V * s.NV * s.TPR) return s;
+    }
+    return {0, 0};
+}
+
+// f(io type, V, NV, TPR)
+template <typename F>
+hipError_t by_shape(bool bf, int C, F f) {
+    const Shape s = shape_of(bf, C);
+#define GDR_SHAPE(T, V_, NV_, TPR_)                                                                                   \
+    if (s.NV == NV_ && s.TPR == TPR_) {                                                                               \
+        f(T{}, std::integral_constant<int, V_>{}, std::integral_constant<int, NV_>{}, std::integral_constant<int, TPR_>{}); \
+        return hipGetLastError();                                                                                     \
+    }
+    if (bf) {
+        GDR_SHAPE(bf16, 8, 1, 16) GDR_SHAPE(bf16, 8, 1, 64) GDR_SHAPE(bf16, 8, 2, 64) GDR_SHAPE(bf16, 8, 1, 256)
+        GDR_SHAPE(bf16, 8, 2, 256) GDR_SHAPE(bf16, 8, 2, 512) GDR_SHAPE(bf16, 8, 2, 1024)
+    } else {
+        GDR_SHAPE(float, 4, 1, 16) GDR_SHAPE(float, 4, 2, 16) GDR_SHAPE(float, 4, 1, 64) GDR_SHAPE(float, 4, 2, 64)
+        GDR_SHAPE(float, 4, 4, 64) GDR_SHAPE(float, 4, 2, 256) GDR_SHAPE(float, 4, 4, 256) GDR_SHAPE(float, 4, 4, 512)
+        GDR_SHAPE(float, 4, 4, 1024)
+    }
+#undef GDR_SHAPE
+    return hipErrorInvalidValue;
+}
+int64_t row_blocks(int64_t rows, int TPR) {
+    const int rpb = TPR < 256 ? 256 / TPR : 1;
+    return (rows + rpb - 1) / rpb;
+}
+// four rows a thread where there are many, and never more threads than 32 bits count
+unsigned fwd_blocks(int64_t rows, int TPR) {
+    const int64_t n = row_blocks(rows, TPR), least = 8192, most = (int64_t)1 << 21;
+    const int64_t quarter = n / 4 > least ? n / 4 : least;
+    return (unsigned)(n < quarter ? n : quarter < most ? quarter : most);
+}
+int bwd_blocks(int64_t rows, bool bf, int C) {
+    const int64_t n = row_blocks(rows, shape_of(bf, C).TPR), most = 512;
+    return (int)(n < most ? n : most);
+}
+
+}  // namespace
+
+int gated_norm_bwd_blocks(const gdr_gated_norm_problem_t& p) { return bwd_blocks(p.rows, p.io_dtype == GDR_BF16, p.cols); }
+int residual_norm_bwd_blocks(const gdr_residual_norm_problem_t& p) {
+    return bwd_blocks(p.rows, p.io_dtype == GDR_BF16, p.cols);
+}
+
+#define GDR_LAUNCH(kernel, grid, once, a)                                                                         \
+    do {                                                                                                          \
+        typedef decltype(type) T;                                                                                 \
+        constexpr int V = decltype(vec)::value, NV = decltype(nv)::value, TPR = decltype(tpr)::value;             \
+        if (once) kernel<T, V, NV, TPR, true><<<dim3(grid), kBlock<TPR>, 0, (a).stream>>>(a);                     \
+        else kernel<T, V, NV, TPR, false><<<dim3(grid), kBlock<TPR>, 0, (a).stream>>>(a);                         \
+    } while (0)
+
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a) {
+    if (a.p.rows == 0) return hipSuccess;
+    const bool once = beyond_caches(a.p.rows * a.p.cols * (2 * size_of(a.p.io_dtype) + size_of(a.p.out_dtype)));
+    return by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
+        GDR_LAUNCH(k_gated_norm_fwd, fwd_blocks(a.p.rows, TPR), once, a);
+    });
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a) {
+    const int blocks = gated_norm_bwd_blocks(a.p);
+    if (blocks > 0) {
+        const bool once = beyond_caches(a.p.rows * a.p.cols *
+                                        (2 * size_of(a.p.io_dtype) + size_of(a.p.dy_dtype) + 2 * size_of(a.p.grad_dtype)));
+        const hipError_t e = by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
+            GDR_LAUNCH(k_gated_norm_bwd, (unsigned)blocks, once, a);
+        });
+        if (e != hipSuccess) return e;
+    }
+    return a.dweight ? sum_partials(a.partial, blocks, a.p.cols, OneSum{a.dweight}, a.stream) : hipSuccess;
+}
+
+hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a) {
+    if (a.p.rows == 0) return hipSuccess;
+    const int token = a.p.gate == GDR_GATE_TOKEN;
+    const bool once = beyond_caches(a.p.rows * a.p.cols * ((1 + token) * size_of(a.p.io_dtype) + size_of(a.p.out_dtype) +
+                                                           2 * size_of(a.p.stream_dtype)));
+    return by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
+        GDR_LAUNCH(k_residual_norm_fwd, fwd_blocks(a.p.rows, TPR), once, a);
+    });
+}
+
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a) {
+    const int blocks = residual_norm_bwd_blocks(a.p);
+    const bool chan = a.p.gate == GDR_GATE_CHANNEL;
+    if (blocks > 0) {
+        const int token = a.p.gate == GDR_GATE_TOKEN;
+        const bool once = beyond_caches(a.p.rows * a.p.cols *
+                                        ((1 + token) * (size_of(a.p.io_dtype) + size_of(a.p.grad_dtype)) +
+                                         size_of(a.p.stream_dtype) + size_of(a.p.dy_dtype) + size_of(a.p.dh_dtype) +
+                                         size_of(a.p.dres_dtype)));
+        const hipError_t e = by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
+            GDR_LAUNCH(k_residual_norm_bwd, (unsigned)blocks, once, a);
+        });
+        if (e != hipSuccess) return e;
+    }
+    ThreeSums out{a.dweight, a.x_weight ? a.dx_weight : nullptr, chan ? (float*)a.dgate : nullptr, a.p.cols};
+    if (!out.a && !out.b && !out.c) return hipSuccess;
+    return sum_partials(a.partial, blocks, 3 * (int64_t)a.p.cols, out, a.stream);
+}
+
+}  // namespace gdr

@@ -42,6 +42,30 @@ int norm_bwd_blocks(const gdr_norm_problem_t& p);
 hipError_t launch_norm_fwd(const NormArgs& a);
 hipError_t launch_norm_bwd(const NormArgs& a);
 
+struct GatedNormArgs {
+    gdr_gated_norm_problem_t p;
+    const void *x, *z, *weight, *d_y;
+    void *y, *dx, *dz;
+    float *rstd, *dweight;
+    float* partial;            // [blocks][cols]
+    hipStream_t stream;
+};
+int gated_norm_bwd_blocks(const gdr_gated_norm_problem_t& p);
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a);
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a);
+
+struct ResidualNormArgs {
+    gdr_residual_norm_problem_t p;
+    const void *x, *residual, *weight, *x_weight, *gate, *h_in, *d_y, *d_h;
+    void *y, *h, *dx, *dresidual, *dgate;
+    float *rstd, *x_rstd, *dweight, *dx_weight;
+    float* partial;            // [blocks][3][cols]: dweight, dx_weight, dgate of a gate per channel
+    hipStream_t stream;
+};
+int residual_norm_bwd_blocks(const gdr_residual_norm_problem_t& p);
+hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a);
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a);
+
 struct ScanArgs {
     gdr_scan_problem_t p;
     int64_t Ttot, max_len;     // total tokens, longest sequence (host)

@@ -1,5 +1,7 @@
 // Host side of the layer operators declared in include/gdr_mixer.h: argument
 // checks and launch arguments.
+#include <cmath>
+
 #include "gdr_checks.hpp"
 
 namespace {
@@ -74,18 +76,57 @@ gdr::ScanArgs scan_args(const gdr_scan_problem_t* p, const void* x, const void* 
     return a;
 }
 
-// ---------------------------------------------------------------- layer norm
+// ---------------------------------------------------------------- norms
+// what the three kinds of norms share
+gdr_status_t check_rows(int64_t rows, int32_t cols, float eps) {
+    if (rows < 0 || cols < 1) return fail(GDR_ERR_SHAPE, "rows must be >= 0 and cols positive");
+    if (cols > 16384) return fail(GDR_ERR_UNSUPPORTED, "cols %d not supported (1 to 16384)", cols);
+    if (rows > ((int64_t)1 << 40)) return fail(GDR_ERR_SHAPE, "too many rows");
+    if (!(eps >= 0.f)) return fail(GDR_ERR_SHAPE, "eps must be >= 0");
+    return GDR_OK;
+}
 gdr_status_t check_norm(const gdr_norm_problem_t* p) {
     if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
-    if (p->rows < 0 || p->cols < 1) return fail(GDR_ERR_SHAPE, "rows must be >= 0 and cols positive");
-    if (p->cols > 16384) return fail(GDR_ERR_UNSUPPORTED, "cols %d not supported (1 to 16384)", p->cols);
-    if (p->rows > ((int64_t)1 << 40)) return fail(GDR_ERR_SHAPE, "too many rows");
-    if (!(p->eps >= 0.f)) return fail(GDR_ERR_SHAPE, "eps must be >= 0");
+    GDR_TRY(check_rows(p->rows, p->cols, p->eps));
     if (!is_dtype(p->io_dtype)) return fail(GDR_ERR_DTYPE, "unknown io_dtype %d", p->io_dtype);
     if (!io_or_f32(p->param_dtype, p->io_dtype) || !io_or_f32(p->out_dtype, p->io_dtype) ||
         !io_or_f32(p->dy_dtype, p->io_dtype) || !io_or_f32(p->grad_dtype, p->io_dtype))
         return fail(GDR_ERR_DTYPE, "param_dtype, out_dtype, dy_dtype and grad_dtype must equal io_dtype or be GDR_F32");
     return check_stride("x_stride", p->x_stride, p->cols);
+}
+gdr_status_t check_gated(const gdr_gated_norm_problem_t* p) {
+    if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
+    GDR_TRY(check_rows(p->rows, p->cols, p->eps));
+    if (!is_dtype(p->io_dtype)) return fail(GDR_ERR_DTYPE, "unknown io_dtype %d", p->io_dtype);
+    for (int32_t t : {p->param_dtype, p->out_dtype, p->dy_dtype, p->grad_dtype})
+        if (!io_or_f32(t, p->io_dtype))
+            return fail(GDR_ERR_DTYPE, "param_dtype, out_dtype, dy_dtype and grad_dtype must equal io_dtype or be GDR_F32");
+    if (p->activation != GDR_ACT_SILU && p->activation != GDR_ACT_SIGMOID)
+        return fail(GDR_ERR_UNSUPPORTED, "activation %d not supported (GDR_ACT_SILU or GDR_ACT_SIGMOID)", p->activation);
+    GDR_TRY(check_stride("x_stride", p->x_stride, p->cols));
+    return check_stride("z_stride", p->z_stride, p->cols);
+}
+gdr_status_t check_residual(const gdr_residual_norm_problem_t* p) {
+    if (!p) return fail(GDR_ERR_NULL, "problem is NULL");
+    GDR_TRY(check_rows(p->rows, p->cols, p->eps));
+    if (!std::isfinite(p->scale)) return fail(GDR_ERR_SHAPE, "scale must be finite");
+    if (!is_dtype(p->io_dtype)) return fail(GDR_ERR_DTYPE, "unknown io_dtype %d", p->io_dtype);
+    for (int32_t t : {p->param_dtype, p->stream_dtype, p->out_dtype, p->dy_dtype, p->dh_dtype, p->grad_dtype, p->dres_dtype})
+        if (!io_or_f32(t, p->io_dtype))
+            return fail(GDR_ERR_DTYPE, "param, stream, out, dy, dh, grad and dres dtype must equal io_dtype or be GDR_F32");
+    if (p->gate < GDR_GATE_NONE || p->gate > GDR_GATE_TOKEN) return fail(GDR_ERR_UNSUPPORTED, "unknown gate %d", p->gate);
+    GDR_TRY(check_stride("x_stride", p->x_stride, p->cols));
+    if (p->gate == GDR_GATE_TOKEN) GDR_TRY(check_stride("gate_stride", p->gate_stride, p->cols));
+    return check_stride("residual_stride", p->residual_stride, p->cols);
+}
+gdr_status_t check_gate(const gdr_residual_norm_problem_t* p, const void* gate) {
+    if ((gate == nullptr) != (p->gate == GDR_GATE_NONE) && (gate || p->rows > 0))
+        return fail(GDR_ERR_NULL, "the gate must be NULL for GDR_GATE_NONE and given otherwise");
+    return GDR_OK;
+}
+size_t gated_bwd_bytes(const gdr_gated_norm_problem_t* p) { return (size_t)gdr::gated_norm_bwd_blocks(*p) * p->cols * 4; }
+size_t residual_bwd_bytes(const gdr_residual_norm_problem_t* p) {
+    return (size_t)gdr::residual_norm_bwd_blocks(*p) * 3 * p->cols * 4;
 }
 size_t norm_bwd_bytes(const gdr_norm_problem_t* p) { return (size_t)gdr::norm_bwd_blocks(*p) * 2 * p->cols * 4; }
 
@@ -274,6 +315,99 @@ gdr_status_t gdr_layer_norm_bwd(const gdr_norm_problem_t* p, const void* x, cons
     a.partial = static_cast<float*>(workspace);
     a.stream = static_cast<hipStream_t>(stream);
     return done(gdr::launch_norm_bwd(a));
+}
+
+gdr_status_t gdr_gated_norm_fwd(const gdr_gated_norm_problem_t* p, const void* x, const void* z, const void* weight,
+                                void* y, float* rstd, void* stream) {
+    GDR_TRY(check_gated(p));
+    const Ptr ptrs[] = {{x, p->io_dtype, true, "x"}, {z, p->io_dtype, true, "z"}, {weight, p->param_dtype, false, "weight"},
+                        {y, p->out_dtype, true, "y"}, {rstd, GDR_F32, false, "rstd"}};
+    GDR_TRY(check_ptrs(ptrs, p->rows > 0));
+    gdr::GatedNormArgs a{};
+    a.p = *p;
+    a.x = x; a.z = z; a.weight = weight; a.y = y; a.rstd = rstd;
+    a.stream = static_cast<hipStream_t>(stream);
+    return done(gdr::launch_gated_norm_fwd(a));
+}
+
+gdr_status_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem_t* p, size_t* bytes) {
+    if (!bytes) return fail(GDR_ERR_NULL, "bytes is NULL");
+    GDR_TRY(check_gated(p));
+    *bytes = gated_bwd_bytes(p);
+    return GDR_OK;
+}
+
+gdr_status_t gdr_gated_norm_bwd(const gdr_gated_norm_problem_t* p, const void* x, const void* z, const void* d_y,
+                                const void* weight, const float* rstd, void* dx, void* dz, float* dweight,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    GDR_TRY(check_gated(p));
+    const Ptr ptrs[] = {{x, p->io_dtype, true, "x"}, {z, p->io_dtype, true, "z"}, {d_y, p->dy_dtype, true, "d_y"},
+                        {weight, p->param_dtype, false, "weight"}, {rstd, GDR_F32, true, "rstd"},
+                        {dx, p->grad_dtype, true, "dx"}, {dz, p->grad_dtype, true, "dz"},
+                        {dweight, GDR_F32, false, "dweight"}};
+    GDR_TRY(check_ptrs(ptrs, p->rows > 0));
+    GDR_TRY(check_workspace(workspace, workspace_bytes, gated_bwd_bytes(p)));
+    gdr::GatedNormArgs a{};
+    a.p = *p;
+    a.x = x; a.z = z; a.d_y = d_y; a.weight = weight; a.rstd = const_cast<float*>(rstd);
+    a.dx = dx; a.dz = dz; a.dweight = dweight;
+    a.partial = static_cast<float*>(workspace);
+    a.stream = static_cast<hipStream_t>(stream);
+    return done(gdr::launch_gated_norm_bwd(a));
+}
+
+gdr_status_t gdr_residual_norm_fwd(const gdr_residual_norm_problem_t* p, const void* x, const void* residual,
+                                   const void* weight, const void* x_weight, const void* gate, void* y, void* h,
+                                   float* rstd, float* x_rstd, void* stream) {
+    GDR_TRY(check_residual(p));
+    const int32_t gate_dtype = p->gate == GDR_GATE_TOKEN ? p->io_dtype : p->param_dtype;
+    const Ptr ptrs[] = {{x, p->io_dtype, true, "x"}, {residual, p->stream_dtype, true, "residual"},
+                        {weight, p->param_dtype, false, "weight"}, {x_weight, p->param_dtype, false, "x_weight"},
+                        {gate, gate_dtype, false, "gate"}, {y, p->out_dtype, true, "y"}, {h, p->stream_dtype, true, "h"},
+                        {rstd, GDR_F32, false, "rstd"}, {x_rstd, GDR_F32, false, "x_rstd"}};
+    GDR_TRY(check_ptrs(ptrs, p->rows > 0));
+    GDR_TRY(check_gate(p, gate));
+    gdr::ResidualNormArgs a{};
+    a.p = *p;
+    a.x = x; a.residual = residual; a.weight = weight; a.x_weight = x_weight; a.gate = gate;
+    a.y = y; a.h = h; a.rstd = rstd; a.x_rstd = x_rstd;
+    a.stream = static_cast<hipStream_t>(stream);
+    return done(gdr::launch_residual_norm_fwd(a));
+}
+
+gdr_status_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_norm_problem_t* p, size_t* bytes) {
+    if (!bytes) return fail(GDR_ERR_NULL, "bytes is NULL");
+    GDR_TRY(check_residual(p));
+    *bytes = residual_bwd_bytes(p);
+    return GDR_OK;
+}
+
+gdr_status_t gdr_residual_norm_bwd(const gdr_residual_norm_problem_t* p, const void* x, const void* h, const void* d_y,
+                                   const void* d_h, const void* weight, const void* x_weight, const void* gate,
+                                   const float* rstd, const float* x_rstd, void* dx, void* dresidual, float* dweight,
+                                   float* dx_weight, void* dgate, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    GDR_TRY(check_residual(p));
+    const bool token = p->gate == GDR_GATE_TOKEN;
+    const int32_t gate_dtype = token ? p->io_dtype : p->param_dtype;
+    const Ptr ptrs[] = {{x, p->io_dtype, true, "x"}, {h, p->stream_dtype, true, "h"}, {d_y, p->dy_dtype, true, "d_y"},
+                        {d_h, p->dh_dtype, false, "d_h"}, {weight, p->param_dtype, false, "weight"},
+                        {x_weight, p->param_dtype, false, "x_weight"}, {gate, gate_dtype, false, "gate"},
+                        {rstd, GDR_F32, true, "rstd"}, {x_rstd, GDR_F32, x_weight != nullptr, "x_rstd"},
+                        {dx, p->grad_dtype, true, "dx"}, {dresidual, p->dres_dtype, true, "dresidual"},
+                        {dweight, GDR_F32, false, "dweight"}, {dx_weight, GDR_F32, false, "dx_weight"},
+                        {dgate, token ? p->grad_dtype : GDR_F32, false, "dgate"}};
+    GDR_TRY(check_ptrs(ptrs, p->rows > 0));
+    GDR_TRY(check_gate(p, gate));
+    GDR_TRY(check_workspace(workspace, workspace_bytes, residual_bwd_bytes(p)));
+    gdr::ResidualNormArgs a{};
+    a.p = *p;
+    a.x = x; a.h_in = h; a.d_y = d_y; a.d_h = d_h; a.weight = weight; a.x_weight = x_weight; a.gate = gate;
+    a.rstd = const_cast<float*>(rstd); a.x_rstd = const_cast<float*>(x_rstd);
+    a.dx = dx; a.dresidual = dresidual; a.dweight = dweight; a.dx_weight = dx_weight; a.dgate = dgate;
+    a.partial = static_cast<float*>(workspace);
+    a.stream = static_cast<hipStream_t>(stream);
+    return done(gdr::launch_residual_norm_bwd(a));
 }
 
 }  // extern "C"

@@ -13,45 +13,13 @@
 // cuts is moved by elements.
 #include <type_traits>
 
-#include "gdr_mixer.hpp"
+#include "gdr_norm.hpp"
 
 namespace gdr {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// elements c .. c + V - 1 of a row of C, zero past its end
-template <typename T, int V, bool ONCE = false>
-__device__ __forceinline__ typename Raw<T, V>::type load_piece(const T* row, int c, int C) {
-    typename Raw<T, V>::type r;
-    if (c + V <= C) return load_raw<T, V, ONCE>(row + c);
-#pragma unroll
-    for (int v = 0; v < V; ++v) r[v] = c + v < C ? row[c + v] : to_t<T>(0.f);
-    return r;
-}
-// a parameter's elements, which are T or fp32; `none` where there is no parameter
-template <typename T, int V>
-__device__ __forceinline__ void load_param(const void* p, int c, int C, int f32, float none, float (&f)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = none;
-    if (!p || c >= C) return;
-    if (f32) unpack<float, V>(load_piece<float, V>((const float*)p, c, C), f);
-    else unpack<T, V>(load_piece<T, V>((const T*)p, c, C), f);
-}
-template <typename T, int V, bool ONCE = false>
-__device__ __forceinline__ void store_piece(T* row, int c, int C, const float (&f)[V]) {
-    typename Raw<T, V>::type r;
-#pragma unroll
-    for (int v = 0; v < V; ++v) r[v] = to_t<T>(f[v]);
-    if (c + V <= C) {
-        store_raw<T, V, ONCE>(row + c, r);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (c + v < C) row[c + v] = r[v];
-    }
-}
 
 // Sum over the TPR threads of a row: butterfly inside a wavefront, LDS across;
 // the caller alternates between two LDS slots, so that one barrier a sum is enough.

@@ -1,6 +1,6 @@
 """The operators that stand next to the gated delta rule in a layer
 (include/gdr_mixer.h): the short causal convolution, the selective state space
-scan and layer norm.
+scan, layer norm, the gated RMS norm, and the residual sum with its norms.
 
 As in ``api``, argument marshalling only: torch supplies device memory and the
 current HIP stream. Inputs that hold tokens ([B, T, ...]) may be slices of a
@@ -13,10 +13,12 @@ synchronisation is needed); empty sequences are allowed.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
-from .api import _DTYPES, ConvProblem, NormProblem, ScanProblem, _check, load_library
+from .api import (_DTYPES, ConvProblem, GatedNormProblem, NormProblem, ResidualNormProblem, ScanProblem, _check,
+                  load_library)
 
 _ACTIVATIONS = {None: 0, "silu": 1}
 
@@ -362,4 +364,143 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, grad_dtype=None):
     ws, n = _workspace(lib.gdr_layer_norm_bwd_workspace_size, prob, dev)
     _launch(lib.gdr_layer_norm_bwd, dev, ctypes.byref(prob), _p(x), _p(d_y), _p(weight), _p(mean), _p(rstd),
             _p(out["dx"]), _p(out["dweight"]), _p(out["dbias"]), _p(ws), n)
+    return out
+
+
+# ---------------------------------------------------------------- gated RMS norm
+_GATES = {"silu": 1, "sigmoid": 2}
+
+
+def _rows(t, name, shape, dtypes, dev):
+    """The row stride of a tensor [..., C] of evenly strided rows."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev:
+        _refuse(t, name, shape, dtypes)
+    return shape[-1] if t.is_contiguous() else _token_stride(t, name, shape[-1])
+
+
+def _cols(x):
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("expected x [..., C]")
+    return x.shape[-1]
+
+
+def _gated(x, z, weight, activation, eps, out, grad=torch.float32, d_y=None):
+    dev, io, C = x.device, x.dtype, _cols(x)
+    if activation not in _GATES:
+        raise ValueError("activation must be 'silu' or 'sigmoid'")
+    xs, zs = _rows(x, "x", x.shape, (io,), dev), _rows(z, "z", x.shape, (io,), dev)
+    _dense(weight, "weight", (C,), (io, torch.float32), dev)
+    t_io = _DTYPES[io]
+    return GatedNormProblem(x.numel() // C, xs, zs, C, eps, _GATES[activation], t_io,
+                            t_io if weight is None else _DTYPES[weight.dtype], _DTYPES[out],
+                            t_io if d_y is None else _DTYPES[d_y.dtype], _DTYPES[grad])
+
+
+def gated_norm_fwd(x, z, weight=None, activation="silu", eps=1e-5, out_dtype=None):
+    """RMS norm over the last axis (at most 16384 elements) with a gate:
+    y = x rstd weight act(z) with rstd = 1 / sqrt(mean(x^2) + eps) and act "silu"
+    or "sigmoid". x, z [..., C] (rows evenly strided, slices of a projection for
+    one); weight [C] in the io dtype or float32. Returns (y, rstd), rstd [...]
+    float32 as gated_norm_bwd takes it. out_dtype: the io dtype (default) or
+    float32."""
+    dev = _device(x)
+    out = _out_dtype(out_dtype, x.dtype)
+    prob = _gated(x, z, weight, activation, eps, out)
+    y = x.new_empty(x.shape, dtype=out)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    _launch(load_library().gdr_gated_norm_fwd, dev, ctypes.byref(prob), _p(x), _p(z), _p(weight), _p(y), _p(rstd))
+    return y, rstd
+
+
+def gated_norm_bwd(x, z, d_y, rstd, weight=None, activation="silu", grad_dtype=None):
+    """Gradients of gated_norm_fwd, given dL/dy (io dtype or float32) and the
+    forward's rstd: dict dx, dz (in grad_dtype: float32, the default, or the io
+    dtype) and dweight (float32, summed over the rows)."""
+    dev = _device(x)
+    io, grad = x.dtype, _grad_dtype(grad_dtype, x.dtype)
+    _dense(d_y, "d_y", x.shape, (io, torch.float32), dev)
+    _dense(rstd, "rstd", x.shape[:-1], (torch.float32,), dev)
+    prob = _gated(x, z, weight, activation, 0.0, io, grad, d_y)
+    out = dict(dx=torch.empty(x.shape, dtype=grad, device=dev), dz=torch.empty(x.shape, dtype=grad, device=dev),
+               dweight=torch.empty(x.shape[-1], dtype=torch.float32, device=dev))
+    lib = load_library()
+    ws, n = _workspace(lib.gdr_gated_norm_bwd_workspace_size, prob, dev)
+    _launch(lib.gdr_gated_norm_bwd, dev, ctypes.byref(prob), _p(x), _p(z), _p(d_y), _p(weight), _p(rstd), _p(out["dx"]),
+            _p(out["dz"]), _p(out["dweight"]), _p(ws), n)
+    return out
+
+
+# ---------------------------------------------------------------- residual sum with norms
+def _residual(x, res, name, weight, x_weight, gate, scale, eps, out, grad=torch.float32, dres=torch.float32, d_y=None,
+              d_h=None):
+    dev, io, C = x.device, x.dtype, _cols(x)
+    kinds, t_io = (io, torch.float32), _DTYPES[x.dtype]
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite")
+    xs, rs = _rows(x, "x", x.shape, (io,), dev), _rows(res, name, x.shape, kinds, dev)
+    token = gate is not None and gate.dim() == x.dim() and (x.dim() > 1 or gate.dtype == io)
+    param = next((t.dtype for t in (weight, x_weight, None if token else gate) if t is not None), io)
+    if param not in kinds:
+        raise ValueError("weight, x_weight and a gate per channel must be in the io dtype or float32")
+    for t, label in ((weight, "weight"), (x_weight, "x_weight"), (None if token else gate, "gate")):
+        _dense(t, label, (C,), (param,), dev)
+    gs = _rows(gate, "gate", x.shape, (io,), dev) if token else 0
+    return ResidualNormProblem(x.numel() // C, xs, rs, gs, C, eps, scale, 0 if gate is None else 2 if token else 1, t_io,
+                               _DTYPES[param], _DTYPES[res.dtype], _DTYPES[out], t_io if d_y is None else _DTYPES[d_y.dtype],
+                               t_io if d_h is None else _DTYPES[d_h.dtype], _DTYPES[grad], _DTYPES[dres])
+
+
+def residual_norm_fwd(x, residual, weight=None, x_weight=None, gate=None, scale=1.0, eps=1e-5, out_dtype=None):
+    """What lies between two blocks: h = residual + scale gate a, y = RMS norm of
+    h times weight, where a is x, the block's output, or with x_weight the RMS
+    norm of x times x_weight. All norms over the last axis (at most 16384).
+
+    x [..., C]; residual [..., C] in the io dtype or float32 (rows evenly
+    strided); gate: None, one a channel [C], or one a token, shaped like x in the
+    io dtype; weight, x_weight and a channels' gate share a dtype, the io dtype or
+    float32. Returns (y, h, rstd, x_rstd): y in out_dtype (the io dtype, or
+    float32), h in residual's dtype, rstd and x_rstd (None without x_weight) [...]
+    float32, as residual_norm_bwd takes them."""
+    dev = _device(x)
+    out = _out_dtype(out_dtype, x.dtype)
+    prob = _residual(x, residual, "residual", weight, x_weight, gate, scale, eps, out)
+    y = x.new_empty(x.shape, dtype=out)
+    h = x.new_empty(x.shape, dtype=residual.dtype)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    x_rstd = None if x_weight is None else torch.empty_like(rstd)
+    _launch(load_library().gdr_residual_norm_fwd, dev, ctypes.byref(prob), _p(x), _p(residual), _p(weight), _p(x_weight),
+            _p(gate), _p(y), _p(h), _p(rstd), _p(x_rstd))
+    return y, h, rstd, x_rstd
+
+
+def residual_norm_bwd(x, h, d_y, rstd, weight=None, d_h=None, x_weight=None, x_rstd=None, gate=None, scale=1.0,
+                      grad_dtype=None):
+    """Gradients of residual_norm_fwd, given dL/dy and dL/dh (d_h, None: zeros;
+    each in the io dtype or float32) and the forward's h, rstd and x_rstd: dict
+    dx, dresidual, dweight and, with them, dx_weight and dgate (shaped like the
+    gate). grad_dtype None (default): all float32; the io dtype: dx and a token
+    gate's gradient in it, dresidual in h's dtype. Sums over rows are float32."""
+    dev = _device(x)
+    io, grad = x.dtype, _grad_dtype(grad_dtype, x.dtype)
+    dres = torch.float32 if grad_dtype is None else h.dtype
+    _dense(h, "h", x.shape, (io, torch.float32), dev)
+    _dense(d_y, "d_y", x.shape, (io, torch.float32), dev)
+    _dense(d_h, "d_h", x.shape, (io, torch.float32), dev)
+    _dense(rstd, "rstd", x.shape[:-1], (torch.float32,), dev)
+    _dense(x_rstd, "x_rstd", x.shape[:-1], (torch.float32,), dev)
+    if (x_weight is None) != (x_rstd is None):
+        raise ValueError("x_weight and x_rstd come together")
+    prob = _residual(x, h, "h", weight, x_weight, gate, scale, 0.0, io, grad, dres, d_y, d_h)
+    new = lambda shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)
+    C = x.shape[-1:]
+    out = dict(dx=new(x.shape, grad), dresidual=new(x.shape, dres), dweight=new(C))
+    if x_weight is not None:
+        out["dx_weight"] = new(C)
+    if gate is not None:
+        out["dgate"] = new(x.shape, grad) if prob.gate == 2 else new(C)
+    lib = load_library()
+    ws, n = _workspace(lib.gdr_residual_norm_bwd_workspace_size, prob, dev)
+    _launch(lib.gdr_residual_norm_bwd, dev, ctypes.byref(prob), _p(x), _p(h), _p(d_y), _p(d_h), _p(weight), _p(x_weight),
+            _p(gate), _p(rstd), _p(x_rstd), _p(out["dx"]), _p(out["dresidual"]), _p(out["dweight"]),
+            _p(out.get("dx_weight")), _p(out.get("dgate")), _p(ws), n)
     return out

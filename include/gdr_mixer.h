@@ -5,6 +5,8 @@
  *   short causal convolution   forward, one token per sequence, backward
  *   selective state space scan forward, one token per sequence, backward
  *   layer norm                 forward, backward
+ *   gated RMS norm             forward, backward
+ *   residual sum with norms    forward, backward
  *
  * Conventions are those of gdr.h: device pointers except cu_seqlens_host, the
  * caller owns every buffer, work is enqueued on `stream` and nothing is
@@ -34,7 +36,7 @@
 extern "C" {
 #endif
 
-typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation_t;
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_activation_t;
 
 /*
  * Short causal convolution, one filter per channel:
@@ -50,7 +52,7 @@ typedef struct {
     int32_t num_seqs;       /* batch, or len(cu_seqlens) - 1                             */
     int32_t channels;       /* D: 1 to 2^30                                              */
     int32_t width;          /* W: 2, 3 or 4                                              */
-    int32_t activation;     /* gdr_activation_t                                          */
+    int32_t activation;     /* GDR_ACT_NONE or GDR_ACT_SILU                              */
     int32_t io_dtype;       /* x, y and states                                           */
     int32_t param_dtype;    /* weight and bias: io_dtype or GDR_F32                      */
     int32_t dy_dtype;       /* backward: d_y and d_final_state, io_dtype or GDR_F32      */
@@ -163,6 +165,72 @@ gdr_status_t gdr_layer_norm_bwd_workspace_size(const gdr_norm_problem_t* problem
 gdr_status_t gdr_layer_norm_bwd(const gdr_norm_problem_t* problem, const void* x, const void* d_y,
                                 const void* weight, const float* mean, const float* rstd, void* dx, float* dweight,
                                 float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm over the last axis with a gate, behind the heads of a mixer:
+ *   y = x rstd weight act(z),   rstd = 1 / sqrt(mean(x^2) + eps),   act = silu or sigmoid
+ *   x, z [rows, cols] io_dtype, row strides x_stride and z_stride; weight [cols] param_dtype or NULL (ones)
+ *   y [rows, cols] out_dtype, dense; rstd [rows] fp32 (forward: NULL to skip)
+ */
+typedef struct {
+    int64_t rows, x_stride, z_stride;
+    int32_t cols;           /* 1 to 16384                                                */
+    float eps;              /* >= 0                                                      */
+    int32_t activation;     /* GDR_ACT_SILU or GDR_ACT_SIGMOID                           */
+    int32_t io_dtype, param_dtype;
+    int32_t out_dtype;      /* y: io_dtype or GDR_F32                                    */
+    int32_t dy_dtype;       /* backward: d_y (dense), io_dtype or GDR_F32                */
+    int32_t grad_dtype;     /* backward: dx and dz (dense), io_dtype or GDR_F32          */
+} gdr_gated_norm_problem_t;
+
+gdr_status_t gdr_gated_norm_fwd(const gdr_gated_norm_problem_t* problem, const void* x, const void* z,
+                                const void* weight, void* y, float* rstd, void* stream);
+
+/* For dL/dy and the forward's rstd. dweight fp32 [cols], the sum over rows (NULL: skipped). */
+gdr_status_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem_t* problem, size_t* bytes);
+gdr_status_t gdr_gated_norm_bwd(const gdr_gated_norm_problem_t* problem, const void* x, const void* z, const void* d_y,
+                                const void* weight, const float* rstd, void* dx, void* dz, float* dweight,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * What lies between two blocks: the norm behind a block, its gate and scale, the
+ * residual sum, and the norm before the next block:
+ *   a = x x_rstd x_weight (x itself without x_weight),   h = residual + scale gate a,   y = h rstd weight
+ * with the RMS norms' rstd of x and of h. y is formed from h before that is rounded.
+ *   x [rows, cols] io_dtype; residual stream_dtype; row strides x_stride and residual_stride
+ *   weight (NULL: ones), x_weight (NULL: no norm behind the block) [cols] param_dtype
+ *   gate: none (NULL), one of [cols] param_dtype, or one of [rows, cols] io_dtype of row stride gate_stride
+ *   y out_dtype, h stream_dtype, both dense; rstd, x_rstd [rows] fp32 (forward: NULL to skip)
+ */
+typedef enum { GDR_GATE_NONE = 0, GDR_GATE_CHANNEL = 1, GDR_GATE_TOKEN = 2 } gdr_gate_t;
+typedef struct {
+    int64_t rows, x_stride, residual_stride, gate_stride;
+    int32_t cols;           /* 1 to 16384                                                */
+    float eps;              /* >= 0                                                      */
+    float scale;            /* finite                                                    */
+    int32_t gate;           /* gdr_gate_t                                                */
+    int32_t io_dtype, param_dtype;
+    int32_t stream_dtype;   /* residual and h: io_dtype or GDR_F32                       */
+    int32_t out_dtype;      /* y: io_dtype or GDR_F32                                    */
+    int32_t dy_dtype;       /* backward: d_y (dense), io_dtype or GDR_F32                */
+    int32_t dh_dtype;       /* backward: d_h (dense), io_dtype or GDR_F32                */
+    int32_t grad_dtype;     /* backward: dx and a token gate's dgate, io_dtype or F32    */
+    int32_t dres_dtype;     /* backward: dresidual, io_dtype or GDR_F32                  */
+} gdr_residual_norm_problem_t;
+
+gdr_status_t gdr_residual_norm_fwd(const gdr_residual_norm_problem_t* problem, const void* x, const void* residual,
+                                   const void* weight, const void* x_weight, const void* gate, void* y, void* h,
+                                   float* rstd, float* x_rstd, void* stream);
+
+/* For dL/dy, dL/dh (d_h, NULL: zeros) and the forward's h, rstd and x_rstd (NULL
+ * without x_weight). dx, dresidual dense; dgate: as the gate, [rows, cols] in
+ * grad_dtype or [cols] fp32; dweight, dx_weight [cols] fp32 (NULL: skipped, as is dgate). */
+gdr_status_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_norm_problem_t* problem, size_t* bytes);
+gdr_status_t gdr_residual_norm_bwd(const gdr_residual_norm_problem_t* problem, const void* x, const void* h,
+                                   const void* d_y, const void* d_h, const void* weight, const void* x_weight,
+                                   const void* gate, const float* rstd, const float* x_rstd, void* dx, void* dresidual,
+                                   float* dweight, float* dx_weight, void* dgate, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
