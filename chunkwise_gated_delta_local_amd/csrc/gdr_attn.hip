@@ -9,18 +9,22 @@ namespace {
 
 // ---------------------------------------------------------------- softmax over tiles
 // What a lane keeps of its query: the output's dims 32 t + 8 i + 4 h + j in o[t][4 i + j],
-// the maximum of the raw scores that the weights refer to, and its half's sum of the weights.
+// the raw score m that the weights refer to and its product mc with c = scale log2(e) as
+// it was rounded, and its half's sum of the weights. Weights and sums share the rounding
+// of mc, so that it cancels in o.
 template <int DV>
 struct State {
     f32x16 o[DV / 32];
-    float m, l;
+    float m, mc, l;
     __device__ void clear() {
 #pragma unroll
         for (int t = 0; t < DV / 32; ++t) o[t] = zero16();
-        m = kNegInf;
+        m = mc = kNegInf;
         l = 0.f;
     }
 };
+// the factor from sums that refer to a to sums that refer to b >= a (either may be -inf)
+__device__ __forceinline__ float refer(float a, float b) { return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b); }
 
 // whether 16 bits or 32 bits (shifted past the sign) hold Inf or NaN
 __device__ __forceinline__ bool not_finite(const Vec<bf16>::v8& v) {
@@ -38,11 +42,12 @@ __device__ __forceinline__ bool not_finite(const Vec<float>::v8& v) {
 }
 
 // One tile of 32 NT keys, whose raw scores are s (overwritten by the weights) and
-// whose values lie in V. c = scale log2(e). partial: some query may not see some key.
+// whose values lie in V. partial: some query may not see some key.
 //
-// Weights are exp2(c (s - m)). m follows the maximum only when that has grown by more
-// than 8 in the exponent: weights then stay below 2^8 and the sums, in fp32, hardly
-// notice, while most tiles are spared the product of o with exp2(c (m - m_new)).
+// Weights are exp2(c s - mc). m follows the maximum only when that has grown by more
+// than 8 in the exponent: weights then stay below 2^9 and the sums, in fp32, hardly
+// notice, while most tiles are spared the product of o with the change. Beyond 2^24 the
+// rounding of mc reaches the exponent's units, and the difference is formed first.
 template <typename T, int DV, int NT>
 __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, float c, bool partial,
                                        const Sight& sees) {
@@ -60,22 +65,31 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][i]);
     top = pair_max(top);
-    const float m = fmaxf(st.m, top);
-    if (__any((m - st.m) * c > 8.f)) {
-        const float f = m == st.m ? 1.f : __builtin_amdgcn_exp2f((st.m - m) * c);
+    if (__any((top - st.m) * c > 8.f)) {
+        const float m = fmaxf(st.m, top), mc = m * c, f = refer(st.mc, mc);
         st.l *= f;
 #pragma unroll
         for (int t = 0; t < DV / 32; ++t) st.o[t] = st.o[t] * f;
         st.m = m;
+        st.mc = mc;
     }
-    const float mc = st.m == kNegInf ? 0.f : st.m * c;
+    const float mc = st.m == kNegInf ? 0.f : st.mc;
+    if (__any(fabsf(mc) > 16777216.f)) {
+        const float m = st.m == kNegInf ? 0.f : st.m;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[k][i] = __builtin_amdgcn_exp2f((s[k][i] - m) * c);
+    } else {
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], c, -mc));
+    }
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], c, -mc));
-            st.l += s[k][i];
-        }
+        for (int i = 0; i < 16; ++i) st.l += s[k][i];
     if (partial) {
         bool bad = false;
 #pragma unroll 1
@@ -147,7 +161,7 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, const Query& q, co
             else store4((T*)a.o + row * dv, d, dv, y);
         }
     if (a.lse && h == 0)
-        a.lse[row] = (st.m * (a.p.scale * kLog2e) + __builtin_amdgcn_logf(l)) * kLn2;
+        a.lse[row] = (st.mc + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- many rows
@@ -303,7 +317,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     // join the wavefronts: a common maximum, then one tile of 32 dims after another
     st.l = pair_sum(st.l);
     if (lane < 32) {
-        ml[w][0][lane] = st.m;
+        ml[w][0][lane] = st.mc;
         ml[w][1][lane] = st.l;
     }
     __syncthreads();
@@ -313,9 +327,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
         const float mi = ml[i][0][lane & 31], li = ml[i][1][lane & 31];
-        l += mi == m ? li : li * __builtin_amdgcn_exp2f((mi - m) * c);
+        l += li * refer(mi, m);
     }
-    const float f = st.m == m ? 1.f : __builtin_amdgcn_exp2f((st.m - m) * c);
+    const float f = refer(st.mc, m);
     const int64_t row = q.token * a.p.num_q_heads + q.head, rows = a.Ttot * a.p.num_q_heads;
     const int h = lane >> 5;
     float* part_o = a.ws + (int64_t)sp * rows * (dv + 2);
@@ -346,7 +360,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
             part_o[row * (dv + 2) + dv] = idle ? 0.f : m;
             part_o[row * (dv + 2) + dv + 1] = idle ? -1.f : l;
         } else if (a.lse) {
-            a.lse[row] = (m * c + __builtin_amdgcn_logf(l)) * kLn2;
+            a.lse[row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
         }
     }
 }
@@ -358,14 +372,13 @@ __global__ __launch_bounds__(256) void k_window_join(AttnArgs a, int splits) {
     const int64_t rows = a.Ttot * a.p.num_q_heads, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (row >= rows) return;
     const int dv = a.p.head_dim_v, lane = threadIdx.x & 63;
-    const float c = a.p.scale * kLog2e;
     const float* part = a.ws + row * (dv + 2);
     const int64_t step = rows * (dv + 2);
     float m = kNegInf, l = 0.f, y[2] = {0.f, 0.f};
     const bool idle = part[dv + 1] < 0.f;
     for (int i = 0; i < splits; ++i) m = fmaxf(m, part[i * step + dv]);
     for (int i = 0; i < splits; ++i) {
-        const float mi = part[i * step + dv], f = mi == m ? 1.f : __builtin_amdgcn_exp2f((mi - m) * c);
+        const float mi = part[i * step + dv], f = refer(mi, m);
         l = __builtin_fmaf(part[i * step + dv + 1], f, l);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -376,7 +389,7 @@ __global__ __launch_bounds__(256) void k_window_join(AttnArgs a, int splits) {
     for (int j = 0; j < 2; ++j)
         if (lane + 64 * j < dv)
             store_as<T>(a.o, row * dv + lane + 64 * j, idle ? 0.f : y[j] * inv, a.p.out_dtype == GDR_F32);
-    if (a.lse && lane == 0) a.lse[row] = (m * c + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && lane == 0) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- the new tokens into the caches
