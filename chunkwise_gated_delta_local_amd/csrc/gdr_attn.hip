@@ -26,33 +26,69 @@ struct State {
 // the factor from sums that refer to a to sums that refer to b >= a (either may be -inf)
 __device__ __forceinline__ float refer(float a, float b) { return a == b ? 1.f : __builtin_amdgcn_exp2f(a - b); }
 
-// whether 16 bits or 32 bits (shifted past the sign) hold Inf or NaN
-__device__ __forceinline__ bool not_finite(const Vec<bf16>::v8& v) {
-    const u32x4 w = __builtin_bit_cast(u32x4, v);
-    bool bad = false;
+// Whether a tile of N elements holds Inf or NaN, by a wavefront
+template <typename T, int N>
+__device__ __forceinline__ bool any_special(const T* tile) {
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int i = (int)(threadIdx.x & 63) * kUnit<T>; i < N; i += 64 * kUnit<T>) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+        for (int e = 0; e < 4; ++e) {
+            // without their signs; two elements of 16 bits compare as the upper halves do
+            const uint32_t a = x[e] & 0x7fffffffu, b = sizeof(T) == 2 ? x[e] << 16 & 0x7fffffffu : 0u;
+            top = top > a ? top : a;
+            top = top > b ? top : b;
+        }
+    }
+    return __any(top >= 0x7f800000u);
 }
-__device__ __forceinline__ bool not_finite(const Vec<float>::v8& v) {
-    bool bad = false;
+
+// A weight of zero does not stop an infinite or NaN v. Copies a tile of ROWS rows with
+// zeros for such elements (`to` may be `from`), by a wavefront, and returns the keys
+// that had one: the lane's key 8 i + 4 h + j of subtile k in bit 16 k + 4 i + j.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ uint32_t copy_finite(const T* from, T* to) {
+    constexpr int UN = D / kUnit<T>;                       // units (lanes) to a row
+    static_assert(UN <= 64 && 64 % UN == 0, "whole rows a step");
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    uint32_t lost = 0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < ROWS; r0 += 64 / UN) {
+        typename Raw<T, kUnit<T>>::type x = load_raw<T, kUnit<T>>(from + (r0 * UN + lane) * kUnit<T>);
+        bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= (__float_as_uint(v[i]) & 0x7f800000u) == 0x7f800000u;
-    return bad;
+        for (int e = 0; e < kUnit<T>; ++e) {
+            const bool ok = fabsf(to_f(x[e])) < __builtin_inff();
+            bad |= !ok;
+            x[e] = ok ? x[e] : to_t<T>(0.f);
+        }
+        store_raw<T, kUnit<T>>(to + (r0 * UN + lane) * kUnit<T>, x);
+        const uint64_t who = __ballot(bad);
+#pragma unroll
+        for (int k = 0; k < 64 / UN; ++k) {
+            const int key = r0 + k;
+            if ((who >> (k * UN)) << (64 - UN) && (key >> 2 & 1) == h)
+                lost |= 1u << (16 * (key >> 5) + 4 * (key >> 3 & 3) + (key & 3));
+        }
+    }
+    return lost;
 }
 
 // One tile of 32 NT keys, whose raw scores are s (overwritten by the weights) and
-// whose values lie in V. partial: some query may not see some key.
+// whose values lie in V. partial: some query may not see some key; the values are then
+// copied to `clean` first.
 //
 // Weights are exp2(c s - mc). m follows the maximum only when that has grown by more
 // than 8 in the exponent: weights then stay below 2^9 and the sums, in fp32, hardly
 // notice, while most tiles are spared the product of o with the change. Beyond 2^24 the
 // rounding of mc reaches the exponent's units, and the difference is formed first.
 template <typename T, int DV, int NT>
-__device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, float c, bool partial,
-                                       const Sight& sees) {
+__device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, T* clean, float c,
+                                       bool partial, const Sight& sees) {
     const int h = (threadIdx.x >> 5) & 1;
     if (partial) {
+        asm volatile("");                                  // a branch: most tiles are seen whole
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
@@ -63,7 +99,7 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][i]);
+        for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[k][i]);
     top = pair_max(top);
     if (__any((top - st.m) * c > 8.f)) {
         const float m = fmaxf(st.m, top), mc = m * c, f = refer(st.mc, mc);
@@ -90,40 +126,17 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
     for (int k = 0; k < NT; ++k)
 #pragma unroll
         for (int i = 0; i < 16; ++i) st.l += s[k][i];
-    if (partial) {
-        bool bad = false;
-#pragma unroll 1
-        for (int q = 0; q < 2 * NT; ++q)
+    if (partial && any_special<T, 32 * NT * DV>(V)) {
+        const uint32_t lost = copy_finite<T, DV, 32 * NT>(V, clean);
+        if (lost) {                                        // who sees such a key loses its sum
 #pragma unroll
-            for (int t = 0; t < DV / 32; ++t) bad |= not_finite(col_frag<DV>(V, 16 * q, 32 * t));
-        if (__any(bad)) {
-            // A weight of zero does not stop an infinite or NaN v: the product is made of
-            // the finite elements, and the queries that see another lose their sum.
+            for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int q = 0; q < 2 * NT; ++q) {
-                const auto w = acc_frag<T>(s[q >> 1], q & 1);
-                unsigned lost = 0;
-#pragma unroll
-                for (int t = 0; t < DV / 32; ++t) {
-                    auto v = col_frag<DV>(V, 16 * q, 32 * t);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const bool ok = fabsf(to_f(v[e])) < __builtin_inff();
-                        lost |= ok ? 0u : 1u << e;
-                        v[e] = ok ? v[e] : to_t<T>(0.f);
-                    }
-                    st.o[t] = mma(v, w, st.o[t]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint64_t who = __ballot(lost >> e & 1);      // one key in each half's lanes
-                    if ((uint32_t)(h ? who >> 32 : who) && sees(16 * q + 8 * (e >> 2) + 4 * h + (e & 3)))
+                for (int i = 0; i < 16; ++i)
+                    if ((lost >> (16 * k + i) & 1) && sees(32 * k + 8 * (i >> 2) + 4 * h + (i & 3)))
                         st.l = __builtin_nanf("");
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            return;
         }
+        V = clean;
     }
 #pragma unroll
     for (int k = 0; k < NT; ++k)
@@ -175,6 +188,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
     constexpr int KT = kTileKeys<T>, NT = KT / 32, KF = DK / (2 * kUnit<T>);
     __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK];
     __shared__ __attribute__((aligned(16))) T Vs[2][KT * DV];
+    // the finite values of a tile at an edge: all wavefronts that need it write the same
+    __shared__ __attribute__((aligned(16))) T Clean[KT * DV];
     // consecutive blocks of a key head on one XCD: their windows overlap
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
@@ -222,7 +237,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
 #pragma unroll
                 for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(Ks[cur], 32 * k, t), qf[t], s[k]);
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
-            absorb<T, DV, NT>(st, s, Vs[cur], c, partial, Sight{pos0, n, q.p, W, S});
+            absorb<T, DV, NT>(st, s, Vs[cur], Clean, c, partial, Sight{pos0, n, q.p, W, S});
         }
         if (cnt > 0) {
             sk.store(Ks[cur ^ 1], tid);
@@ -311,7 +326,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
             for (int t = 0; t < KF; ++t) s[0] = mma(kf[t], qf[t], s[0]);
             load_keys();
             const bool partial = n < 32 || pos0 + 31 > pa || (pos0 <= pb - W && pos0 + 32 > S);
-            absorb<T, DV, 1>(st, s, Vs[w], c, partial, Sight{pos0, n, q.p, W, S});
+            absorb<T, DV, 1>(st, s, Vs[w], Vs[w], c, partial, Sight{pos0, n, q.p, W, S});
         }
     }
     // join the wavefronts: a common maximum, then one tile of 32 dims after another
