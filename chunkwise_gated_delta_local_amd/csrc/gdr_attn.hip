@@ -86,7 +86,7 @@ __device__ __forceinline__ uint32_t copy_finite(const T* from, T* to) {
 template <typename T, int DV, int NT>
 __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, T* clean, float c,
                                        bool partial, const Sight& sees) {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
     if (partial) {
         asm volatile("");                                  // a branch: most tiles are seen whole
 #pragma unroll
@@ -144,7 +144,7 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
         for (int q = 0; q < 2; ++q) {
             const auto w = acc_frag<T>(s[k], q);
 #pragma unroll
-            for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<DV>(V, 32 * k + 16 * q, 32 * t), w, st.o[t]);
+            for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<DV>(V, 32 * k + 16 * q, 32 * t, lane), w, st.o[t]);
         }
 }
 
@@ -186,8 +186,7 @@ template <typename T> constexpr int kTileKeys = sizeof(T) == 2 ? 64 : 32;
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = kTileKeys<T>, NT = KT / 32, KF = DK / (2 * kUnit<T>);
-    __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK];
-    __shared__ __attribute__((aligned(16))) T Vs[2][KT * DV];
+    __shared__ __attribute__((aligned(16))) T K0[KT * DK], K1[KT * DK], V0[KT * DV], V1[KT * DV];
     // the finite values of a tile at an edge: all wavefronts that need it write the same
     __shared__ __attribute__((aligned(16))) T Clean[KT * DV];
     // consecutive blocks of a key head on one XCD: their windows overlap
@@ -209,24 +208,28 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
     const float c = a.p.scale * kLog2e;
 
     Keys keys(len + b.t0, len + b.t0 + b.tn - 1, len, W, S);
-    Stage<T, DK, KT, 64 * NW, VEC> sk;
-    Stage<T, DV, KT, 64 * NW, VEC> sv;
+    Copy<T, DK, KT, 64 * NW, VEC> ck;
+    Copy<T, DV, KT, 64 * NW, VEC> cv;
     int pos, cnt, row;
     bool cached;
-    auto fetch = [&] {
+    auto fetch = [&](T* K, T* V) {
         keys.next(KT, &pos, &cnt, &row, &cached);
         if (cnt == 0) return;
         const Source<T> s = source<T>(a, b, hk, row, cached);
-        sk.load(s.k, s.kld, cnt, dk, tid);
-        sv.load(s.v, s.vld, cnt, dv, tid);
+        ck.start(K, s.k, s.kld, cnt, dk, tid);
+        cv.start(V, s.v, s.vld, cnt, dv, tid);
     };
-    fetch();
-    sk.store(Ks[0], tid);
-    sv.store(Vs[0], tid);
-    __syncthreads();
-    for (int cur = 0; cnt > 0; cur ^= 1) {
+    auto land = [&](T* K, T* V) {
+        if (cnt > 0) {
+            ck.finish(K, tid);
+            cv.finish(V, tid);
+        }
+        __syncthreads();
+    };
+    // a tile in (K, V), the next one on its way to (Kn, Vn)
+    auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
         const int pos0 = pos, n = cnt;
-        fetch();
+        fetch(Kn, Vn);
         // some query of this wavefront sees a key of the tile
         if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
             f32x16 s[NT];
@@ -235,15 +238,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
 #pragma unroll
             for (int t = 0; t < KF; ++t)
 #pragma unroll
-                for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(Ks[cur], 32 * k, t), qf[t], s[k]);
+                for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, lane), qf[t], s[k]);
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
-            absorb<T, DV, NT>(st, s, Vs[cur], Clean, c, partial, Sight{pos0, n, q.p, W, S});
+            absorb<T, DV, NT>(st, s, V, Clean, c, partial, Sight{pos0, n, q.p, W, S});
         }
-        if (cnt > 0) {
-            sk.store(Ks[cur ^ 1], tid);
-            sv.store(Vs[cur ^ 1], tid);
-        }
-        __syncthreads();
+        land(Kn, Vn);
+    };
+    fetch(K0, V0);
+    land(K0, V0);
+    while (cnt > 0) {
+        turn(K0, V0, K1, V1);
+        if (cnt == 0) break;
+        turn(K1, V1, K0, V0);
     }
     store_rows<T, DV>(a, q, st, pair_sum(st.l));
 }
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     if (left > 0) {
         frag_t<T> qf[KF], kf[KF];
         load_query<T, DK, VEC>(a, q, qf);
-        Stage<T, DV, 32, 64, VEC> sv;
+        OwnCopy<T, DV, 32, VEC> sv;
         int pos = 0, cnt = 0, row = 0;
         bool cached = false;
         auto next = [&] {
@@ -311,14 +317,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
         };
         auto load_values = [&] {
             const Source<T> s = source<T>(a, b, hk, row, cached);
-            sv.load(s.v, s.vld, cnt, dv, lane);
+            sv.load(s.v, s.vld, cnt, dv);
         };
         next();
         load_keys();
         load_values();
         while (cnt > 0) {
             const int pos0 = pos, n = cnt;
-            sv.store(Vs[w], lane);
+            sv.store(Vs[w]);
             next();
             load_values();
             f32x16 s[1] = {zero16()};

@@ -195,10 +195,18 @@ struct Keys {
 };
 
 // ---------------------------------------------------------------- tiles
-// Rows of D elements in LDS, in 16-byte units; unit u of row lies at u ^ swz(row),
-// so that neither 8 rows' reads of one unit nor a transposing read of 4 rows meet
-// in the banks.
-__device__ __forceinline__ int swz(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
+// Rows of D elements in LDS, in UN 16-byte units; unit u of a row lies at u ^ swz(row).
+// The 64 banks give 256 bytes a cycle to accesses that spread over them: 16 rows' reads
+// of one unit (16 lanes of 16 bytes) and transposing reads of 4 rows (32 lanes of 8
+// bytes). For rows of 256 bytes swz takes 16 rows to 16 units, the 4 rows of a transposing
+// read to different groups of 4; of 128 bytes, every other row to 8 units. Cycles an
+// instruction with eight wavefronts, so and with 3 bits of the row's number: 16 bytes
+// 3.8 and 6.3, transposing 2.3 and 3.5.
+template <int UN>
+__device__ __forceinline__ int swz(int row) {
+    if constexpr (UN == 8) return (row >> 1 & 1) << 2 | (row >> 2 & 3);
+    else return (row & 3) << 2 | (row >> 2 & 3);
+}
 
 // A row's operand for a contraction over the head dimension
 template <typename T> struct Frag;
@@ -225,35 +233,43 @@ __device__ __forceinline__ f32x16 zero16() {
     return z;
 }
 
+// The lane's number as a value that the compiler does not know, so that it forms addresses
+// where they are used and does not keep them all in registers through a loop.
+__device__ __forceinline__ int fresh_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // row r0 + lane % 32, step t
 template <typename T, int D>
-__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t) {
-    const int lane = threadIdx.x & 63, row = r0 + (lane & 31);
-    return *reinterpret_cast<const frag_t<T>*>(tile + row * D + ((2 * t + (lane >> 5)) ^ swz(row)) * kUnit<T>);
+__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t, int lane) {
+    const int row = r0 + (lane & 31);
+    return *reinterpret_cast<const frag_t<T>*>(tile + row * D + ((2 * t + (lane >> 5)) ^ swz<D / kUnit<T>>(row)) * kUnit<T>);
 }
 // Operand of the transpose: row d0 + lane % 32 (a column of the tile), contracted
 // over the 16 tile rows r0 + 8 i + 4 h + j, i < 2
 template <int D>
-__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int d0) {
+__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int d0, int lane) {
     typedef __attribute__((address_space(3))) s16x4* lds_p;
-    const int lane = threadIdx.x & 63, l = lane & 15;
+    const int l = lane & 15;
     const int unit = (d0 + (lane & 16)) / 8 + (l >> 1 & 1);
     s16x4 x[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = r0 + 8 * i + 4 * (lane >> 5) + (l >> 2);
-        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(tile + row * D + (unit ^ swz(row)) * 8 + 4 * (l & 1)));
+        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(tile + row * D + (unit ^ swz<D / 8>(row)) * 8 + 4 * (l & 1)));
     }
     return __builtin_bit_cast(Vec<bf16>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int D>
-__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int d0) {
-    const int lane = threadIdx.x & 63, d = d0 + (lane & 31);
+__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int d0, int lane) {
+    const int d = d0 + (lane & 31);
     Vec<float>::v8 x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = r0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-        x[i] = tile[row * D + ((d >> 2) ^ swz(row)) * 4 + (d & 3)];
+        x[i] = tile[row * D + ((d >> 2) ^ swz<D / 4>(row)) * 4 + (d & 3)];
     }
     return x;
 }
@@ -271,11 +287,12 @@ __device__ __forceinline__ typename Vec<T>::v8 acc_frag(const f32x16& s, int q) 
     return x;
 }
 
+constexpr int kOutside = 0x7ffffff0;                       // bytes behind the end of every buffer
 // 16 bytes of a row through a range-checked buffer, zero from element d on; VEC:
 // rows begin and end at 16-byte addresses
 template <typename T, bool VEC>
 __device__ __forceinline__ u32x4 load_unit(__amdgpu_buffer_rsrc_t rs, int row_bytes, int unit, int d) {
-    constexpr int out = 0x7ffffff0;                          // behind every buffer
+    constexpr int out = kOutside;
     if constexpr (VEC) {
         return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                              rs, unit * kUnit<T> < d ? row_bytes + unit * 16 : out, 0, 0));
@@ -317,31 +334,61 @@ __device__ __forceinline__ frag_t<T> load_frag_row(const T* row, int unit, int d
     return x;
 }
 
-// `rows` rows of a tile on their way from memory to LDS through the registers of NT
-// threads; the copy is not waited for before it is stored.
+// ROWS rows of a tile on their way from memory to LDS, by NT threads: `start` issues the
+// loads, `finish` has them in LDS once the caller has waited at a barrier. With 16-byte
+// rows they go there directly, else through registers. A kernel keeps its two buffers
+// in two arrays and takes turns in its code, so that the compiler sees that reads of one
+// need not wait for loads into the other.
 template <typename T, int D, int ROWS, int NT, bool VEC>
-struct Stage {
+struct Copy {
     static constexpr int UN = D / kUnit<T>, N = ROWS * UN / NT;
-    static_assert(ROWS * UN % NT == 0, "whole units a thread");
-    u32x4 x[N];
+    static_assert(ROWS * UN % NT == 0 && NT % 64 == 0, "whole units a thread");
+    u32x4 x[VEC ? 1 : N];
     // row_at(row): its bytes behind base, of which `bytes` are valid
     template <typename F>
-    __device__ __forceinline__ void load(const T* base, uint32_t bytes, F row_at, int d, int tid) {
+    __device__ __forceinline__ void start(T* tile, const T* base, uint32_t bytes, F row_at, int d, int tid) {
         const auto rs = buf_rsrc(base, bytes);
+        const int first = __builtin_amdgcn_readfirstlane(tid) & ~63;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz(row);
-            x[i] = load_unit<T, VEC>(rs, row_at(row), unit, d);
+            const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz<UN>(row);
+            if constexpr (VEC)
+                buffer_to_lds16(rs, tile + (first + i * NT) * kUnit<T>, unit * kUnit<T> < d ? row_at(row) + unit * 16 : kOutside);
+            else x[i] = load_unit<T, VEC>(rs, row_at(row), unit, d);
         }
     }
-    __device__ __forceinline__ void load(const T* base, int ld, int rows, int d, int tid) {
+    __device__ __forceinline__ void start(T* tile, const T* base, int ld, int rows, int d, int tid) {
         const uint32_t row_bytes = (uint32_t)ld * sizeof(T);
-        load(base, rows > 0 ? (rows - 1) * row_bytes + d * (uint32_t)sizeof(T) : 0,
-             [&](int row) { return row * (int)row_bytes; }, d, tid);
+        start(tile, base, rows > 0 ? (rows - 1) * row_bytes + d * (uint32_t)sizeof(T) : 0,
+              [&](int row) { return row * (int)row_bytes; }, d, tid);
     }
-    __device__ __forceinline__ void store(T* tile, int tid) const {
+    __device__ __forceinline__ void finish(T* tile, int tid) const {
+        if constexpr (!VEC) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (tid + i * NT) * kUnit<T>) = x[i];
+            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (tid + i * NT) * kUnit<T>) = x[i];
+        }
+    }
+};
+// The same by one wavefront for itself, through registers: `load` early, `store` when the
+// tile before has been read.
+template <typename T, int D, int ROWS, bool VEC>
+struct OwnCopy {
+    static constexpr int UN = D / kUnit<T>, N = ROWS * UN / 64;
+    u32x4 x[N];
+    __device__ __forceinline__ void load(const T* base, int ld, int rows, int d) {
+        const uint32_t row_bytes = (uint32_t)ld * sizeof(T);
+        const auto rs = buf_rsrc(base, rows > 0 ? (rows - 1) * row_bytes + d * (uint32_t)sizeof(T) : 0);
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = lane + i * 64, row = id / UN, unit = (id % UN) ^ swz<UN>(row);
+            x[i] = load_unit<T, VEC>(rs, row * (int)row_bytes, unit, d);
+        }
+    }
+    __device__ __forceinline__ void store(T* tile) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<u32x4*>(tile + ((int)(threadIdx.x & 63) + i * 64) * kUnit<T>) = x[i];
     }
 };
 

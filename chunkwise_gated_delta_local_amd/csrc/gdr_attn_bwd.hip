@@ -76,8 +76,7 @@ __global__ __launch_bounds__(256) void k_window_rows_prep(AttnArgs a, int key_bl
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = KT / 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
-    __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK];
-    __shared__ __attribute__((aligned(16))) T Vs[2][KT * DV];
+    __shared__ __attribute__((aligned(16))) T K0[KT * DK], K1[KT * DK], V0[KT * DV], V1[KT * DV];
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
     const int hh = id / nblk, G = a.p.num_q_heads / a.p.num_kv_heads, hk = hh / rb.HC, hc = hh % rb.HC;
@@ -100,24 +99,27 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
     for (int t = 0; t < DK / 32; ++t) acc[t] = zero16();
 
     Keys keys(b.t0, b.t0 + b.tn - 1, 0, W, S);
-    Stage<T, DK, KT, 64 * NW, VEC> sk;
-    Stage<T, DV, KT, 64 * NW, VEC> sv;
+    Copy<T, DK, KT, 64 * NW, VEC> ck;
+    Copy<T, DV, KT, 64 * NW, VEC> cv;
     int pos, cnt, at;
     bool cached;
-    auto fetch = [&] {
+    auto fetch = [&](T* K, T* V) {
         keys.next(KT, &pos, &cnt, &at, &cached);
         if (cnt == 0) return;
         const Source<T> s = source<T>(a, b, hk, at, false);
-        sk.load(s.k, s.kld, cnt, dk, tid);
-        sv.load(s.v, s.vld, cnt, dv, tid);
+        ck.start(K, s.k, s.kld, cnt, dk, tid);
+        cv.start(V, s.v, s.vld, cnt, dv, tid);
     };
-    fetch();
-    sk.store(Ks[0], tid);
-    sv.store(Vs[0], tid);
-    __syncthreads();
-    for (int cur = 0; cnt > 0; cur ^= 1) {
-        const int pos0 = pos, n = cnt;
-        fetch();
+    auto land = [&](T* K, T* V) {
+        if (cnt > 0) {
+            ck.finish(K, tid);
+            cv.finish(V, tid);
+        }
+        __syncthreads();
+    };
+    auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
+        const int pos0 = pos, n = cnt, ln = fresh_lane();
+        fetch(Kn, Vn);
         if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
             const Sight sees{pos0, n, q.p, W, S};
@@ -125,9 +127,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
             for (int k = 0; k < NT; ++k) {
                 f32x16 s = zero16(), g = zero16();
 #pragma unroll
-                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(Ks[cur], 32 * k, t), qf[t], s);
+                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ln), qf[t], s);
 #pragma unroll
-                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(Vs[cur], 32 * k, t), gf[t], g);
+                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, ln), gf[t], g);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
@@ -139,15 +141,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
                 for (int e = 0; e < 2; ++e) {
                     const auto x = acc_frag<T>(s, e);
 #pragma unroll
-                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(Ks[cur], 32 * k + 16 * e, 32 * t), x, acc[t]);
+                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(K, 32 * k + 16 * e, 32 * t, ln), x, acc[t]);
                 }
             }
         }
-        if (cnt > 0) {
-            sk.store(Ks[cur ^ 1], tid);
-            sv.store(Vs[cur ^ 1], tid);
-        }
-        __syncthreads();
+        land(Kn, Vn);
+    };
+    fetch(K0, V0);
+    land(K0, V0);
+    while (cnt > 0) {
+        turn(K0, V0, K1, V1);
+        if (cnt == 0) break;
+        turn(K1, V1, K0, V0);
     }
     if (!q.live) return;
 #pragma unroll
@@ -164,15 +169,20 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
 }
 
 // ---------------------------------------------------------------- dk, dv
-// A wavefront owns 32 keys (a lane a key), with their k and v as operands and the
-// sums of dk and dv in registers; the queries' tiles go through LDS. Work numbers
-// from `main` on are the runs of queries that see sinks alone.
+constexpr int kQueryTile = 32;
+
+// A wavefront owns 32 keys (a lane a key), with their k as operand and the sums of dk
+// and dv in registers; the queries' tiles go through LDS. v is an operand in registers
+// too (fp32), or lies in LDS, so that two wavefronts fit a SIMD (bf16). Work numbers from
+// `main` on are the runs of queries that see sinks alone.
 template <typename T, int DK, int DV, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, 1) void k_window_dkv(AttnArgs a, RowBlock rb, int nblk, int main, int nwork) {
-    constexpr int QT = sizeof(T) == 2 ? 64 : 32, KB = 32 * NW, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
-    __shared__ __attribute__((aligned(16))) T Qs[2][QT * DK];
-    __shared__ __attribute__((aligned(16))) T Gs[2][QT * DV];
-    __shared__ __attribute__((aligned(16))) float Rs[2][2][QT];
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(AttnArgs a, RowBlock rb, int nblk,
+                                                                                int main, int nwork) {
+    constexpr int QT = kQueryTile, KB = 32 * NW, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
+    constexpr bool VLDS = sizeof(T) == 2;
+    __shared__ __attribute__((aligned(16))) T Vk[VLDS ? KB * DV : 1];
+    __shared__ __attribute__((aligned(16))) T Q0[QT * DK], Q1[QT * DK], G0[QT * DV], G1[QT * DV];
+    __shared__ __attribute__((aligned(16))) float R0[2 * QT], R1[2 * QT];      // lse of the rows, then delta
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
     const int Nk = a.p.num_kv_heads, G = a.p.num_q_heads / Nk, W = a.p.window, S = a.p.sinks;
@@ -222,120 +232,139 @@ __global__ __launch_bounds__(64 * NW, 1) void k_window_dkv(AttnArgs a, RowBlock 
         slot = u;
     }
     const int mine = b.t0 + 32 * w + (lane & 31);                  // the lane's key
+    const unsigned mine_for = mine < S ? 0x7fffffffu : (unsigned)W; // tokens that see it, itself the first
     const int ja = b.t0 + 32 * w, jb = ja + 31 < b.t0 + keys - 1 ? ja + 31 : b.t0 + keys - 1;
     const bool live = mine < b.t0 + keys;
     const float c = a.p.scale * kLog2e;
-    frag_t<T> kf[KF], vf[VF];
+    frag_t<T> kf[KF], vf[VLDS ? 1 : VF];
     {
         const int64_t tok = b.start + (live ? mine : b.t0);
+        const T* vrow = (const T*)a.v + (int64_t)hk * dv;
 #pragma unroll
         for (int t = 0; t < KF; ++t)
             kf[t] = load_frag_row<T, VEC>((const T*)a.k + tok * a.p.k_stride + (int64_t)hk * dk, 2 * t + h, dk, live);
+        if constexpr (VLDS) {
+            Copy<T, DV, KB, 64 * NW, VEC> cv;
+            cv.start(Vk, vrow + (b.start + b.t0) * a.p.v_stride, a.v_ld, keys, dv, tid);
+            cv.finish(Vk, tid);
+        } else {
 #pragma unroll
-        for (int t = 0; t < VF; ++t)
-            vf[t] = load_frag_row<T, VEC>((const T*)a.v + tok * a.p.v_stride + (int64_t)hk * dv, 2 * t + h, dv, live);
+            for (int t = 0; t < VF; ++t) vf[t] = load_frag_row<T, VEC>(vrow + tok * a.p.v_stride, 2 * t + h, dv, live);
+        }
     }
+    auto v_frag = [&](int t, int ln) {
+        if constexpr (VLDS) return row_frag<T, DV>(Vk, 32 * w, t, ln);
+        else return vf[t];
+    };
     f32x16 dK[DK / 32], dV[DV / 32];
 #pragma unroll
     for (int t = 0; t < DK / 32; ++t) dK[t] = zero16();
 #pragma unroll
     for (int t = 0; t < DV / 32; ++t) dV[t] = zero16();
 
-    // row r of a tile: token r / HPB, head r % HPB
+    // row r of a tile: token r / HPB, head r % HPB. Rows that are not there come as zeros
+    // and add nothing.
     const int magic = (65536 + rb.HPB - 1) / rb.HPB;               // r / HPB = r magic / 65536 for r < 256
-    const int span = rb.HPB * rb.TPB;
-    Stage<T, DK, QT, 64 * NW, VEC> sq;
-    Stage<T, DV, QT, 64 * NW, VEC> sg;
-    float r0 = 0.f, r1 = 0.f;
-    int t = ta, hc = 0, t_now = ta, n_now = 0;
+    const int span = rb.HPB * rb.TPB, Nq = a.p.num_q_heads;
+    auto row_at = [&](int r, int ld, int d) {
+        const int x = (r * magic) >> 16, g = r - x * rb.HPB;
+        return r < span ? (x * ld + g * d) * (int)sizeof(T) : kOutside;
+    };
+    Copy<T, DK, QT, 64 * NW, VEC> cq;
+    Copy<T, DV, QT, 64 * NW, VEC> cg;
+    int t = ta, hc = 0, p0 = ta, p1 = ta;
     bool more = true;
-    auto fetch = [&] {
+    auto fetch = [&](T* Q, T* Gr, float* R) {
         more = t < te;
         if (!more) return;
         const int n = te - t < rb.TPB ? te - t : rb.TPB, heads = G - hc * rb.HPB < rb.HPB ? G - hc * rb.HPB : rb.HPB;
         const int64_t tok = b.start + t;
-        const int head = hk * G + hc * rb.HPB;
-        constexpr int out = 0x7ffffff0;
-        const int q_ld = a.q_ld, g_ld = a.p.num_q_heads * dv;
-        sq.load((const T*)a.q + tok * a.p.q_stride + (int64_t)head * dk,
-                (uint32_t)((n - 1) * q_ld + heads * dk) * sizeof(T), [&](int r) {
-                    const int x = (r * magic) >> 16, g = r - x * rb.HPB;
-                    return r < span && x < n && g < heads ? (x * q_ld + g * dk) * (int)sizeof(T) : out;
-                }, dk, tid);
-        sg.load((const T*)a.d_o + (tok * a.p.num_q_heads + head) * dv,
-                (uint32_t)((n - 1) * g_ld + heads * dv) * sizeof(T), [&](int r) {
-                    const int x = (r * magic) >> 16, g = r - x * rb.HPB;
-                    return r < span && x < n && g < heads ? (x * g_ld + g * dv) * (int)sizeof(T) : out;
-                }, dv, tid);
-        if (tid < QT) {
-            const int x = (tid * magic) >> 16, g = tid - x * rb.HPB;
-            const bool in = tid < span && x < n && g < heads;
-            const float* p = a.rows + 2 * ((tok + (in ? x : 0)) * a.p.num_q_heads + head + (in ? g : 0));
-            r0 = in ? p[0] : __builtin_inff();                     // a row that is not there weighs nothing
-            r1 = in ? p[1] : 0.f;
+        const int head = hk * G + hc * rb.HPB, g_ld = Nq * dv;
+        cq.start(Q, (const T*)a.q + tok * a.p.q_stride + (int64_t)head * dk,
+                 (uint32_t)((n - 1) * a.q_ld + heads * dk) * sizeof(T), [&](int r) { return row_at(r, a.q_ld, dk); }, dk, tid);
+        cg.start(Gr, (const T*)a.d_o + (tok * Nq + head) * dv, (uint32_t)((n - 1) * g_ld + heads * dv) * sizeof(T),
+                 [&](int r) { return row_at(r, g_ld, dv); }, dv, tid);
+        if (w == 0) {
+            const int r = lane & 31, x = (r * magic) >> 16, g = r - x * rb.HPB;
+            static_assert(QT == 32, "lse and delta of a tile in 64 lanes");
+            buffer_to_lds4(buf_rsrc(a.rows + 2 * (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 8), R,
+                           r < span ? (x * Nq + g) * 8 + 4 * h : kOutside);
         }
-        t_now = t;
-        n_now = n;
+        p0 = t;
+        p1 = t + n - 1;
         if (++hc == rb.HC) {
             hc = 0;
             t += rb.TPB;
         }
     };
-    auto put = [&](int buf) {
-        sq.store(Qs[buf], tid);
-        sg.store(Gs[buf], tid);
-        if (tid < QT) {
-            Rs[buf][0][tid] = r0;
-            Rs[buf][1][tid] = r1;
+    auto land = [&](T* Q, T* Gr) {
+        if (more) {
+            cq.finish(Q, tid);
+            cg.finish(Gr, tid);
         }
+        __syncthreads();
     };
-    fetch();
-    if (more) put(0);
-    __syncthreads();
-    for (int cur = 0; more; cur ^= 1) {
-        const int p0 = t_now, p1 = t_now + n_now - 1;
-        fetch();
-        if (ja <= jb && p1 >= ja && (ja < S || p0 <= jb + (int64_t)W - 1)) {
-            const bool partial = p0 < jb || (p1 - W >= ja && jb >= S);
+    auto turn = [&](const T* Q, const T* Gr, const float* R, T* Qn, T* Gn, float* Rn) {
+        const int a0 = p0, a1 = p1, ln = fresh_lane();             // the queries' positions
+        fetch(Qn, Gn, Rn);
+        if (ja <= jb && a1 >= ja && (ja < S || a0 <= jb + (int64_t)W - 1)) {
+            const bool partial = a0 < jb || (a1 - W >= ja && jb >= S);
+            // one product after the other: what each needs in registers leaves room for two wavefronts a SIMD
+            f32x16 s = zero16(), g = zero16();
 #pragma unroll
-            for (int k = 0; k < QT / 32; ++k) {
-                f32x16 s = zero16(), g = zero16();
+            for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Q, 0, u, ln), kf[u], s);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Qs[cur], 32 * k, u), kf[u], s);
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 L = *reinterpret_cast<const f32x4*>(&R[8 * i + 4 * h]);
 #pragma unroll
-                for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gs[cur], 32 * k, u), vf[u], g);
+                for (int j = 0; j < 4; ++j)
+                    s[4 * i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
+            }
+            if (partial) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 L = *reinterpret_cast<const f32x4*>(&Rs[cur][0][32 * k + 8 * i + 4 * h]);
-                    const f32x4 D = *reinterpret_cast<const f32x4*>(&Rs[cur][1][32 * k + 8 * i + 4 * h]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
-                        s[4 * i + j] = p;
-                        g[4 * i + j] = p * (g[4 * i + j] - D[j]);
-                    }
-                }
-                if (partial) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 32 * k + 8 * (i >> 2) + 4 * h + (i & 3), p = p0 + ((r * magic) >> 16);
-                        const bool see = p >= mine && (mine < S || p - mine < W);
-                        s[i] = see ? s[i] : 0.f;
-                        g[i] = see ? g[i] : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const auto x = acc_frag<T>(s, e), y = acc_frag<T>(g, e);
-#pragma unroll
-                    for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gs[cur], 32 * k + 16 * e, 32 * u), x, dV[u]);
-#pragma unroll
-                    for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Qs[cur], 32 * k + 16 * e, 32 * u), y, dK[u]);
+                for (int i = 0; i < 16; ++i) {
+                    const int r = 8 * (i >> 2) + 4 * h + (i & 3), p = a0 + ((r * magic) >> 16);
+                    s[i] = (unsigned)(p - mine) < mine_for ? s[i] : 0.f;
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto x = acc_frag<T>(s, e);
+#pragma unroll
+                for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gr, 16 * e, 32 * u, ln), x, dV[u]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, ln), v_frag(u, ln), g);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 D = *reinterpret_cast<const f32x4*>(&R[QT + 8 * i + 4 * h]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // a NaN of a query that does not see the key stays out
+                    const float x = s[4 * i + j] * (g[4 * i + j] - D[j]);
+                    g[4 * i + j] = partial && s[4 * i + j] == 0.f ? 0.f : x;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto y = acc_frag<T>(g, e);
+#pragma unroll
+                for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Q, 16 * e, 32 * u, ln), y, dK[u]);
+            }
         }
-        if (more) put(cur ^ 1);
-        __syncthreads();
+        land(Qn, Gn);
+    };
+    fetch(Q0, G0, R0);
+    land(Q0, G0);
+    while (more) {
+        turn(Q0, G0, R0, Q1, G1, R1);
+        if (!more) break;
+        turn(Q1, G1, R1, Q0, G0, R0);
     }
     if (!live) return;
     const bool to_slot = slot >= 0 && mine < S;
@@ -443,7 +472,7 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
     by_dims(a.p, [&](auto type, auto dk, auto dv) {
         typedef decltype(type) T;
         constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NQ = 8, NK = 4, KB = 32 * NK;
-        constexpr int QT = sizeof(T) == 2 ? 64 : 32;
+        constexpr int QT = kQueryTile;
         const RowBlock rq = row_block(32 * NQ, G), rk = row_block(QT, G);
         const int64_t bq = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, rq.TPB), wq = bq * Nk * rq.HC;
         const int64_t bk = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, KB), wm = bk * Nk;
