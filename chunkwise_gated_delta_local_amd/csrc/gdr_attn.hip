@@ -87,6 +87,7 @@ template <typename T, int DV, int NT>
 __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, T* clean, float c,
                                        bool partial, const Sight& sees) {
     const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int co = fresh(col_offset<T, DV>(lane));
     if (partial) {
         asm volatile("");                                  // a branch: most tiles are seen whole
 #pragma unroll
@@ -144,7 +145,7 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
         for (int q = 0; q < 2; ++q) {
             const auto w = acc_frag<T>(s[k], q);
 #pragma unroll
-            for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<DV>(V, 32 * k + 16 * q, 32 * t, lane), w, st.o[t]);
+            for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<DV>(V, 32 * k + 16 * q, t, co), w, st.o[t]);
         }
 }
 
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
     };
     // a tile in (K, V), the next one on its way to (Kn, Vn)
     auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
-        const int pos0 = pos, n = cnt;
+        const int pos0 = pos, n = cnt, ro = fresh(row_offset<T, DK>(lane));
         fetch(Kn, Vn);
         // some query of this wavefront sees a key of the tile
         if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
 #pragma unroll
             for (int t = 0; t < KF; ++t)
 #pragma unroll
-                for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, lane), qf[t], s[k]);
+                for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s[k]);
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
             absorb<T, DV, NT>(st, s, V, Clean, c, partial, Sight{pos0, n, q.p, W, S});
         }

@@ -233,44 +233,57 @@ __device__ __forceinline__ f32x16 zero16() {
     return z;
 }
 
-// The lane's number as a value that the compiler does not know, so that it forms addresses
-// where they are used and does not keep them all in registers through a loop.
-__device__ __forceinline__ int fresh_lane() {
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    return lane;
+// A lane's byte offsets into a tile of rows of D elements, for the operands below: what
+// an access adds to them is known when the kernel is compiled, a bitwise sum of unit
+// numbers (the swizzle is one) and a number of rows.
+template <typename T, int D>
+__device__ __forceinline__ int row_offset(int lane) {
+    const int row = lane & 31;
+    return row * D * (int)sizeof(T) + (((lane >> 5) ^ swz<D / kUnit<T>>(row)) << 4);
+}
+template <typename T, int D>
+__device__ __forceinline__ int col_offset(int lane) {
+    const int h = lane >> 5, l = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+        const int row = 4 * h + (l >> 2), unit = (lane >> 3 & 2) | (l >> 1 & 1);
+        return row * D * 2 + ((unit ^ swz<D / 8>(row)) << 4) + 8 * (l & 1);
+    } else {
+        return 4 * h * D * 4 + (((lane & 31) >> 2 ^ swz<D / 4>(4 * h)) << 4) + 4 * (lane & 3);
+    }
+}
+// A value that the compiler does not know: addresses are then formed where they are used
+// and not all kept in registers through a loop.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
-// row r0 + lane % 32, step t
+// row r0 + lane % 32 (r0 a multiple of 32), step t; off: row_offset
 template <typename T, int D>
-__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t, int lane) {
-    const int row = r0 + (lane & 31);
-    return *reinterpret_cast<const frag_t<T>*>(tile + row * D + ((2 * t + (lane >> 5)) ^ swz<D / kUnit<T>>(row)) * kUnit<T>);
+__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t, int off) {
+    return *reinterpret_cast<const frag_t<T>*>(reinterpret_cast<const char*>(tile) + (off ^ (t << 5)) +
+                                               r0 * D * (int)sizeof(T));
 }
-// Operand of the transpose: row d0 + lane % 32 (a column of the tile), contracted
-// over the 16 tile rows r0 + 8 i + 4 h + j, i < 2
+// Operand of the transpose: row 32 u + lane % 32 (a column of the tile), contracted over
+// the 16 tile rows r0 + 8 i + 4 h + j, i < 2 (r0 a multiple of 16); off: col_offset
 template <int D>
-__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int d0, int lane) {
+__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int u, int off) {
     typedef __attribute__((address_space(3))) s16x4* lds_p;
-    const int l = lane & 15;
-    const int unit = (d0 + (lane & 16)) / 8 + (l >> 1 & 1);
     s16x4 x[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = r0 + 8 * i + 4 * (lane >> 5) + (l >> 2);
-        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(tile + row * D + (unit ^ swz<D / 8>(row)) * 8 + 4 * (l & 1)));
-    }
+    for (int i = 0; i < 2; ++i)
+        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(reinterpret_cast<const char*>(tile) +
+                                                               (off ^ (u << 6 | i << 5)) + (r0 + 8 * i) * D * 2));
     return __builtin_bit_cast(Vec<bf16>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int D>
-__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int d0, int lane) {
-    const int d = d0 + (lane & 31);
+__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int u, int off) {
     Vec<float>::v8 x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = r0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-        x[i] = tile[row * D + ((d >> 2) ^ swz<D / 4>(row)) * 4 + (d & 3)];
-    }
+    for (int i = 0; i < 8; ++i)
+        x[i] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(tile) +
+                                               (off ^ (u << 7 ^ (i & 3) << 6 ^ (i >> 2) << 5)) +
+                                               (r0 + 8 * (i >> 2) + (i & 3)) * D * 4);
     return x;
 }
 __device__ __forceinline__ f32x16 mma(const Vec<float>::v8& a, const Vec<float>::v8& b, f32x16 c) {

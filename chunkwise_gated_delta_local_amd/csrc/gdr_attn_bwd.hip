@@ -118,7 +118,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
         __syncthreads();
     };
     auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
-        const int pos0 = pos, n = cnt, ln = fresh_lane();
+        const int pos0 = pos, n = cnt;
+        const int ro = fresh(row_offset<T, DK>(lane)), rv = DK == DV ? ro : fresh(row_offset<T, DV>(lane)),
+                  co = fresh(col_offset<T, DK>(lane));
         fetch(Kn, Vn);
         if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
@@ -127,9 +129,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
             for (int k = 0; k < NT; ++k) {
                 f32x16 s = zero16(), g = zero16();
 #pragma unroll
-                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ln), qf[t], s);
+                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s);
 #pragma unroll
-                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, ln), gf[t], g);
+                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, rv), gf[t], g);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
                 for (int e = 0; e < 2; ++e) {
                     const auto x = acc_frag<T>(s, e);
 #pragma unroll
-                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(K, 32 * k + 16 * e, 32 * t, ln), x, acc[t]);
+                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(K, 32 * k + 16 * e, t, co), x, acc[t]);
                 }
             }
         }
@@ -183,8 +185,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
     __shared__ __attribute__((aligned(16))) T Vk[VLDS ? KB * DV : 1];
     __shared__ __attribute__((aligned(16))) T Q0[QT * DK], Q1[QT * DK], G0[QT * DV], G1[QT * DV];
     __shared__ __attribute__((aligned(16))) float R0[2 * QT], R1[2 * QT];      // lse of the rows, then delta
-    const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
+    // consecutive key blocks of a head on one XCD; the runs are dealt to all of them
+    const int per = (main + 7) / 8, at = (int)(blockIdx.x >> 3);
+    const int id = at < per ? (int)(blockIdx.x & 7) * per + at : (int)blockIdx.x - 8 * per + main;
+    if (id >= nwork || (at < per && id >= main)) return;
     const int Nk = a.p.num_kv_heads, G = a.p.num_q_heads / Nk, W = a.p.window, S = a.p.sinks;
     const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v;
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
@@ -252,8 +256,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             for (int t = 0; t < VF; ++t) vf[t] = load_frag_row<T, VEC>(vrow + tok * a.p.v_stride, 2 * t + h, dv, live);
         }
     }
-    auto v_frag = [&](int t, int ln) {
-        if constexpr (VLDS) return row_frag<T, DV>(Vk, 32 * w, t, ln);
+    auto v_frag = [&](int t, int off) {
+        if constexpr (VLDS) return row_frag<T, DV>(Vk, 32 * w, t, off);
         else return vf[t];
     };
     f32x16 dK[DK / 32], dV[DV / 32];
@@ -305,14 +309,16 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
         __syncthreads();
     };
     auto turn = [&](const T* Q, const T* Gr, const float* R, T* Qn, T* Gn, float* Rn) {
-        const int a0 = p0, a1 = p1, ln = fresh_lane();             // the queries' positions
+        const int a0 = p0, a1 = p1;                                // the queries' positions
+        const int rq = fresh(row_offset<T, DK>(lane)), rg = DK == DV ? rq : fresh(row_offset<T, DV>(lane));
+        const int cq_ = fresh(col_offset<T, DK>(lane)), cg_ = DK == DV ? cq_ : fresh(col_offset<T, DV>(lane));
         fetch(Qn, Gn, Rn);
         if (ja <= jb && a1 >= ja && (ja < S || a0 <= jb + (int64_t)W - 1)) {
             const bool partial = a0 < jb || (a1 - W >= ja && jb >= S);
             // one product after the other: what each needs in registers leaves room for two wavefronts a SIMD
             f32x16 s = zero16(), g = zero16();
 #pragma unroll
-            for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Q, 0, u, ln), kf[u], s);
+            for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Q, 0, u, rq), kf[u], s);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -333,28 +339,29 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             for (int e = 0; e < 2; ++e) {
                 const auto x = acc_frag<T>(s, e);
 #pragma unroll
-                for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gr, 16 * e, 32 * u, ln), x, dV[u]);
+                for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gr, 16 * e, u, cg_), x, dV[u]);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, ln), v_frag(u, ln), g);
+            for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, rg), v_frag(u, rg), g);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 D = *reinterpret_cast<const f32x4*>(&R[QT + 8 * i + 4 * h]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // a NaN of a query that does not see the key stays out
-                    const float x = s[4 * i + j] * (g[4 * i + j] - D[j]);
-                    g[4 * i + j] = partial && s[4 * i + j] == 0.f ? 0.f : x;
-                }
+                for (int j = 0; j < 4; ++j) g[4 * i + j] = s[4 * i + j] * (g[4 * i + j] - D[j]);
+            }
+            if (partial) {                                         // what a key does not see may be NaN
+                asm volatile("");
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = s[i] == 0.f ? 0.f : g[i];
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const auto y = acc_frag<T>(g, e);
 #pragma unroll
-                for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Q, 16 * e, 32 * u, ln), y, dK[u]);
+                for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Q, 16 * e, u, cq_), y, dK[u]);
             }
         }
         land(Qn, Gn);
@@ -438,7 +445,8 @@ Plan plan_of(const gdr_attn_problem_t& p) {
     const int64_t T = p.batch * p.seq_len, W = p.window;
     x.rows = up((size_t)T * p.num_q_heads * 8);
     if (p.do_dtype != p.io_dtype) x.d_o16 = up((size_t)T * p.num_q_heads * p.head_dim_v * size_of(p.io_dtype));
-    x.run = (int)(W < 512 ? 512 : W < 4096 ? W : 4096);
+    const int64_t run = p.seq_len / 64;
+    x.run = (int)(run < 256 ? 256 : run < 4096 ? run : 4096);
     if (p.sinks > 0 && T > W) {
         const int64_t longer = T / (W + 1);                        // sequences that can be longer than a window
         x.slots = T / x.run + 2 * (longer < p.num_seqs ? longer : p.num_seqs) + 1;
@@ -484,7 +492,7 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
         const int64_t rows = (a.Ttot * a.p.num_q_heads + 15) / 16, most = 8192;
         k_window_rows_prep<T><<<dim3((unsigned)((rows < most ? rows : most) + 1)), 256, 0, a.stream>>>(a, KB);
         if (a.d_o16) a.d_o = a.d_o16;
-        const dim3 gq((unsigned)((wq + 7) / 8 * 8)), gk((unsigned)((wk + 7) / 8 * 8));
+        const dim3 gq((unsigned)((wq + 7) / 8 * 8)), gk((unsigned)((wm + 7) / 8 * 8 + wk - wm));
         auto go = [&](auto vec) {
             constexpr bool VEC = decltype(vec)::value;
             k_window_dkv<T, DK, DV, NK, VEC><<<gk, 64 * NK, 0, a.stream>>>(a, rk, (int)bk, (int)wm, (int)wk);
