@@ -415,13 +415,23 @@ __global__ __launch_bounds__(256) void k_window_join(AttnArgs a, int splits) {
 }
 
 // ---------------------------------------------------------------- the new tokens into the caches
-// After the attention has read them. A workgroup takes tokens of all sequences in
-// turn; of a sequence, those that are sinks and the last `window` of the others.
-template <typename T>
+// After the attention has read them, a wavefront a token: the sinks, and the last
+// `window` of a sequence's other tokens.
+template <typename T, bool VEC>
+__device__ __forceinline__ void copy_row(T* to, const T* from, int n) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (VEC) {
+        for (int i = lane * kUnit<T>; i < n; i += 64 * kUnit<T>)
+            *reinterpret_cast<u32x4*>(to + i) = *reinterpret_cast<const u32x4*>(from + i);
+    } else {
+        for (int i = lane; i < n; i += 64) to[i] = from[i];
+    }
+}
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_window_keep(AttnArgs a) {
     const int W = a.p.window, S = a.p.sinks, Nk = a.p.num_kv_heads;
     const int kw = Nk * a.p.head_dim_qk, vw = Nk * a.p.head_dim_v;
-    for (int64_t t = blockIdx.x; t < a.Ttot; t += gridDim.x) {
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.Ttot; t += (int64_t)gridDim.x * 4) {
         const int n = seq_of_token(a.cu, a.p.num_seqs, a.p.seq_len, t);
         int64_t s, e;
         seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
@@ -429,9 +439,8 @@ __global__ __launch_bounds__(256) void k_window_keep(AttnArgs a) {
         const int len = past_len(a, n), p = len + (int)(t - s);
         if (p >= S && e - t > W) continue;
         const int64_t at = (int64_t)n * ((int64_t)S + W) + (p < S ? p : S + (p - S) % W);
-        const T *k = (const T*)a.k + t * a.p.k_stride, *v = (const T*)a.v + t * a.p.v_stride;
-        for (int i = threadIdx.x; i < kw; i += 256) ((T*)a.kc)[at * kw + i] = k[i];
-        for (int i = threadIdx.x; i < vw; i += 256) ((T*)a.vc)[at * vw + i] = v[i];
+        copy_row<T, VEC>((T*)a.kc + at * kw, (const T*)a.k + t * a.p.k_stride, kw);
+        copy_row<T, VEC>((T*)a.vc + at * vw, (const T*)a.v + t * a.p.v_stride, vw);
     }
 }
 
@@ -502,8 +511,10 @@ hipError_t launch_attn_fwd(const AttnArgs& a) {
         }
         e = hipGetLastError();
         if (e == hipSuccess && a.kc && !a.one) {
-            const int64_t most = 4096;
-            k_window_keep<T><<<dim3((unsigned)(a.Ttot < most ? a.Ttot : most)), 256, 0, a.stream>>>(a);
+            const int64_t need = (a.Ttot + 3) / 4, most = 8192;
+            const dim3 grid((unsigned)(need < most ? need : most));
+            if (a.vec) k_window_keep<T, true><<<grid, 256, 0, a.stream>>>(a);
+            else k_window_keep<T, false><<<grid, 256, 0, a.stream>>>(a);
             e = hipGetLastError();
         }
     });

@@ -5,7 +5,8 @@
 //
 // The scores are formed again, twice: k_window_dq walks the keys of a block of
 // queries, k_window_dkv the queries of a block of keys, each summing what it
-// owns in registers, so that no sum crosses workgroups and its order is fixed.
+// owns in registers, so that no sum crosses workgroups and its order is fixed. The
+// first also forms delta and leaves it for the second.
 // The first tokens alone are seen by queries of the whole sequence: those behind
 // the ones that a key block meets anyway are shared out in runs of sink_run tokens,
 // whose sums go to slots in memory and are added up by k_window_sinks.
@@ -15,59 +16,43 @@ namespace gdr {
 
 namespace {
 
-// ---------------------------------------------------------------- per row: lse and delta
-// 16 lanes a row of up to 128 elements. The last workgroup counts the slots instead.
-template <typename T>
-__global__ __launch_bounds__(256) void k_window_rows_prep(AttnArgs a, int key_block) {
-    if (blockIdx.x == gridDim.x - 1) {
-        if (threadIdx.x >= 64 || !a.slots) return;
-        int base = 0;
-        for (int n0 = 0; n0 <= a.p.num_seqs; n0 += 64) {
-            const int n = n0 + (int)threadIdx.x;
-            int m = 0;
-            if (n < a.p.num_seqs) {
-                int64_t s, e;
-                seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
-                // tokens behind all that the sinks' key blocks meet, in runs; and a slot for those blocks' own sums
-                const int64_t behind = e - s - a.p.window;
-                if (behind > 0) m = (int)((behind + a.sink_run - 1) / a.sink_run) + 1;
-            }
-            int sum = m;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int x = __shfl_up(sum, d, 64);
-                if ((int)threadIdx.x >= d) sum += x;
-            }
-            const int first = base + sum - m;
-            if (n <= a.p.num_seqs) a.slots[n] = first < a.max_slots ? first : a.max_slots;
-            base += __shfl(sum, 63, 64);
+// First slot of each sequence, by one wavefront: a slot for the own sums of the key blocks
+// with sinks, and one for each run of sink_run tokens behind a window.
+__device__ void count_slots(const AttnArgs& a) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int n0 = 0; n0 <= a.p.num_seqs; n0 += 64) {
+        const int n = n0 + lane;
+        int m = 0;
+        if (n < a.p.num_seqs) {
+            int64_t s, e;
+            seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
+            const int64_t behind = e - s - a.p.window;
+            if (behind > 0) m = (int)((behind + a.sink_run - 1) / a.sink_run) + 1;
         }
-        return;
+        int sum = m;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int x = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += x;
+        }
+        const int first = base + sum - m;
+        if (n <= a.p.num_seqs) a.slots[n] = first < a.max_slots ? first : a.max_slots;
+        base += __shfl(sum, 63, 64);
     }
-    const int l = threadIdx.x & 15, dv = a.p.head_dim_v;
-    const int64_t rows = a.Ttot * a.p.num_q_heads, step = (int64_t)(gridDim.x - 1) * 16;
-    for (int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); r < rows; r += step) {
-        const int o32 = a.p.out_dtype == GDR_F32, g32 = a.p.do_dtype == GDR_F32;
-        float s = 0.f;
-        if (8 * l + 8 <= dv) {
-            float o[8], g[8];
-            load_vec_as<T, 8>(a.oin, r * dv + 8 * l, o32, o);
-            load_vec_as<T, 8>(a.d_o, r * dv + 8 * l, g32, g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(o[i], g[i], s);
-            if (a.d_o16) store_vec<T, 8>((T*)a.d_o16 + r * dv + 8 * l, g);
+}
+
+// A d_o in fp32 in the io type, 4 elements a thread
+template <typename T>
+__global__ __launch_bounds__(256) void k_window_round(const float* from, T* to, int64_t n) {
+    const int64_t step = (int64_t)gridDim.x * 1024;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += step) {
+        if (i + 4 <= n) {
+            float x[4];
+            unpack<float, 4>(load_raw<float, 4>(from + i), x);
+            store_vec<T, 4>(to + i, x);
         } else {
-            for (int i = 8 * l; i < dv; ++i) {
-                const float g = load_as<T>(a.d_o, r * dv + i, g32);
-                s = __builtin_fmaf(load_as<T>(a.oin, r * dv + i, o32), g, s);
-                if (a.d_o16) ((T*)a.d_o16)[r * dv + i] = to_t<T>(g);
-            }
-        }
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m, 64);
-        if (l == 0) {
-            a.rows[2 * r] = a.lse_in[r] * kLog2e;
-            a.rows[2 * r + 1] = s;
+            for (int64_t j = i; j < n; ++j) to[j] = to_t<T>(from[j]);
         }
     }
 }
@@ -77,6 +62,7 @@ template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = KT / 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
     __shared__ __attribute__((aligned(16))) T K0[KT * DK], K1[KT * DK], V0[KT * DV], V1[KT * DV];
+    if (blockIdx.x == 0 && threadIdx.x < 64 && a.slots) count_slots(a);
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
     const int hh = id / nblk, G = a.p.num_q_heads / a.p.num_kv_heads, hk = hh / rb.HC, hc = hh % rb.HC;
@@ -93,7 +79,29 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
         qf[t] = load_frag_row<T, VEC>((const T*)a.q + q.token * a.p.q_stride + (int64_t)q.head * dk, 2 * t + h, dk, q.live);
 #pragma unroll
     for (int t = 0; t < VF; ++t) gf[t] = load_frag_row<T, VEC>((const T*)a.d_o + row * dv, 2 * t + h, dv, q.live);
-    const float lse = a.rows[2 * row], delta = a.rows[2 * row + 1], c = a.p.scale * kLog2e;
+    // lse in units of log 2, and delta: here for the lane's query, in memory for k_window_dkv
+    const float lse = a.lse_in[row] * kLog2e, c = a.p.scale * kLog2e;
+    float delta = 0.f;
+#pragma unroll
+    for (int t = 0; t < VF; ++t) {
+        const int d0 = (2 * t + h) * kUnit<T>;
+        float o[kUnit<T>];
+        if (VEC && d0 < dv) {
+            load_vec_as<T, kUnit<T>>(a.oin, row * dv + d0, a.p.out_dtype == GDR_F32, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kUnit<T>; ++e)
+                o[e] = d0 + e < dv ? load_as<T>(a.oin, row * dv + d0 + e, a.p.out_dtype == GDR_F32) : 0.f;
+        }
+        // rows that are not there have a d_o of zero
+#pragma unroll
+        for (int e = 0; e < kUnit<T>; ++e) delta = __builtin_fmaf(q.live ? o[e] : 0.f, to_f(gf[t][e]), delta);
+    }
+    delta = pair_sum(delta);
+    if (q.live && h == 0) {
+        a.rows[2 * row] = lse;
+        a.rows[2 * row + 1] = delta;
+    }
     f32x16 acc[DK / 32];
 #pragma unroll
     for (int t = 0; t < DK / 32; ++t) acc[t] = zero16();
@@ -404,7 +412,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
 }
 
 // ---------------------------------------------------------------- sums of the sinks' slots
-// Workgroups (slot, key head); those of a sequence's first slot add up its slots in order.
+// Workgroups (slot, key head): those of a sequence share its sinks' elements and add up its
+// slots in order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_window_sinks(AttnArgs a) {
     const int Nk = a.p.num_kv_heads, u = blockIdx.x / Nk, hk = blockIdx.x % Nk, S = a.p.sinks;
@@ -417,16 +426,17 @@ __global__ __launch_bounds__(256) void k_window_sinks(AttnArgs a) {
         lo += x;
     }
     const int n = __builtin_amdgcn_readfirstlane(lo), first = a.slots[n], end = a.slots[n + 1];
-    if (u != first || u >= end) return;
+    if (u >= end) return;
     int64_t s, e;
     seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
     const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v, d = dk + dv;
     const int rows = S < e - s ? S : (int)(e - s);
     const int64_t step = (int64_t)S * Nk * d;
-    for (int64_t i = threadIdx.x; i < (int64_t)rows * d; i += 256) {
+    for (int64_t i = (int64_t)(u - first) * 256 + threadIdx.x; i < (int64_t)rows * d; i += (int64_t)(end - first) * 256) {
         const int j = (int)(i / d), x = (int)(i % d);
         const float* p = a.sink_part + (((int64_t)first * S + j) * Nk + hk) * d + x;
         float sum = 0.f;
+#pragma unroll 8
         for (int k = first; k < end; ++k, p += step) sum += *p;
         const int64_t row = (s + j) * Nk + hk;
         if (x < dk) store_as<T>(a.dk, row * dk + x, sum, a.p.grad_dtype == GDR_F32);
@@ -489,14 +499,17 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
             e = hipErrorInvalidConfiguration;
             return;
         }
-        const int64_t rows = (a.Ttot * a.p.num_q_heads + 15) / 16, most = 8192;
-        k_window_rows_prep<T><<<dim3((unsigned)((rows < most ? rows : most) + 1)), 256, 0, a.stream>>>(a, KB);
-        if (a.d_o16) a.d_o = a.d_o16;
+        if (a.d_o16) {
+            const int64_t n = a.Ttot * a.p.num_q_heads * a.p.head_dim_v, need = (n + 1023) / 1024, most = 8192;
+            k_window_round<T><<<dim3((unsigned)(need < most ? need : most)), 256, 0, a.stream>>>((const float*)a.d_o,
+                                                                                               (T*)a.d_o16, n);
+            a.d_o = a.d_o16;
+        }
         const dim3 gq((unsigned)((wq + 7) / 8 * 8)), gk((unsigned)((wm + 7) / 8 * 8 + wk - wm));
         auto go = [&](auto vec) {
             constexpr bool VEC = decltype(vec)::value;
-            k_window_dkv<T, DK, DV, NK, VEC><<<gk, 64 * NK, 0, a.stream>>>(a, rk, (int)bk, (int)wm, (int)wk);
             k_window_dq<T, DK, DV, NQ, VEC><<<gq, 64 * NQ, 0, a.stream>>>(a, rq, (int)bq, (int)wq);
+            k_window_dkv<T, DK, DV, NK, VEC><<<gk, 64 * NK, 0, a.stream>>>(a, rk, (int)bk, (int)wm, (int)wk);
         };
         a.vec ? go(std::true_type{}) : go(std::false_type{});
         if (x.slots) k_window_sinks<T><<<dim3((unsigned)(x.slots * Nk)), 256, 0, a.stream>>>(a);
