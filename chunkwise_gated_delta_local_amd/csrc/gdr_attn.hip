@@ -2,10 +2,29 @@
 #include <type_traits>
 
 #include "gdr_attn.hpp"
+#include <cstdlib>
+#include <cstdio>
+#ifndef OCC64
+#define OCC64 4
+#endif
 
 namespace gdr {
 
 namespace {
+
+// Order of a run of N operands that are read from LDS in R reads each and used in M
+// products each: AHEAD operands are read before the first product.
+template <int N, int R, int M, int AHEAD = 6>
+__device__ __forceinline__ void feed() {
+    constexpr int A = AHEAD < N ? AHEAD : N;
+    __builtin_amdgcn_sched_group_barrier(0x100, A * R, 0);
+#pragma unroll
+    for (int i = 0; i < N - A; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, A * M, 0);
+}
 
 // ---------------------------------------------------------------- softmax over tiles
 // What a lane keeps of its query: the output's dims 32 t + 8 i + 4 h + j in o[t][4 i + j],
@@ -28,11 +47,11 @@ __device__ __forceinline__ float refer(float a, float b) { return a == b ? 1.f :
 
 // Whether a tile of N elements holds Inf or NaN, by a wavefront
 template <typename T, int N>
-__device__ __forceinline__ bool any_special(const T* tile) {
+__device__ __forceinline__ bool any_special(lds_c tile) {
     uint32_t top = 0;
 #pragma unroll 4
-    for (int i = (int)(threadIdx.x & 63) * kUnit<T>; i < N; i += 64 * kUnit<T>) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + i);
+    for (int i = (int)(threadIdx.x & 63) * 16; i < N * (int)sizeof(T); i += 1024) {
+        const u32x4 x = *(lds_p<u32x4>)(tile + i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             // without their signs; two elements of 16 bits compare as the upper halves do
@@ -48,14 +67,14 @@ __device__ __forceinline__ bool any_special(const T* tile) {
 // zeros for such elements (`to` may be `from`), by a wavefront, and returns the keys
 // that had one: the lane's key 8 i + 4 h + j of subtile k in bit 16 k + 4 i + j.
 template <typename T, int D, int ROWS>
-__device__ __forceinline__ uint32_t copy_finite(const T* from, T* to) {
+__device__ __forceinline__ uint32_t copy_finite(lds_c from, lds_c to) {
     constexpr int UN = D / kUnit<T>;                       // units (lanes) to a row
     static_assert(UN <= 64 && 64 % UN == 0, "whole rows a step");
     const int lane = threadIdx.x & 63, h = lane >> 5;
     uint32_t lost = 0;
 #pragma unroll 1
     for (int r0 = 0; r0 < ROWS; r0 += 64 / UN) {
-        typename Raw<T, kUnit<T>>::type x = load_raw<T, kUnit<T>>(from + (r0 * UN + lane) * kUnit<T>);
+        auto x = __builtin_bit_cast(typename Raw<T, kUnit<T>>::type, *(lds_p<u32x4>)(from + (r0 * UN + lane) * 16));
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < kUnit<T>; ++e) {
@@ -63,7 +82,7 @@ __device__ __forceinline__ uint32_t copy_finite(const T* from, T* to) {
             bad |= !ok;
             x[e] = ok ? x[e] : to_t<T>(0.f);
         }
-        store_raw<T, kUnit<T>>(to + (r0 * UN + lane) * kUnit<T>, x);
+        *(lds_p<u32x4>)(to + (r0 * UN + lane) * 16) = __builtin_bit_cast(u32x4, x);
         const uint64_t who = __ballot(bad);
 #pragma unroll
         for (int k = 0; k < 64 / UN; ++k) {
@@ -75,19 +94,16 @@ __device__ __forceinline__ uint32_t copy_finite(const T* from, T* to) {
     return lost;
 }
 
-// One tile of 32 NT keys, whose raw scores are s (overwritten by the weights) and
-// whose values lie in V. partial: some query may not see some key; the values are then
-// copied to `clean` first.
+// The weights of one tile of 32 NT keys, whose raw scores are s, in their place.
+// partial: some query may not see some key.
 //
 // Weights are exp2(c s - mc). m follows the maximum only when that has grown by more
 // than 8 in the exponent: weights then stay below 2^9 and the sums, in fp32, hardly
 // notice, while most tiles are spared the product of o with the change. Beyond 2^24 the
 // rounding of mc reaches the exponent's units, and the difference is formed first.
-template <typename T, int DV, int NT>
-__device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* V, T* clean, float c,
-                                       bool partial, const Sight& sees) {
-    const int lane = threadIdx.x & 63, h = lane >> 5;
-    const int co = fresh(col_offset<T, DV>(lane));
+template <int DV, int NT>
+__device__ __forceinline__ void weigh(State<DV>& st, f32x16 (&s)[NT], float c, bool partial, const Sight& sees) {
+    const int h = (threadIdx.x >> 5) & 1;
     if (partial) {
         asm volatile("");                                  // a branch: most tiles are seen whole
 #pragma unroll
@@ -109,24 +125,34 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
         for (int t = 0; t < DV / 32; ++t) st.o[t] = st.o[t] * f;
         st.m = m;
         st.mc = mc;
+        arrived(st.o);
     }
-    const float mc = st.m == kNegInf ? 0.f : st.mc;
+    float mc = st.m == kNegInf ? 0.f : st.mc;
     if (__any(fabsf(mc) > 16777216.f)) {
+        asm volatile("");
         const float m = st.m == kNegInf ? 0.f : st.m;
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[k][i] = __builtin_amdgcn_exp2f((s[k][i] - m) * c);
-    } else {
-#pragma unroll
-        for (int k = 0; k < NT; ++k)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], c, -mc));
+            for (int i = 0; i < 16; ++i) s[k][i] -= m;
+        mc = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
+        for (int i = 0; i < 16; ++i) s[k][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], c, -mc));
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
         for (int i = 0; i < 16; ++i) st.l += s[k][i];
+}
+
+// o += V^T P: a tile's values in V, its weights packed in w. Where some query may not see
+// some key, values with Inf or NaN are copied to `clean` first.
+template <typename T, int DV, int NT>
+__device__ __forceinline__ void add_values(State<DV>& st, const typename Vec<T>::v8 (&w)[2 * NT], lds_c V, lds_c clean,
+                                           bool partial, const Sight& sees) {
+    const int lane = threadIdx.x & 63, h = lane >> 5, co = fresh(col_offset<T, DV>(lane));
     if (partial && any_special<T, 32 * NT * DV>(V)) {
         const uint32_t lost = copy_finite<T, DV, 32 * NT>(V, clean);
         if (lost) {                                        // who sees such a key loses its sum
@@ -140,13 +166,11 @@ __device__ __forceinline__ void absorb(State<DV>& st, f32x16 (&s)[NT], const T* 
         V = clean;
     }
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int q = 0; q < 2 * NT; ++q)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const auto w = acc_frag<T>(s[k], q);
-#pragma unroll
-            for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<DV>(V, 32 * k + 16 * q, t, co), w, st.o[t]);
-        }
+        for (int t = 0; t < DV / 32; ++t) st.o[t] = mma(col_frag<T, DV>(V, 16 * q, t, co), w[q], st.o[t]);
+    arrived(st.o);
+    feed<2 * NT * DV / 32, sizeof(T) == 2 ? 2 : 8, sizeof(T) == 2 ? 1 : 8>();
 }
 
 template <typename T, int DK, bool VEC>
@@ -187,8 +211,8 @@ template <typename T> constexpr int kTileKeys = sizeof(T) == 2 ? 64 : 32;
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = kTileKeys<T>, NT = KT / 32, KF = DK / (2 * kUnit<T>);
-    __shared__ __attribute__((aligned(16))) T K0[KT * DK], K1[KT * DK], V0[KT * DV], V1[KT * DV];
-    // the finite values of a tile at an edge: all wavefronts that need it write the same
+    __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK], Vs[2][KT * DV];
+    // the finite values of a tile at an edge: all wavefronts that need them write the same
     __shared__ __attribute__((aligned(16))) T Clean[KT * DV];
     // consecutive blocks of a key head on one XCD: their windows overlap
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
@@ -207,45 +231,51 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
     State<DV> st;
     st.clear();
     const float c = a.p.scale * kLog2e;
+    const lds_c K0 = lds_of(Ks[0]), K1 = lds_of(Ks[1]), V0 = lds_of(Vs[0]), V1 = lds_of(Vs[1]), clean = lds_of(Clean);
 
     Keys keys(len + b.t0, len + b.t0 + b.tn - 1, len, W, S);
     Copy<T, DK, KT, 64 * NW, VEC> ck;
     Copy<T, DV, KT, 64 * NW, VEC> cv;
     int pos, cnt, row;
     bool cached;
-    auto fetch = [&](T* K, T* V) {
+    auto fetch = [&](lds_c K, lds_c V) {
         keys.next(KT, &pos, &cnt, &row, &cached);
         if (cnt == 0) return;
         const Source<T> s = source<T>(a, b, hk, row, cached);
         ck.start(K, s.k, s.kld, cnt, dk, tid);
         cv.start(V, s.v, s.vld, cnt, dv, tid);
     };
-    auto land = [&](T* K, T* V) {
+    auto land = [&](lds_c K, lds_c V) {
         if (cnt > 0) {
             ck.finish(K, tid);
             cv.finish(V, tid);
         }
-        __syncthreads();
+        landed();
     };
-    // a tile in (K, V), the next one on its way to (Kn, Vn)
-    auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
+    // a tile in (K, V), the next one on its way to (Kn, Vn). Tiles that none of a
+    // wavefront's queries sees are few and give weights of zero.
+    auto turn = [&](lds_c K, lds_c V, lds_c Kn, lds_c Vn) {
         const int pos0 = pos, n = cnt, ro = fresh(row_offset<T, DK>(lane));
         fetch(Kn, Vn);
-        // some query of this wavefront sees a key of the tile
-        if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
-            f32x16 s[NT];
+        f32x16 s[NT];
 #pragma unroll
-            for (int k = 0; k < NT; ++k) s[k] = zero16();
+        for (int k = 0; k < NT; ++k) s[k] = zero16();
 #pragma unroll
-            for (int t = 0; t < KF; ++t)
+        for (int t = 0; t < KF; ++t)
 #pragma unroll
-                for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s[k]);
-            const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
-            absorb<T, DV, NT>(st, s, V, Clean, c, partial, Sight{pos0, n, q.p, W, S});
-        }
+            for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s[k]);
+        feed<KF * NT, 1, sizeof(T) == 2 ? 1 : 4>();
+        const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
+        const Sight sees{pos0, n, q.p, W, S};
+        weigh<DV, NT>(st, s, c, partial, sees);
+        typename Vec<T>::v8 wt[2 * NT];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) wt[i] = acc_frag<T>(s[i >> 1], i & 1);
+        add_values<T, DV, NT>(st, wt, V, clean, partial, sees);
         land(Kn, Vn);
     };
     fetch(K0, V0);
+    arrived(qf);
     land(K0, V0);
     while (cnt > 0) {
         turn(K0, V0, K1, V1);
@@ -289,6 +319,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     st.clear();
     const float c = a.p.scale * kLog2e;
     Keys keys(len + b.t0, len + b.t0 + b.tn - 1, len, W, S);
+    const lds_c mine_v = lds_of(&Vs[0][0]) + w * 32 * DV * (int)sizeof(T);
     // this wavefront's share of the keys, in tiles
     const int all = keys.total(), parts = splits * NW, part = sp * NW + w;
     const int share = ((all + parts - 1) / parts + 31) / 32 * 32;
@@ -325,7 +356,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
         load_values();
         while (cnt > 0) {
             const int pos0 = pos, n = cnt;
-            sv.store(Vs[w]);
+            sv.store(mine_v);
             next();
             load_values();
             f32x16 s[1] = {zero16()};
@@ -333,7 +364,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
             for (int t = 0; t < KF; ++t) s[0] = mma(kf[t], qf[t], s[0]);
             load_keys();
             const bool partial = n < 32 || pos0 + 31 > pa || (pos0 <= pb - W && pos0 + 32 > S);
-            absorb<T, DV, 1>(st, s, Vs[w], Vs[w], c, partial, Sight{pos0, n, q.p, W, S});
+            const Sight sees{pos0, n, q.p, W, S};
+            weigh<DV, 1>(st, s, c, partial, sees);
+            const typename Vec<T>::v8 wt[2] = {acc_frag<T>(s[0], 0), acc_frag<T>(s[0], 1)};
+            add_values<T, DV, 1>(st, wt, mine_v, mine_v, partial, sees);
         }
     }
     // join the wavefronts: a common maximum, then one tile of 32 dims after another
@@ -383,6 +417,231 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
             part_o[row * (dv + 2) + dv + 1] = idle ? -1.f : l;
         } else if (a.lse) {
             a.lse[row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+// The token at position p sees the first min(p + 1, sinks + window) rows of its
+// sequence's caches, in whatever order, its own row taken from the call. Up to 16 heads
+// of a key head are the columns of 16x16 tiles (layouts as in gdr_device.hpp): scores
+// transposed, 32 rows of the caches at a time, k straight into the operand's registers,
+// v through LDS of the wavefront's own, the next 32 under way meanwhile. NW wavefronts
+// and `splits` workgroups share the rows; rows behind the last one are read as the last
+// one, with a weight of zero.
+template <typename T, int D> struct StepTile {
+    static constexpr int UN = D / kUnit<T>;
+    // v's rows in LDS, so that the operand's reads spread over the banks
+    static __device__ __forceinline__ int swz(int row) {
+        if constexpr (sizeof(T) == 4) return (row >> 2 & 3) << 2;
+        else if constexpr (UN == 8) return (row >> 1 & 3) << 1;
+        else return (row & 7) << 1;
+    }
+    // dims 16 t + lane % 16 of rows 4 qd + j and 16 + 4 qd + j
+    static __device__ __forceinline__ typename Vec<T>::v8 operand(lds_c tile, int t) {
+        const int lane = threadIdx.x & 63, r = lane & 15, qd = lane >> 4;
+        typename Vec<T>::v8 v;
+        if constexpr (sizeof(T) == 2) {
+            s16x4 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 16 * i + 4 * qd + (r >> 2), unit = 2 * t + (r >> 1 & 1);
+                x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p<s16x4>)(tile + row * D * 2 + (unit ^ swz(row)) * 16 + 8 * (r & 1)));
+            }
+            v = __builtin_bit_cast(typename Vec<T>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 16 * (e >> 2) + 4 * qd + (e & 3), unit = 4 * t + (r >> 2);
+                v[e] = *(lds_p<float>)(tile + row * D * 4 + (unit ^ swz(row)) * 16 + 4 * (r & 3));
+            }
+        }
+        return v;
+    }
+};
+// 8 elements of a row at dim d0; VEC: in 16-byte pieces
+template <typename T, bool VEC, bool ONCE>
+__device__ __forceinline__ typename Vec<T>::v8 load8(const T* row, int d0, int d) {
+    typename Vec<T>::v8 x;
+    if constexpr (VEC) {
+        constexpr int U = kUnit<T>;
+#pragma unroll
+        for (int i = 0; i < 8; i += U) {
+            typename Raw<T, U>::type y;
+            if (d0 + i < d) y = load_raw<T, U, ONCE>(row + d0 + i);
+            else y = typename Raw<T, U>::type{};
+#pragma unroll
+            for (int e = 0; e < U; ++e) x[i + e] = y[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = d0 + e < d ? row[d0 + e] : to_t<T>(0.f);
+    }
+    return x;
+}
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16, 64));
+    return pair_max(x);
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor(x, 16, 64);
+    return pair_sum(x);
+}
+
+template <typename T, int DK, int DV, int NW, bool VEC, bool ONCE>
+__global__ __launch_bounds__(64 * NW, 2) void k_window_step(AttnArgs a, int splits) {
+    typedef StepTile<T, DV> Tile;
+    constexpr int KS = DK / 32, VS = DV / 16, VU = 32 * Tile::UN / 64;
+    __shared__ __attribute__((aligned(16))) T Vs[NW][32 * DV];
+    __shared__ float ml[NW][2][16];
+    const int Nk = a.p.num_kv_heads, G = a.p.num_q_heads / Nk, HC = (G + 15) / 16, HPB = G < 16 ? G : 16;
+    const int sp = blockIdx.x % splits, id = blockIdx.x / splits, hh = id % (Nk * HC), n = id / (Nk * HC);
+    const int hk = hh / HC, hc = hh % HC;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, qd = lane >> 4;
+    const int dk = a.p.head_dim_qk, dv = a.p.head_dim_v, S = a.p.sinks, W = a.p.window;
+    const T *kn = (const T*)a.k + n * a.p.k_stride + (int64_t)hk * dk, *vn = (const T*)a.v + n * a.p.v_stride + (int64_t)hk * dv;
+    const int g = hc * 16 + r, head = hk * G + (g < G ? g : G - 1);
+    const T* qn = (const T*)a.q + n * a.p.q_stride + (int64_t)head * dk;
+    typename Vec<T>::v8 qf[KS];
+#pragma unroll
+    for (int t = 0; t < KS; ++t) qf[t] = load8<T, VEC, false>(qn, 32 * t + 8 * qd, dk);
+    const int p = __builtin_amdgcn_readfirstlane(a.lens[n]);
+    const bool idle = p < 0;
+    const int64_t cap = (int64_t)S + W;
+    const int rows = (int64_t)p + 1 < cap ? p + 1 : (int)cap, own = p < S ? p : S + (p - S) % W;
+    T *kc = (T*)a.kc + (n * cap * Nk + hk) * dk, *vc = (T*)a.vc + (n * cap * Nk + hk) * dv;
+    const int64_t kld = (int64_t)Nk * dk, vld = (int64_t)Nk * dv;
+    if (!idle && hc == 0 && sp == 0) {
+        // nobody reads the token's row of the caches: its old token is out of sight
+        for (int d = tid; d < dk; d += 64 * NW) kc[own * kld + d] = kn[d];
+        for (int d = tid; d < dv; d += 64 * NW) vc[own * vld + d] = vn[d];
+    }
+    const float c = a.p.scale * kLog2e;
+    const int parts = splits * NW, tiles = idle ? 0 : (rows + 31) / 32, share = (tiles + parts - 1) / parts;
+    const int first = (sp * NW + w) * share, last = first + share < tiles ? first + share : tiles;
+    f32x4 o[VS];
+#pragma unroll
+    for (int t = 0; t < VS; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = kNegInf, mc = kNegInf, l = 0.f;
+    const lds_c mine_v = lds_of(&Vs[0][0]) + w * 32 * DV * (int)sizeof(T);
+    typename Vec<T>::v8 kf[2][KS];
+    u32x4 vx[VU];
+    auto load_keys = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int row = 32 * tile + 16 * i + r;
+            row = row < rows ? row : rows - 1;
+            const T* x = row == own ? kn : kc + row * kld;
+#pragma unroll
+            for (int t = 0; t < KS; ++t) kf[i][t] = load8<T, VEC, ONCE>(x, 32 * t + 8 * qd, dk);
+        }
+    };
+    auto load_values = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int at = lane + 64 * i;
+            int row = 32 * tile + at / Tile::UN;
+            row = row < rows ? row : rows - 1;
+            const T* x = row == own ? vn : vc + row * vld;
+            const int d0 = at % Tile::UN * kUnit<T>;
+            typename Raw<T, kUnit<T>>::type y;
+            if constexpr (VEC) {
+                if (d0 < dv) y = load_raw<T, kUnit<T>, ONCE>(x + d0);
+                else y = typename Raw<T, kUnit<T>>::type{};
+            } else {
+#pragma unroll
+                for (int e = 0; e < kUnit<T>; ++e) y[e] = d0 + e < dv ? x[d0 + e] : to_t<T>(0.f);
+            }
+            vx[i] = __builtin_bit_cast(u32x4, y);
+        }
+    };
+    if (first < last) {
+        load_keys(first);
+        load_values(first);
+    }
+#pragma unroll 1
+    for (int tile = first; tile < last; ++tile) {
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int at = lane + 64 * i, row = at / Tile::UN, unit = at % Tile::UN ^ Tile::swz(row);
+            *(lds_p<u32x4>)(mine_v + (row * Tile::UN + unit) * 16) = vx[i];
+        }
+        const int next = tile + 1 < last ? tile + 1 : tile;
+        load_values(next);
+        f32x4 s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < KS; ++t) s[i] = mfma_pair(kf[i][t], qf[t], s[i]);
+        }
+        load_keys(next);
+        if (32 * tile + 32 > rows) {
+            asm volatile("");
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i >> 2][i & 3] = 32 * tile + 16 * (i >> 2) + 4 * qd + (i & 3) < rows ? s[i >> 2][i & 3] : kNegInf;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = __builtin_elementwise_maximum(top, s[i >> 2][i & 3]);
+        top = quad_max(top);
+        if (__any((top - m) * c > 8.f)) {
+            const float mn = fmaxf(m, top), mcn = mn * c, f = refer(mc, mcn);
+            l *= f;
+#pragma unroll
+            for (int t = 0; t < VS; ++t) o[t] = o[t] * f;
+            m = mn;
+            mc = mcn;
+        }
+        // as in absorb
+        const float m0 = m == kNegInf ? 0.f : m, mc0 = m == kNegInf ? 0.f : mc;
+        const bool far = __any(fabsf(mc0) > 16777216.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = s[i >> 2][i & 3], e = far ? (x - m0) * c : __builtin_fmaf(x, c, -mc0);
+            s[i >> 2][i & 3] = __builtin_amdgcn_exp2f(e);
+            l += s[i >> 2][i & 3];
+        }
+        const auto wt = acc_to_pair<T>(s[0], s[1]);
+#pragma unroll
+        for (int t = 0; t < VS; ++t) o[t] = mfma_pair(Tile::operand(mine_v, t), wt, o[t]);
+    }
+    // join the wavefronts: all their sums in LDS, then a thread an output
+    l = quad_sum(l);
+    float* mine = reinterpret_cast<float*>(Vs[w]);
+    static_assert(32 * DV * sizeof(T) >= 16 * DV * 4, "a wavefront's values make room for its outputs");
+#pragma unroll
+    for (int t = 0; t < VS; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine[(16 * t + 4 * qd + j) * 16 + r] = o[t][j];
+    if (lane < 16) {
+        ml[w][0][lane] = mc;
+        ml[w][1][lane] = l;
+    }
+    __syncthreads();
+    const int cols = G - hc * 16 < HPB ? G - hc * 16 : HPB;
+    for (int i = tid; i < dv * cols; i += 64 * NW) {
+        const int h = i / dv, d = i - h * dv;
+        float mm = kNegInf, ll = 0.f, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) mm = fmaxf(mm, ml[k][0][h]);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const float f = refer(ml[k][0][h], mm);
+            ll = __builtin_fmaf(ml[k][1][h], f, ll);
+            y = __builtin_fmaf(reinterpret_cast<const float*>(Vs[k])[d * 16 + h], f, y);
+        }
+        const int64_t row = (int64_t)n * a.p.num_q_heads + hk * G + hc * 16 + h;
+        if (splits == 1) {
+            store_as<T>(a.o, row * dv + d, idle ? 0.f : y / ll, a.p.out_dtype == GDR_F32);
+        } else {
+            float* part = a.ws + ((int64_t)sp * a.Ttot * a.p.num_q_heads + row) * (dv + 2);
+            part[d] = y;
+            if (d == 0) {
+                part[dv] = idle ? 0.f : mm;
+                part[dv + 1] = idle ? -1.f : ll;
+            }
         }
     }
 }
@@ -463,6 +722,7 @@ Plan plan_of(const gdr_attn_problem_t& p) {
     const int64_t few = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB) * p.num_kv_heads * x.rb.HC;
     x.split = rows <= 32 * 1024;
     if (p.seq_len == 1 && !packed) x.split = true;
+    if (getenv("GDR_SPLIT")) x.split = atoi(getenv("GDR_SPLIT"));
     if (x.split) {
         x.NW = p.io_dtype == GDR_BF16 ? 8 : 4;
         x.nblk = few / (p.num_kv_heads * x.rb.HC);
@@ -470,10 +730,12 @@ Plan plan_of(const gdr_attn_problem_t& p) {
         const int64_t want = few > 0 ? 512 / few : 1, most = (keys + 32 * x.NW - 1) / (32 * x.NW);
         const int64_t s = want < most ? want : most;
         x.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+        if (getenv("GDR_SPLITS")) x.splits = atoi(getenv("GDR_SPLITS"));
         return x;
     }
     x.NW = 8;
     x.splits = 1;
+    if (getenv("GDR_NW")) x.NW = atoi(getenv("GDR_NW"));
     x.rb = row_block(32 * x.NW, G);
     x.nblk = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB);
     x.nwork = x.nblk * p.num_kv_heads * x.rb.HC;
@@ -486,6 +748,44 @@ size_t attn_fwd_workspace(const gdr_attn_problem_t& p) {
     const Plan x = plan_of(p);
     if (x.splits <= 1) return 0;
     return (size_t)x.splits * p.batch * p.seq_len * p.num_q_heads * (p.head_dim_v + 2) * 4;
+}
+
+// Single tokens: workgroups that share the rows of a sequence's key head
+constexpr int kStepWaves = 8;
+int step_splits(const gdr_attn_problem_t& p) {
+    if (getenv("GDR_SPLITS")) return atoi(getenv("GDR_SPLITS"));
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * ((group(p) + 15) / 16), rows = (int64_t)p.sinks + p.window;
+    const int64_t want = units > 0 ? 256 / units : 1, most = rows / (32 * kStepWaves * 2);
+    const int64_t s = want < most ? want : most;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+hipError_t launch_attn_step(const AttnArgs& a) {
+    if (a.Ttot == 0) return hipSuccess;
+    const int splits = step_splits(a.p);
+    const int64_t units = (int64_t)a.p.num_seqs * a.p.num_kv_heads * ((group(a.p) + 15) / 16) * splits;
+    if (!grid_fits(units, 64 * kStepWaves)) return hipErrorInvalidConfiguration;
+    const int64_t rows = (int64_t)a.p.sinks + a.p.window;
+    const bool once = beyond_caches(a.p.num_seqs * rows * a.p.num_kv_heads * (a.p.head_dim_qk + a.p.head_dim_v) *
+                                    size_of(a.p.io_dtype));
+    by_dims(a.p, [&](auto type, auto dk, auto dv) {
+        typedef decltype(type) T;
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NW = kStepWaves;
+        const dim3 grid((unsigned)units);
+        if (!a.vec) k_window_step<T, DK, DV, NW, false, false><<<grid, 64 * NW, 0, a.stream>>>(a, splits);
+        else if (once) k_window_step<T, DK, DV, NW, true, true><<<grid, 64 * NW, 0, a.stream>>>(a, splits);
+        else k_window_step<T, DK, DV, NW, true, false><<<grid, 64 * NW, 0, a.stream>>>(a, splits);
+        if (splits > 1) {
+            const int64_t n = a.Ttot * a.p.num_q_heads;
+            k_window_join<T><<<dim3((unsigned)((n + 3) / 4)), 256, 0, a.stream>>>(a, splits);
+        }
+    });
+    return hipGetLastError();
+}
+
+size_t attn_step_workspace(const gdr_attn_problem_t& p) {
+    const int s = step_splits(p);
+    return s > 1 ? (size_t)s * p.num_seqs * p.num_q_heads * (p.head_dim_v + 2) * 4 : 0;
 }
 
 hipError_t launch_attn_fwd(const AttnArgs& a) {
@@ -506,7 +806,9 @@ hipError_t launch_attn_fwd(const AttnArgs& a) {
             }
         } else {
             const dim3 grid((unsigned)((x.nwork + 7) / 8 * 8));
-            if (a.vec) k_window_rows<T, DK, DV, 8, true><<<grid, 512, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            if (a.vec && x.NW == 2) k_window_rows<T, DK, DV, 2, true><<<grid, 128, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            else if (a.vec && x.NW == 4) k_window_rows<T, DK, DV, 4, true><<<grid, 256, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            else if (a.vec) k_window_rows<T, DK, DV, 8, true><<<grid, 512, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
             else k_window_rows<T, DK, DV, 8, false><<<grid, 512, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
         }
         e = hipGetLastError();

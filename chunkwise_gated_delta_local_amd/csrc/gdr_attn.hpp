@@ -48,6 +48,8 @@ struct AttnArgs {
 
 size_t attn_fwd_workspace(const gdr_attn_problem_t& p);
 hipError_t launch_attn_fwd(const AttnArgs& a);
+size_t attn_step_workspace(const gdr_attn_problem_t& p);
+hipError_t launch_attn_step(const AttnArgs& a);
 size_t attn_bwd_workspace(const gdr_attn_problem_t& p);
 hipError_t launch_attn_bwd(const AttnArgs& a);
 
@@ -57,6 +59,13 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNegInf = -__builtin_inff();
+
+// Tiles in LDS are addressed as LDS, by bytes: a pointer that could point anywhere costs
+// a test for NULL wherever an LDS address is made of it.
+template <typename T> using lds_p = __attribute__((address_space(3))) T*;
+typedef lds_p<char> lds_c;
+template <typename T>
+__device__ __forceinline__ lds_c lds_of(T* tile) { return (lds_c)(lds_p<T>)tile; }
 
 // elements in 16 bytes
 template <typename T> constexpr int kUnit = 16 / (int)sizeof(T);
@@ -258,33 +267,36 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
+// Operands that were loaded before a loop are waited for here, not in each of its turns
+// (where the copies under way would be waited for with them).
+template <typename F, int N>
+__device__ __forceinline__ void arrived(F (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+}
+
 // row r0 + lane % 32 (r0 a multiple of 32), step t; off: row_offset
 template <typename T, int D>
-__device__ __forceinline__ frag_t<T> row_frag(const T* tile, int r0, int t, int off) {
-    return *reinterpret_cast<const frag_t<T>*>(reinterpret_cast<const char*>(tile) + (off ^ (t << 5)) +
-                                               r0 * D * (int)sizeof(T));
+__device__ __forceinline__ frag_t<T> row_frag(lds_c tile, int r0, int t, int off) {
+    return *(lds_p<frag_t<T>>)(tile + (off ^ (t << 5)) + r0 * D * (int)sizeof(T));
 }
 // Operand of the transpose: row 32 u + lane % 32 (a column of the tile), contracted over
 // the 16 tile rows r0 + 8 i + 4 h + j, i < 2 (r0 a multiple of 16); off: col_offset
-template <int D>
-__device__ __forceinline__ Vec<bf16>::v8 col_frag(const bf16* tile, int r0, int u, int off) {
-    typedef __attribute__((address_space(3))) s16x4* lds_p;
-    s16x4 x[2];
+template <typename T, int D>
+__device__ __forceinline__ typename Vec<T>::v8 col_frag(lds_c tile, int r0, int u, int off) {
+    if constexpr (sizeof(T) == 2) {
+        s16x4 x[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(reinterpret_cast<const char*>(tile) +
-                                                               (off ^ (u << 6 | i << 5)) + (r0 + 8 * i) * D * 2));
-    return __builtin_bit_cast(Vec<bf16>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
-}
-template <int D>
-__device__ __forceinline__ Vec<float>::v8 col_frag(const float* tile, int r0, int u, int off) {
-    Vec<float>::v8 x;
+        for (int i = 0; i < 2; ++i)
+            x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p<s16x4>)(tile + (off ^ (u << 6 | i << 5)) + (r0 + 8 * i) * D * 2));
+        return __builtin_bit_cast(typename Vec<T>::v8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        typename Vec<T>::v8 x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(tile) +
-                                               (off ^ (u << 7 ^ (i & 3) << 6 ^ (i >> 2) << 5)) +
-                                               (r0 + 8 * (i >> 2) + (i & 3)) * D * 4);
-    return x;
+        for (int i = 0; i < 8; ++i)
+            x[i] = *(lds_p<float>)(tile + (off ^ (u << 7 ^ (i & 3) << 6 ^ (i >> 2) << 5)) + (r0 + 8 * (i >> 2) + (i & 3)) * D * 4);
+        return x;
+    }
 }
 __device__ __forceinline__ f32x16 mma(const Vec<float>::v8& a, const Vec<float>::v8& b, f32x16 c) {
 #pragma unroll
@@ -347,11 +359,34 @@ __device__ __forceinline__ frag_t<T> load_frag_row(const T* row, int unit, int d
     return x;
 }
 
+// Copies of 16 or 4 bytes a lane to lds + 16 lane (4 lane), as buffer_to_lds16 and
+// buffer_to_lds4 (gdr_device.hpp), which the compiler does not know for ones: it would
+// have every transposing read of LDS wait for all copies under way. Whoever reads the data
+// waits himself: wait_vmem() in the wavefront that copies, and a barrier. m0, which holds
+// the address, is put back; a write of it needs one cycle before its use.
+__device__ __forceinline__ void copy16_to_lds(u32x4 rsrc, lds_c lds, int voffset) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds)), "v"(voffset), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ void copy4_to_lds(u32x4 rsrc, lds_c lds, int voffset) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, 0 offen lds\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds)), "v"(voffset), "s"(rsrc) : "memory");
+}
+// the buffer of `bytes` bytes at base (buf_rsrc) as the instruction takes it
+__device__ __forceinline__ u32x4 raw_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t p = (uint64_t)base;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xffffu)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+
 // ROWS rows of a tile on their way from memory to LDS, by NT threads: `start` issues the
-// loads, `finish` has them in LDS once the caller has waited at a barrier. With 16-byte
-// rows they go there directly, else through registers. A kernel keeps its two buffers
-// in two arrays and takes turns in its code, so that the compiler sees that reads of one
-// need not wait for loads into the other.
+// loads; once `finish` has been called and the workgroup has met at `landed`, the rows
+// are in LDS. With 16-byte rows they go there directly, else through registers.
 template <typename T, int D, int ROWS, int NT, bool VEC>
 struct Copy {
     static constexpr int UN = D / kUnit<T>, N = ROWS * UN / NT;
@@ -359,29 +394,41 @@ struct Copy {
     u32x4 x[VEC ? 1 : N];
     // row_at(row): its bytes behind base, of which `bytes` are valid
     template <typename F>
-    __device__ __forceinline__ void start(T* tile, const T* base, uint32_t bytes, F row_at, int d, int tid) {
-        const auto rs = buf_rsrc(base, bytes);
+    __device__ __forceinline__ void start(lds_c tile, const T* base, uint32_t bytes, F row_at, int d, int tid) {
         const int first = __builtin_amdgcn_readfirstlane(tid) & ~63;
+        if constexpr (VEC) {
+            const u32x4 rs = raw_rsrc(base, bytes);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz<UN>(row);
-            if constexpr (VEC)
-                buffer_to_lds16(rs, tile + (first + i * NT) * kUnit<T>, unit * kUnit<T> < d ? row_at(row) + unit * 16 : kOutside);
-            else x[i] = load_unit<T, VEC>(rs, row_at(row), unit, d);
+            for (int i = 0; i < N; ++i) {
+                const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz<UN>(row);
+                copy16_to_lds(rs, tile + (first + i * NT) * 16,
+                              unit * kUnit<T> < d ? row_at(row) + unit * 16 : kOutside);
+            }
+        } else {
+            const auto rs = buf_rsrc(base, bytes);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int id = tid + i * NT, row = id / UN, unit = (id % UN) ^ swz<UN>(row);
+                x[i] = load_unit<T, VEC>(rs, row_at(row), unit, d);
+            }
         }
     }
-    __device__ __forceinline__ void start(T* tile, const T* base, int ld, int rows, int d, int tid) {
+    __device__ __forceinline__ void start(lds_c tile, const T* base, int ld, int rows, int d, int tid) {
         const uint32_t row_bytes = (uint32_t)ld * sizeof(T);
         start(tile, base, rows > 0 ? (rows - 1) * row_bytes + d * (uint32_t)sizeof(T) : 0,
               [&](int row) { return row * (int)row_bytes; }, d, tid);
     }
-    __device__ __forceinline__ void finish(T* tile, int tid) const {
+    __device__ __forceinline__ void finish(lds_c tile, int tid) const {
         if constexpr (!VEC) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (tid + i * NT) * kUnit<T>) = x[i];
+            for (int i = 0; i < N; ++i) *(lds_p<u32x4>)(tile + (tid + i * NT) * 16) = x[i];
         }
     }
 };
+__device__ __forceinline__ void landed() {
+    wait_vmem();
+    lds_barrier();
+}
 // The same by one wavefront for itself, through registers: `load` early, `store` when the
 // tile before has been read.
 template <typename T, int D, int ROWS, bool VEC>
@@ -398,10 +445,9 @@ struct OwnCopy {
             x[i] = load_unit<T, VEC>(rs, row * (int)row_bytes, unit, d);
         }
     }
-    __device__ __forceinline__ void store(T* tile) const {
+    __device__ __forceinline__ void store(lds_c tile) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            *reinterpret_cast<u32x4*>(tile + ((int)(threadIdx.x & 63) + i * 64) * kUnit<T>) = x[i];
+        for (int i = 0; i < N; ++i) *(lds_p<u32x4>)(tile + ((int)(threadIdx.x & 63) + i * 64) * 16) = x[i];
     }
 };
 

@@ -98,7 +98,7 @@ gdr_status_t gdr_window_attn_fwd(const gdr_attn_problem_t* p, const void* q, con
 gdr_status_t gdr_window_attn_step_workspace_size(const gdr_attn_problem_t* p, size_t* bytes) {
     if (!bytes) return fail(GDR_ERR_NULL, "bytes is NULL");
     GDR_TRY(check_attn(p, kMostStride));
-    *bytes = attn_fwd_workspace(*p);
+    *bytes = attn_step_workspace(*p);
     return GDR_OK;
 }
 
@@ -112,14 +112,14 @@ gdr_status_t gdr_window_attn_step(const gdr_attn_problem_t* p, const void* q, co
     const Ptr ptrs[] = {{q, io, true, "q"}, {k, io, true, "k"}, {v, io, true, "v"}, {k_cache, io, true, "k_cache"},
                         {v_cache, io, true, "v_cache"}, {lens, GDR_F32, true, "lens"}, {o, p->out_dtype, true, "o"}};
     GDR_TRY(check_ptrs(ptrs, p->batch > 0));
-    GDR_TRY(check_workspace(workspace, workspace_bytes, attn_fwd_workspace(*p)));
+    GDR_TRY(check_workspace(workspace, workspace_bytes, attn_step_workspace(*p)));
     AttnArgs a = attn_args(p, q, k, v, k_cache, v_cache, lens, nullptr, workspace, stream);
     a.max_len = 1;
     a.one = true;
     a.k_ld = p->num_kv_heads * p->head_dim_qk;           // of one row no other is reached
     a.v_ld = p->num_kv_heads * p->head_dim_v;
     a.o = o;
-    return done(launch_attn_fwd(a));
+    return done(launch_attn_step(a));
 }
 
 gdr_status_t gdr_window_attn_bwd_workspace_size(const gdr_attn_problem_t* p, size_t* bytes) {

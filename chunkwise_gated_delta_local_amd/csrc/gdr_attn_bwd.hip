@@ -61,7 +61,8 @@ __global__ __launch_bounds__(256) void k_window_round(const float* from, T* to, 
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = KT / 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
-    __shared__ __attribute__((aligned(16))) T K0[KT * DK], K1[KT * DK], V0[KT * DV], V1[KT * DV];
+    __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK], Vs[2][KT * DV];
+    const lds_c K0 = lds_of(Ks[0]), K1 = lds_of(Ks[1]), V0 = lds_of(Vs[0]), V1 = lds_of(Vs[1]);
     if (blockIdx.x == 0 && threadIdx.x < 64 && a.slots) count_slots(a);
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= nwork) return;
@@ -111,21 +112,21 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
     Copy<T, DV, KT, 64 * NW, VEC> cv;
     int pos, cnt, at;
     bool cached;
-    auto fetch = [&](T* K, T* V) {
+    auto fetch = [&](lds_c K, lds_c V) {
         keys.next(KT, &pos, &cnt, &at, &cached);
         if (cnt == 0) return;
         const Source<T> s = source<T>(a, b, hk, at, false);
         ck.start(K, s.k, s.kld, cnt, dk, tid);
         cv.start(V, s.v, s.vld, cnt, dv, tid);
     };
-    auto land = [&](T* K, T* V) {
+    auto land = [&](lds_c K, lds_c V) {
         if (cnt > 0) {
             ck.finish(K, tid);
             cv.finish(V, tid);
         }
-        __syncthreads();
+        landed();
     };
-    auto turn = [&](const T* K, const T* V, T* Kn, T* Vn) {
+    auto turn = [&](lds_c K, lds_c V, lds_c Kn, lds_c Vn) {
         const int pos0 = pos, n = cnt;
         const int ro = fresh(row_offset<T, DK>(lane)), rv = DK == DV ? ro : fresh(row_offset<T, DV>(lane)),
                   co = fresh(col_offset<T, DK>(lane));
@@ -151,13 +152,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
                 for (int e = 0; e < 2; ++e) {
                     const auto x = acc_frag<T>(s, e);
 #pragma unroll
-                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<DK>(K, 32 * k + 16 * e, t, co), x, acc[t]);
+                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<T, DK>(K, 32 * k + 16 * e, t, co), x, acc[t]);
                 }
             }
         }
         land(Kn, Vn);
     };
     fetch(K0, V0);
+    arrived(qf);
+    arrived(gf);
     land(K0, V0);
     while (cnt > 0) {
         turn(K0, V0, K1, V1);
@@ -190,9 +193,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
                                                                                 int main, int nwork) {
     constexpr int QT = kQueryTile, KB = 32 * NW, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
     constexpr bool VLDS = sizeof(T) == 2;
-    __shared__ __attribute__((aligned(16))) T Vk[VLDS ? KB * DV : 1];
-    __shared__ __attribute__((aligned(16))) T Q0[QT * DK], Q1[QT * DK], G0[QT * DV], G1[QT * DV];
-    __shared__ __attribute__((aligned(16))) float R0[2 * QT], R1[2 * QT];      // lse of the rows, then delta
+    __shared__ __attribute__((aligned(16))) T Vb[VLDS ? KB * DV : 1], Qs[2][QT * DK], Gs[2][QT * DV];
+    __shared__ __attribute__((aligned(16))) float Rs[2][2 * QT];               // lse of the rows, then delta
+    const lds_c Vk = lds_of(Vb), Q0 = lds_of(Qs[0]), Q1 = lds_of(Qs[1]), G0 = lds_of(Gs[0]), G1 = lds_of(Gs[1]);
+    const lds_c R0 = lds_of(Rs[0]), R1 = lds_of(Rs[1]);
     // consecutive key blocks of a head on one XCD; the runs are dealt to all of them
     const int per = (main + 7) / 8, at = (int)(blockIdx.x >> 3);
     const int id = at < per ? (int)(blockIdx.x & 7) * per + at : (int)blockIdx.x - 8 * per + main;
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
     Copy<T, DV, QT, 64 * NW, VEC> cg;
     int t = ta, hc = 0, p0 = ta, p1 = ta;
     bool more = true;
-    auto fetch = [&](T* Q, T* Gr, float* R) {
+    auto fetch = [&](lds_c Q, lds_c Gr, lds_c R) {
         more = t < te;
         if (!more) return;
         const int n = te - t < rb.TPB ? te - t : rb.TPB, heads = G - hc * rb.HPB < rb.HPB ? G - hc * rb.HPB : rb.HPB;
@@ -299,8 +303,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
         if (w == 0) {
             const int r = lane & 31, x = (r * magic) >> 16, g = r - x * rb.HPB;
             static_assert(QT == 32, "lse and delta of a tile in 64 lanes");
-            buffer_to_lds4(buf_rsrc(a.rows + 2 * (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 8), R,
-                           r < span ? (x * Nq + g) * 8 + 4 * h : kOutside);
+            copy4_to_lds(raw_rsrc(a.rows + 2 * (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 8), R,
+                         r < span ? (x * Nq + g) * 8 + 4 * h : kOutside);
         }
         p0 = t;
         p1 = t + n - 1;
@@ -309,14 +313,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             t += rb.TPB;
         }
     };
-    auto land = [&](T* Q, T* Gr) {
+    auto land = [&](lds_c Q, lds_c Gr) {
         if (more) {
             cq.finish(Q, tid);
             cg.finish(Gr, tid);
         }
-        __syncthreads();
+        landed();
     };
-    auto turn = [&](const T* Q, const T* Gr, const float* R, T* Qn, T* Gn, float* Rn) {
+    auto turn = [&](lds_c Q, lds_c Gr, lds_c R, lds_c Qn, lds_c Gn, lds_c Rn) {
         const int a0 = p0, a1 = p1;                                // the queries' positions
         const int rq = fresh(row_offset<T, DK>(lane)), rg = DK == DV ? rq : fresh(row_offset<T, DV>(lane));
         const int cq_ = fresh(col_offset<T, DK>(lane)), cg_ = DK == DV ? cq_ : fresh(col_offset<T, DV>(lane));
@@ -330,7 +334,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 L = *reinterpret_cast<const f32x4*>(&R[8 * i + 4 * h]);
+                const f32x4 L = *(lds_p<f32x4>)(R + 32 * i + 16 * h);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     s[4 * i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
@@ -347,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             for (int e = 0; e < 2; ++e) {
                 const auto x = acc_frag<T>(s, e);
 #pragma unroll
-                for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<DV>(Gr, 16 * e, u, cg_), x, dV[u]);
+                for (int u = 0; u < DV / 32; ++u) dV[u] = mma(col_frag<T, DV>(Gr, 16 * e, u, cg_), x, dV[u]);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -355,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 D = *reinterpret_cast<const f32x4*>(&R[QT + 8 * i + 4 * h]);
+                const f32x4 D = *(lds_p<f32x4>)(R + 4 * QT + 32 * i + 16 * h);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) g[4 * i + j] = s[4 * i + j] * (g[4 * i + j] - D[j]);
             }
@@ -369,12 +373,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             for (int e = 0; e < 2; ++e) {
                 const auto y = acc_frag<T>(g, e);
 #pragma unroll
-                for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<DK>(Q, 16 * e, u, cq_), y, dK[u]);
+                for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<T, DK>(Q, 16 * e, u, cq_), y, dK[u]);
             }
         }
         land(Qn, Gn);
     };
     fetch(Q0, G0, R0);
+    arrived(kf);
+    if constexpr (!VLDS) arrived(vf);
     land(Q0, G0);
     while (more) {
         turn(Q0, G0, R0, Q1, G1, R1);
