@@ -2,29 +2,10 @@
 #include <type_traits>
 
 #include "gdr_attn.hpp"
-#include <cstdlib>
-#include <cstdio>
-#ifndef OCC64
-#define OCC64 4
-#endif
 
 namespace gdr {
 
 namespace {
-
-// Order of a run of N operands that are read from LDS in R reads each and used in M
-// products each: AHEAD operands are read before the first product.
-template <int N, int R, int M, int AHEAD = 6>
-__device__ __forceinline__ void feed() {
-    constexpr int A = AHEAD < N ? AHEAD : N;
-    __builtin_amdgcn_sched_group_barrier(0x100, A * R, 0);
-#pragma unroll
-    for (int i = 0; i < N - A; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, A * M, 0);
-}
 
 // ---------------------------------------------------------------- softmax over tiles
 // What a lane keeps of its query: the output's dims 32 t + 8 i + 4 h + j in o[t][4 i + j],
@@ -258,6 +239,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
         const int pos0 = pos, n = cnt, ro = fresh(row_offset<T, DK>(lane));
         fetch(Kn, Vn);
         f32x16 s[NT];
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int k = 0; k < NT; ++k) s[k] = zero16();
 #pragma unroll
@@ -265,13 +247,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
 #pragma unroll
             for (int k = 0; k < NT; ++k) s[k] = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s[k]);
         feed<KF * NT, 1, sizeof(T) == 2 ? 1 : 4>();
+        __builtin_amdgcn_s_setprio(0);
         const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
         const Sight sees{pos0, n, q.p, W, S};
         weigh<DV, NT>(st, s, c, partial, sees);
+        __builtin_amdgcn_s_setprio(1);
         typename Vec<T>::v8 wt[2 * NT];
 #pragma unroll
         for (int i = 0; i < 2 * NT; ++i) wt[i] = acc_frag<T>(s[i >> 1], i & 1);
         add_values<T, DV, NT>(st, wt, V, clean, partial, sees);
+        __builtin_amdgcn_s_setprio(0);
         land(Kn, Vn);
     };
     fetch(K0, V0);
@@ -286,8 +271,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock
 }
 
 // ---------------------------------------------------------------- few rows
-// 32 rows a workgroup (a token's heads of one key head, when decoding): its NW
-// wavefronts, and `splits` workgroups, share the keys. A wavefront takes 32 keys at a
+// 32 rows a workgroup: its NW wavefronts, and `splits` workgroups, share the keys. A wavefront takes 32 keys at a
 // time straight into the operand's registers, the values through LDS of its own; the
 // next 32 are under way meanwhile. What they have summed is joined in LDS, the
 // workgroups' by k_window_join.
@@ -306,14 +290,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     const int W = a.p.window, S = a.p.sinks, dk = a.p.head_dim_qk, dv = a.p.head_dim_v;
     const int len = past_len(a, b.n);
     const Query q = query_of(b, rb, G, hk, hc, lane & 31, len);
-    const bool idle = a.one && __builtin_amdgcn_readfirstlane(a.lens[b.n]) < 0;
-    if (a.one && !idle && hc == 0 && sp == 0) {
-        // the token's row in the caches held one that no query sees any more
-        const int64_t at = (int64_t)b.n * ((int64_t)S + W) + (len < S ? len : S + (len - S) % W);
-        const Source<T> s = source<T>(a, b, hk, 0, false);
-        for (int d = tid; d < dk; d += 64 * NW) ((T*)a.kc)[(at * a.p.num_kv_heads + hk) * dk + d] = s.k[d];
-        for (int d = tid; d < dv; d += 64 * NW) ((T*)a.vc)[(at * a.p.num_kv_heads + hk) * dv + d] = s.v[d];
-    }
     const int pa = __builtin_amdgcn_readlane(q.p, 0), pb = __builtin_amdgcn_readlane(q.p, 31);
     State<DV> st;
     st.clear();
@@ -324,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     const int all = keys.total(), parts = splits * NW, part = sp * NW + w;
     const int share = ((all + parts - 1) / parts + 31) / 32 * 32;
     int64_t first = (int64_t)share * part;
-    int left = idle || first >= all ? 0 : (int)(all - first < share ? all - first : share);
+    int left = first >= all ? 0 : (int)(all - first < share ? all - first : share);
     if (left > 0) keys.skip((int)first);
     if (left > 0) {
         frag_t<T> qf[KF], kf[KF];
@@ -389,7 +365,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     const int64_t row = q.token * a.p.num_q_heads + q.head, rows = a.Ttot * a.p.num_q_heads;
     const int h = lane >> 5;
     float* part_o = a.ws + (int64_t)sp * rows * (dv + 2);
-    const float inv = idle ? 0.f : 1.f / l;
+    const float inv = 1.f / l;
 #pragma unroll
     for (int t = 0; t < DV / 32; ++t) {
         float* mine = reinterpret_cast<float*>(Vs[w]);
@@ -408,13 +384,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
             const int d = 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
             if (!q.live || d >= dv) continue;
             if (splits > 1) part_o[row * (dv + 2) + d] = y;
-            else store_as<T>(a.o, row * dv + d, idle ? 0.f : y * inv, a.p.out_dtype == GDR_F32);
+            else store_as<T>(a.o, row * dv + d, y * inv, a.p.out_dtype == GDR_F32);
         }
     }
     if (w == 0 && h == 0 && q.live) {
         if (splits > 1) {
-            part_o[row * (dv + 2) + dv] = idle ? 0.f : m;
-            part_o[row * (dv + 2) + dv + 1] = idle ? -1.f : l;
+            part_o[row * (dv + 2) + dv] = m;
+            part_o[row * (dv + 2) + dv + 1] = l;
         } else if (a.lse) {
             a.lse[row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
         }
@@ -704,42 +680,46 @@ __global__ __launch_bounds__(256) void k_window_keep(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- launches
-// Whether 32 rows a workgroup, its wavefronts sharing the keys, or 32 rows a wavefront
+// Many rows: 32 a wavefront; few rows: 32 a workgroup, whose wavefronts share the keys.
+constexpr int kRowWaves = 4;
+template <typename T> constexpr int kSplitWaves = sizeof(T) == 2 ? 8 : 4;
 struct Plan {
     bool split;
-    int NW, splits;
+    int splits;
     RowBlock rb;
     int64_t nblk, nwork;
 };
 Plan plan_of(const gdr_attn_problem_t& p) {
     Plan x{};
     const int G = group(p);
-    const bool packed = p.batch == 1 && p.num_seqs != 1;
-    const int64_t rows = p.batch * p.seq_len * p.num_q_heads;
-    const int64_t keys = (int64_t)p.sinks + p.window;
-    // 32-row blocks of all heads, if none were shared out further
-    x.rb = row_block(32, G);
-    const int64_t few = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB) * p.num_kv_heads * x.rb.HC;
-    x.split = rows <= 32 * 1024;
-    if (p.seq_len == 1 && !packed) x.split = true;
-    if (getenv("GDR_SPLIT")) x.split = atoi(getenv("GDR_SPLIT"));
-    if (x.split) {
-        x.NW = p.io_dtype == GDR_BF16 ? 8 : 4;
-        x.nblk = few / (p.num_kv_heads * x.rb.HC);
-        x.nwork = few;
-        const int64_t want = few > 0 ? 512 / few : 1, most = (keys + 32 * x.NW - 1) / (32 * x.NW);
-        const int64_t s = want < most ? want : most;
-        x.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-        if (getenv("GDR_SPLITS")) x.splits = atoi(getenv("GDR_SPLITS"));
-        return x;
-    }
-    x.NW = 8;
+    const bool bf = p.io_dtype == GDR_BF16, packed = p.batch == 1 && p.num_seqs != 1;
+    auto blocks = [&](int rows) {
+        x.rb = row_block(rows, G);
+        x.nblk = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB);
+        x.nwork = x.nblk * p.num_kv_heads * x.rb.HC;
+    };
+    blocks(32);
     x.splits = 1;
-    if (getenv("GDR_NW")) x.NW = atoi(getenv("GDR_NW"));
-    x.rb = row_block(32 * x.NW, G);
-    x.nblk = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB);
-    x.nwork = x.nblk * p.num_kv_heads * x.rb.HC;
+    x.split = x.nwork <= (bf ? 256 : 512);
+    if (x.split) {
+        // workgroups share the keys too where a wavefront had 16 tiles of them and more
+        const int64_t tiles = ((int64_t)p.sinks + p.window + 31) / 32, each = tiles / (bf ? 8 : 4) / 16;
+        const int64_t want = x.nwork > 0 ? 256 / x.nwork : 1, s = want < each ? want : each;
+        x.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    } else {
+        blocks(32 * kRowWaves);
+    }
     return x;
+}
+
+// Single tokens: workgroups that share the rows of a sequence's key head
+constexpr int kStepWaves = 8;
+int step_splits(const gdr_attn_problem_t& p) {
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * ((group(p) + 15) / 16);
+    const int64_t each = ((int64_t)p.sinks + p.window) / (32 * kStepWaves);       // tiles of a wavefront
+    if (each < 8 || units < 1) return 1;
+    const int64_t want = 256 / units, s = want < each / 2 ? want : each / 2;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
 }  // namespace
@@ -748,16 +728,6 @@ size_t attn_fwd_workspace(const gdr_attn_problem_t& p) {
     const Plan x = plan_of(p);
     if (x.splits <= 1) return 0;
     return (size_t)x.splits * p.batch * p.seq_len * p.num_q_heads * (p.head_dim_v + 2) * 4;
-}
-
-// Single tokens: workgroups that share the rows of a sequence's key head
-constexpr int kStepWaves = 8;
-int step_splits(const gdr_attn_problem_t& p) {
-    if (getenv("GDR_SPLITS")) return atoi(getenv("GDR_SPLITS"));
-    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads * ((group(p) + 15) / 16), rows = (int64_t)p.sinks + p.window;
-    const int64_t want = units > 0 ? 256 / units : 1, most = rows / (32 * kStepWaves * 2);
-    const int64_t s = want < most ? want : most;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
 hipError_t launch_attn_step(const AttnArgs& a) {
@@ -791,28 +761,27 @@ size_t attn_step_workspace(const gdr_attn_problem_t& p) {
 hipError_t launch_attn_fwd(const AttnArgs& a) {
     if (a.Ttot == 0) return hipSuccess;
     const Plan x = plan_of(a.p);
-    if (x.nwork >= (int64_t)1 << 31 || !grid_fits(x.nwork * x.splits + 8, 64 * x.NW)) return hipErrorInvalidConfiguration;
+    const int64_t waves = x.split ? (a.p.io_dtype == GDR_BF16 ? kSplitWaves<bf16> : kSplitWaves<float>) : kRowWaves;
+    if (x.nwork >= (int64_t)1 << 31 || !grid_fits(x.nwork * x.splits + 8, 64 * (int)waves)) return hipErrorInvalidConfiguration;
     hipError_t e = hipSuccess;
     by_dims(a.p, [&](auto type, auto dk, auto dv) {
         typedef decltype(type) T;
-        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NWS = sizeof(T) == 2 ? 8 : 4;
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NS = kSplitWaves<T>, NR = kRowWaves;
         if (x.split) {
             const dim3 grid((unsigned)(x.nwork * x.splits));
-            if (a.vec) k_window_split<T, DK, DV, NWS, true><<<grid, 64 * NWS, 0, a.stream>>>(a, x.rb, (int)x.nblk, x.splits);
-            else k_window_split<T, DK, DV, NWS, false><<<grid, 64 * NWS, 0, a.stream>>>(a, x.rb, (int)x.nblk, x.splits);
+            if (a.vec) k_window_split<T, DK, DV, NS, true><<<grid, 64 * NS, 0, a.stream>>>(a, x.rb, (int)x.nblk, x.splits);
+            else k_window_split<T, DK, DV, NS, false><<<grid, 64 * NS, 0, a.stream>>>(a, x.rb, (int)x.nblk, x.splits);
             if (x.splits > 1) {
                 const int64_t rows = a.Ttot * a.p.num_q_heads;
                 k_window_join<T><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, a.stream>>>(a, x.splits);
             }
         } else {
             const dim3 grid((unsigned)((x.nwork + 7) / 8 * 8));
-            if (a.vec && x.NW == 2) k_window_rows<T, DK, DV, 2, true><<<grid, 128, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
-            else if (a.vec && x.NW == 4) k_window_rows<T, DK, DV, 4, true><<<grid, 256, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
-            else if (a.vec) k_window_rows<T, DK, DV, 8, true><<<grid, 512, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
-            else k_window_rows<T, DK, DV, 8, false><<<grid, 512, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            if (a.vec) k_window_rows<T, DK, DV, NR, true><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            else k_window_rows<T, DK, DV, NR, false><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
         }
         e = hipGetLastError();
-        if (e == hipSuccess && a.kc && !a.one) {
+        if (e == hipSuccess && a.kc) {
             const int64_t need = (a.Ttot + 3) / 4, most = 8192;
             const dim3 grid((unsigned)(need < most ? need : most));
             if (a.vec) k_window_keep<T, true><<<grid, 256, 0, a.stream>>>(a);

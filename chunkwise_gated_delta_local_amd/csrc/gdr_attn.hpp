@@ -24,14 +24,13 @@ namespace gdr {
 
 struct AttnArgs {
     gdr_attn_problem_t p;
-    int64_t Ttot, max_len;     // total tokens, longest sequence (host)
-    int32_t q_ld, k_ld, v_ld;  // elements between tokens of one sequence (a single token: any)
+    int64_t Ttot;              // total tokens
+    int32_t q_ld, k_ld, v_ld;  // elements between tokens
     const void *q, *k, *v;
     void *kc, *vc;             // caches or NULL
     const int32_t *lens, *cu;  // NULL: zeros; NULL: batch rows
     void* o;
     float* lse;
-    bool one;                  // single tokens: negative lens pass, the caches are written by the same kernel
     bool vec;                  // rows of q, k, v and the caches in 16-byte pieces at 16-byte addresses
     float* ws;
     // backward
@@ -312,6 +311,20 @@ __device__ __forceinline__ typename Vec<T>::v8 acc_frag(const f32x16& s, int q) 
     return x;
 }
 
+// Order of a run of N operands that are read from LDS in R reads each and used in M
+// products each: AHEAD operands are read before the first product.
+template <int N, int R, int M, int AHEAD = 6>
+__device__ __forceinline__ void feed() {
+    constexpr int A = AHEAD < N ? AHEAD : N;
+    __builtin_amdgcn_sched_group_barrier(0x100, A * R, 0);
+#pragma unroll
+    for (int i = 0; i < N - A; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, A * M, 0);
+}
+
 constexpr int kOutside = 0x7ffffff0;                       // bytes behind the end of every buffer
 // 16 bytes of a row through a range-checked buffer, zero from element d on; VEC:
 // rows begin and end at 16-byte addresses
@@ -509,9 +522,8 @@ __device__ __forceinline__ Source<T> source(const AttnArgs& a, const Block& b, i
         s.kld = Nk * dk;
         s.vld = Nk * dv;
     } else {
-        const int64_t at = b.start * (a.one ? 0 : 1);
-        s.k = (const T*)a.k + (a.one ? b.n * a.p.k_stride : (at + row) * a.p.k_stride) + hk * dk;
-        s.v = (const T*)a.v + (a.one ? b.n * a.p.v_stride : (at + row) * a.p.v_stride) + hk * dv;
+        s.k = (const T*)a.k + (b.start + row) * a.p.k_stride + hk * dk;
+        s.v = (const T*)a.v + (b.start + row) * a.p.v_stride + hk * dv;
         s.kld = a.k_ld;
         s.vld = a.v_ld;
     }

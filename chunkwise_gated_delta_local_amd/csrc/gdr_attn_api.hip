@@ -57,7 +57,6 @@ AttnArgs attn_args(const gdr_attn_problem_t* p, const void* q, const void* k, co
 gdr_status_t check_caches(const gdr_attn_problem_t* p, const void* kc, const void* vc, const int32_t* lens) {
     if ((kc == nullptr) != (vc == nullptr)) return fail(GDR_ERR_NULL, "k_cache and v_cache must both be given or both be NULL");
     if (lens && !kc) return fail(GDR_ERR_NULL, "lens without caches");
-    // rows of a cache are counted from its base in 64 bits
     return GDR_OK;
 }
 
@@ -87,7 +86,6 @@ gdr_status_t gdr_window_attn_fwd(const gdr_attn_problem_t* p, const void* q, con
     GDR_TRY(check_caches(p, k_cache, v_cache, lens));
     GDR_TRY(check_workspace(workspace, workspace_bytes, attn_fwd_workspace(*p)));
     AttnArgs a = attn_args(p, q, k, v, k_cache, v_cache, lens, cu_dev, workspace, stream);
-    a.max_len = max_len;
     a.k_ld = (int32_t)p->k_stride;
     a.v_ld = (int32_t)p->v_stride;
     a.o = o;
@@ -114,10 +112,6 @@ gdr_status_t gdr_window_attn_step(const gdr_attn_problem_t* p, const void* q, co
     GDR_TRY(check_ptrs(ptrs, p->batch > 0));
     GDR_TRY(check_workspace(workspace, workspace_bytes, attn_step_workspace(*p)));
     AttnArgs a = attn_args(p, q, k, v, k_cache, v_cache, lens, nullptr, workspace, stream);
-    a.max_len = 1;
-    a.one = true;
-    a.k_ld = p->num_kv_heads * p->head_dim_qk;           // of one row no other is reached
-    a.v_ld = p->num_kv_heads * p->head_dim_v;
     a.o = o;
     return done(launch_attn_step(a));
 }
@@ -143,7 +137,6 @@ gdr_status_t gdr_window_attn_bwd(const gdr_attn_problem_t* p, const void* q, con
     GDR_TRY(check_ptrs(ptrs, p->batch * p->seq_len > 0));
     GDR_TRY(check_workspace(workspace, workspace_bytes, attn_bwd_workspace(*p)));
     AttnArgs a = attn_args(p, q, k, v, nullptr, nullptr, nullptr, cu_dev, workspace, stream);
-    a.max_len = max_len;
     a.q_ld = (int32_t)p->q_stride;
     a.k_ld = (int32_t)p->k_stride;
     a.v_ld = (int32_t)p->v_stride;

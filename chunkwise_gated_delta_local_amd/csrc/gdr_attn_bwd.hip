@@ -139,8 +139,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
                 f32x16 s = zero16(), g = zero16();
 #pragma unroll
                 for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s);
+                feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
 #pragma unroll
                 for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, rv), gf[t], g);
+                feed<VF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
