@@ -137,12 +137,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
                 f32x16 s = zero16(), g = zero16();
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s);
                 feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
 #pragma unroll
                 for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, rv), gf[t], g);
                 feed<VF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
+                __builtin_amdgcn_s_setprio(0);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
@@ -150,12 +152,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[i] = sees(32 * k + 8 * (i >> 2) + 4 * h + (i & 3)) ? s[i] : 0.f;
                 }
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const auto x = acc_frag<T>(s, e);
 #pragma unroll
                     for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<T, DK>(K, 32 * k + 16 * e, t, co), x, acc[t]);
                 }
+                __builtin_amdgcn_s_setprio(0);
             }
         }
         land(Kn, Vn);
@@ -329,26 +333,41 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
         fetch(Qn, Gn, Rn);
         if (ja <= jb && a1 >= ja && (ja < S || a0 <= jb + (int64_t)W - 1)) {
             const bool partial = a0 < jb || (a1 - W >= ja && jb >= S);
-            // one product after the other: what each needs in registers leaves room for two wavefronts a SIMD
+            // products, vector work and products again, each for itself: what they need in
+            // registers leaves room for two wavefronts a SIMD, of which the one with products
+            // goes first
             f32x16 s = zero16(), g = zero16();
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Q, 0, u, rq), kf[u], s);
+            feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, rg), v_frag(u, rg), g);
+            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 L = *(lds_p<f32x4>)(R + 32 * i + 16 * h);
+                const f32x4 L = *(lds_p<f32x4>)(R + 32 * i + 16 * h), D = *(lds_p<f32x4>)(R + 4 * QT + 32 * i + 16 * h);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[4 * i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
+                for (int j = 0; j < 4; ++j) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -L[j]));
+                    s[4 * i + j] = p;
+                    g[4 * i + j] = p * (g[4 * i + j] - D[j]);
+                }
             }
             if (partial) {
+                asm volatile("");
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int r = 8 * (i >> 2) + 4 * h + (i & 3), p = a0 + ((r * magic) >> 16);
-                    s[i] = (unsigned)(p - mine) < mine_for ? s[i] : 0.f;
+                    const bool see = (unsigned)(p - mine) < mine_for;
+                    s[i] = see ? s[i] : 0.f;
+                    g[i] = see ? g[i] : 0.f;
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const auto x = acc_frag<T>(s, e);
@@ -357,26 +376,12 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, rg), v_frag(u, rg), g);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 D = *(lds_p<f32x4>)(R + 4 * QT + 32 * i + 16 * h);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) g[4 * i + j] = s[4 * i + j] * (g[4 * i + j] - D[j]);
-            }
-            if (partial) {                                         // what a key does not see may be NaN
-                asm volatile("");
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g[i] = s[i] == 0.f ? 0.f : g[i];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const auto y = acc_frag<T>(g, e);
 #pragma unroll
                 for (int u = 0; u < DK / 32; ++u) dK[u] = mma(col_frag<T, DK>(Q, 16 * e, u, cq_), y, dK[u]);
             }
+            __builtin_amdgcn_s_setprio(0);
         }
         land(Qn, Gn);
     };
@@ -497,7 +502,7 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
     hipError_t e = hipSuccess;
     by_dims(a.p, [&](auto type, auto dk, auto dv) {
         typedef decltype(type) T;
-        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NQ = 8, NK = 4, KB = 32 * NK;
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, NQ = 4, NK = 4, KB = 32 * NK;
         constexpr int QT = kQueryTile;
         const RowBlock rq = row_block(32 * NQ, G), rk = row_block(QT, G);
         const int64_t bq = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, rq.TPB), wq = bq * Nk * rq.HC;
