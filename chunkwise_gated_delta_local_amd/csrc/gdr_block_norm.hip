@@ -2,9 +2,17 @@
 // (include/gdr_mixer.h). A few operations an element: HBM bounds them, so a row is
 // read once and stays in registers between its sums and its outputs. TPR threads share
 // a row, each holding NV pieces of V = 16 bytes of the io type; rows go round the
-// grid, and up to 256 threads a row the next row is on its way while one is worked on,
-// with the parameters in registers. Longer rows take 512 or 1,024 threads, whose
-// fewer registers hold one row and no parameters.
+// grid, and up to 512 threads a row (forward up to 1,024, one piece each) the next row
+// is on its way while one is worked on, with the parameters in registers. A thread holds
+// one piece where it can: with four pieces a thread, 256 threads a row of 8,192, the
+// backward pass took 276 us for 4,096 rows, with one piece 151. What overflows into scratch
+// all the same: the backward passes of rows beyond 8,192 (the residual sum's from 4,097
+// on, 130 registers) and the residual sum's forward pass beyond 8,192.
+//
+// Measured in bf16, at the rate of a copy (5.92 TB/s) in brackets: gated rows of 128,
+// 2,097,152 of them, 302 us (274), 524,288 backward 113 us (114); residual sums of rows of
+// 4,096, 16,384 of them, with both norms and a gate per channel 103 us (91), backward with a
+// gate per token 188 us (181); 256 rows 5.0 us replayed from a graph.
 #include <type_traits>
 
 #include "gdr_norm.hpp"
@@ -23,18 +31,18 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[kBlock<TPR> / 64]
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
         __syncthreads();
+        const int first = (int)threadIdx.x / TPR * (TPR / 64);
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) v += red[slot][i];
+        for (int i = 0; i < TPR / 64; ++i) v += red[slot][first + i];
         slot ^= 1;
     }
     return v;
 }
 
 // A parameter's pieces: kept in registers or read again for every row
-template <typename T, int V, int NV, int TPR>
+template <typename T, int V, int NV, int TPR, bool KEEP>
 struct Param {
-    static constexpr bool KEEP = TPR <= 256;
     const void* p;
     int C, f32;
     float none, kept[KEEP ? NV : 1][V];
@@ -55,26 +63,22 @@ struct Param {
     }
 };
 
-// act(z) and its derivative; silu is z sigmoid(z)
+// act(z); silu is z sigmoid(z)
 __device__ __forceinline__ float gate_of(float z, bool silu_) {
     const float s = sigmoid(z);
     return silu_ ? z * s : s;
-}
-__device__ __forceinline__ float gate_slope(float z, bool silu_) {
-    const float s = sigmoid(z);
-    return silu_ ? silu_slope(z, s) : s * (1.f - s);
 }
 
 // ---------------------------------------------------------------- gated norm
 template <typename T, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_fwd(GatedNormArgs a) {
     constexpr int RPB = kBlock<TPR> / TPR;
-    constexpr bool AHEAD = TPR <= 256;
+    constexpr bool AHEAD = NV * V <= 8;
     __shared__ float red[2][kBlock<TPR> / 64];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR;
     const bool act = a.p.activation == GDR_ACT_SILU;
-    const Param<T, V, NV, TPR> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
+    const Param<T, V, NV, TPR, NV * V <= 8> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
     const float inv = 1.f / (float)C;
     typename Raw<T, V>::type rx[NV], rz[NV];
     auto fetch = [&](int64_t r) {
@@ -154,14 +158,14 @@ __device__ __forceinline__ void put_sums(float* part, const float (&s)[NV][V], i
 template <typename T, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a) {
     constexpr int RPB = kBlock<TPR> / TPR;
-    constexpr bool AHEAD = TPR <= 256;
+    constexpr bool AHEAD = TPR <= 512;
     __shared__ float red[2][kBlock<TPR> / 64];
     __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR;
     const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
     const bool act = a.p.activation == GDR_ACT_SILU;
-    const Param<T, V, NV, TPR> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
+    const Param<T, V, NV, TPR, NV * V <= 8> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
     const float inv = 1.f / (float)C;
     float dw[NV][V];
 #pragma unroll
@@ -238,13 +242,13 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a)
 template <typename T, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_fwd(ResidualNormArgs a) {
     constexpr int RPB = kBlock<TPR> / TPR;
-    constexpr bool AHEAD = TPR <= 256;
+    constexpr bool AHEAD = NV * V <= 8;
     __shared__ float red[2][kBlock<TPR> / 64];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR, p32 = a.p.param_dtype == GDR_F32, s32 = a.p.stream_dtype == GDR_F32;
     const bool post = a.x_weight != nullptr, token = a.p.gate == GDR_GATE_TOKEN;
-    const Param<T, V, NV, TPR> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f);
-    const Param<T, V, NV, TPR> gc(a.p.gate == GDR_GATE_CHANNEL ? a.gate : nullptr, C, p32, 1.f);
+    const Param<T, V, NV, TPR, TPR <= 512> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f);
+    const Param<T, V, NV, TPR, TPR <= 512> gc(a.p.gate == GDR_GATE_CHANNEL ? a.gate : nullptr, C, p32, 1.f);
     const float inv = 1.f / (float)C;
     typename Raw<T, V>::type rx[NV], rg[NV];
     AnyPiece<V> rs[NV];
@@ -321,14 +325,14 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_fwd(ResidualNormA
 template <typename T, int V, int NV, int TPR, bool ONCE>
 __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_bwd(ResidualNormArgs a) {
     constexpr int RPB = kBlock<TPR> / TPR;
-    constexpr bool AHEAD = TPR <= 256;
+    constexpr bool AHEAD = TPR <= 512;
     __shared__ float red[2][kBlock<TPR> / 64];
     __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR, p32 = a.p.param_dtype == GDR_F32, s32 = a.p.stream_dtype == GDR_F32;
     const int dy32 = a.p.dy_dtype == GDR_F32, dh32 = a.p.dh_dtype == GDR_F32;
     const bool post = a.x_weight != nullptr, token = a.p.gate == GDR_GATE_TOKEN, chan = a.p.gate == GDR_GATE_CHANNEL;
-    const Param<T, V, NV, TPR> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f), gc(chan ? a.gate : nullptr, C, p32, 1.f);
+    const Param<T, V, NV, TPR, TPR <= 512> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f), gc(chan ? a.gate : nullptr, C, p32, 1.f);
     const float inv = 1.f / (float)C;
     float dw[NV][V], dxw[NV][V], dg[NV][V];
 #pragma unroll
@@ -446,15 +450,12 @@ struct Shape {
     int NV, TPR;
 };
 Shape shape_of(bool bf, int C) {
-    const Shape b[] = {{1, 16}, {1, 64}, {2, 64}, {1, 256}, {2, 256}, {2, 512}, {2, 1024}};
-    const Shape f[] = {{1, 16}, {2, 16}, {1, 64}, {2, 64}, {4, 64}, {2, 256}, {4, 256}, {4, 512}, {4, 1024}};
-    const int V = bf ? 8 : 4;
-    if (bf) {
-        for (const Shape& s : b)
-            if (C <= V * s.NV * s.TPR) return s;
-    } else {
-        for (const Shape& s : f)
-            if (C <= V * s.NV * s.TPR) return s;
+    const Shape b[] = {{1, 16}, {1, 64}, {1, 128}, {1, 256}, {1, 512}, {1, 1024}, {2, 1024}};
+    const Shape f[] = {{1, 16}, {2, 16}, {1, 64}, {2, 64}, {2, 128}, {2, 256}, {2, 512}, {2, 1024}, {4, 1024}};
+    const int V = bf ? 8 : 4, n = bf ? 7 : 9;
+    for (int i = 0; i < n; ++i) {
+        const Shape s = bf ? b[i] : f[i];
+        if (C <= V * s.NV * s.TPR) return s;
     }
     return {0, 0};
 }
@@ -469,28 +470,34 @@ hipError_t by_shape(bool bf, int C, F f) {
         return hipGetLastError();                                                                                     \
     }
     if (bf) {
-        GDR_SHAPE(bf16, 8, 1, 16) GDR_SHAPE(bf16, 8, 1, 64) GDR_SHAPE(bf16, 8, 2, 64) GDR_SHAPE(bf16, 8, 1, 256)
-        GDR_SHAPE(bf16, 8, 2, 256) GDR_SHAPE(bf16, 8, 2, 512) GDR_SHAPE(bf16, 8, 2, 1024)
+        GDR_SHAPE(bf16, 8, 1, 16) GDR_SHAPE(bf16, 8, 1, 64) GDR_SHAPE(bf16, 8, 1, 128) GDR_SHAPE(bf16, 8, 1, 256)
+        GDR_SHAPE(bf16, 8, 1, 512) GDR_SHAPE(bf16, 8, 1, 1024) GDR_SHAPE(bf16, 8, 2, 1024)
     } else {
         GDR_SHAPE(float, 4, 1, 16) GDR_SHAPE(float, 4, 2, 16) GDR_SHAPE(float, 4, 1, 64) GDR_SHAPE(float, 4, 2, 64)
-        GDR_SHAPE(float, 4, 4, 64) GDR_SHAPE(float, 4, 2, 256) GDR_SHAPE(float, 4, 4, 256) GDR_SHAPE(float, 4, 4, 512)
+        GDR_SHAPE(float, 4, 2, 128) GDR_SHAPE(float, 4, 2, 256) GDR_SHAPE(float, 4, 2, 512) GDR_SHAPE(float, 4, 2, 1024)
         GDR_SHAPE(float, 4, 4, 1024)
     }
 #undef GDR_SHAPE
     return hipErrorInvalidValue;
 }
+
 int64_t row_blocks(int64_t rows, int TPR) {
     const int rpb = TPR < 256 ? 256 / TPR : 1;
     return (rows + rpb - 1) / rpb;
 }
-// four rows a thread where there are many, and never more threads than 32 bits count
+// Workgroups that the rows go round. With fewer a workgroup's next row is on its way while
+// it works, with more the card has more rows in flight: rows of 1,024 (bf16) took 132 us in
+// 512 workgroups, 111 in 8,192, and 111 in 16,384; rows of 4,096 102, 115 and 124.
 unsigned fwd_blocks(int64_t rows, int TPR) {
-    const int64_t n = row_blocks(rows, TPR), least = 8192, most = (int64_t)1 << 21;
-    const int64_t quarter = n / 4 > least ? n / 4 : least;
-    return (unsigned)(n < quarter ? n : quarter < most ? quarter : most);
+    const int64_t n = row_blocks(rows, TPR), most = TPR < 256 ? 8192 : 1024;
+    return (unsigned)(n < most ? n : most);
 }
+// Backward, each workgroup leaves its sums for the parameters: rows of 1,024 took 274 us in
+// 256 workgroups, 201 in 512 and 205 in 1,024, rows of 4,096 188, 192 and 201, and rows of
+// 8,192 151, 172 and 218.
 int bwd_blocks(int64_t rows, bool bf, int C) {
-    const int64_t n = row_blocks(rows, shape_of(bf, C).TPR), most = 512;
+    const int TPR = shape_of(bf, C).TPR;
+    const int64_t n = row_blocks(rows, TPR), most = TPR < 256 ? 512 : 256;
     return (int)(n < most ? n : most);
 }
 
