@@ -4,10 +4,10 @@
 // a row, each holding NV pieces of V = 16 bytes of the io type; rows go round the
 // grid, and up to 512 threads a row (forward up to 1,024, one piece each) the next row
 // is on its way while one is worked on, with the parameters in registers. A thread holds
-// one piece where it can: with four pieces a thread, 256 threads a row of 8,192, the
-// backward pass took 276 us for 4,096 rows, with one piece 151. What overflows into scratch
-// all the same: the backward passes of rows beyond 8,192 (the residual sum's from 4,097
-// on, 130 registers) and the residual sum's forward pass beyond 8,192.
+// one piece where it can: 4,096 rows of 8,192 took the backward pass 276 us with four pieces
+// and 256 threads, 152 with one, 132 with the parameters' sums in LDS. Rows beyond 8,192
+// overflow into scratch all the same (16,384, forward and backward: gated 83 and 260 us, where a
+// copy would take 68 and 113; residual sums 205 and 573, 113 and 181), but for the gated forward pass.
 //
 // Measured in bf16, at the rate of a copy (5.92 TB/s) in brackets: gated rows of 128,
 // 2,097,152 of them, 302 us (274), 524,288 backward 113 us (114); residual sums of rows of
@@ -125,10 +125,48 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_fwd(GatedNormArgs a)
     }
 }
 
+// A thread's sums over its rows, a parameter's gradient: in registers, or in LDS where a
+// row has 1,024 threads, whose 128 registers would overflow into scratch
+template <int V, int NV, int TPR, bool SHARED>
+struct Sums {
+    float r[NV][V];
+    __device__ __forceinline__ explicit Sums(float*) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[i][v] = 0.f;
+    }
+    __device__ __forceinline__ void add(int i, const float (&x)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[i][v] += x[v];
+    }
+    __device__ __forceinline__ void get(int i, float (&x)[V]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = r[i][v];
+    }
+};
+template <int V, int NV, int TPR>
+struct Sums<V, NV, TPR, true> {
+    f32x4* p;                      // [NV][V / 4][TPR], so that the lanes' 16 bytes follow each other
+    __device__ __forceinline__ explicit Sums(float* lds) : p((f32x4*)lds + threadIdx.x) {
+#pragma unroll
+        for (int i = 0; i < NV * V / 4; ++i) p[i * TPR] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ void add(int i, const float (&x)[V]) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+            p[(i * (V / 4) + j) * TPR] += f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+    }
+    __device__ __forceinline__ void get(int i, float (&x)[V]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = p[(i * (V / 4) + v / 4) * TPR][v % 4];
+    }
+};
+
 // A workgroup's sums of its rows to memory: in LDS over the rows that it takes at a
 // time, then a thread a column.
-template <int V, int NV, int TPR>
-__device__ __forceinline__ void put_sums(float* part, const float (&s)[NV][V], int C, float* cols) {
+template <int V, int NV, int TPR, bool SHARED>
+__device__ __forceinline__ void put_sums(float* part, const Sums<V, NV, TPR, SHARED>& s, int C, float* cols) {
     constexpr int RPB = kBlock<TPR> / TPR;
     const int l = threadIdx.x % TPR, rr = threadIdx.x / TPR;
     if constexpr (RPB > 1) {
@@ -136,7 +174,7 @@ __device__ __forceinline__ void put_sums(float* part, const float (&s)[NV][V], i
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) cols[rr * (NV * TPR * V) + (i * TPR + l) * V + v] = s[i][v];
+            for (int v = 0; v < V; ++v) cols[rr * (NV * TPR * V) + (i * TPR + l) * V + v] = s.r[i][v];
         __syncthreads();
         for (int c = threadIdx.x; c < C; c += kBlock<TPR>) {
             float x = 0.f;
@@ -148,7 +186,9 @@ __device__ __forceinline__ void put_sums(float* part, const float (&s)[NV][V], i
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + l) * V;
-            if (c < C) store_piece<float, V>(part, c, C, s[i]);
+            float x[V];
+            s.get(i, x);
+            if (c < C) store_piece<float, V>(part, c, C, x);
         }
     }
 }
@@ -160,18 +200,15 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a)
     constexpr int RPB = kBlock<TPR> / TPR;
     constexpr bool AHEAD = TPR <= 512;
     __shared__ float red[2][kBlock<TPR> / 64];
-    __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
+    constexpr bool SHARED = TPR == 1024;
+    __shared__ __attribute__((aligned(16))) float cols[RPB > 1 || SHARED ? RPB * NV * TPR * V : 1];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR;
     const int dy32 = a.p.dy_dtype == GDR_F32, g32 = a.p.grad_dtype == GDR_F32;
     const bool act = a.p.activation == GDR_ACT_SILU;
     const Param<T, V, NV, TPR, NV * V <= 8> w(a.weight, C, a.p.param_dtype == GDR_F32, 1.f);
     const float inv = 1.f / (float)C;
-    float dw[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = 0.f;
+    Sums<V, NV, TPR, SHARED> dw(cols);
     typename Raw<T, V>::type rx[NV], rz[NV];
     AnyPiece<V> rd[NV];
     float rr = 0.f;
@@ -209,18 +246,19 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a)
         if (AHEAD) fetch(r + step);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[V];
+            float f[V], e[V];
             w.get(i, f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float sg = sigmoid(z[i][v]), ac = act ? z[i][v] * sg : sg;
                 const float slope = act ? silu_slope(z[i][v], sg) : sg * (1.f - sg);
                 const float da = g[i][v] * ac;
-                dw[i][v] = __builtin_fmaf(da, x[i][v], dw[i][v]);
+                e[v] = da * x[i][v];
                 z[i][v] = g[i][v] * x[i][v] * f[v] * slope;        // dz
                 g[i][v] = da * f[v];                               // c
                 s = __builtin_fmaf(g[i][v], x[i][v], s);
             }
+            dw.add(i, e);
         }
         s = row_sum<TPR>(s, red, slot) * inv;
         if (!live) continue;
@@ -235,7 +273,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_gated_norm_bwd(GatedNormArgs a)
             store_any<T, V, ONCE>(a.dz, r * C, c, C, g32, z[i]);
         }
     }
-    if (a.dweight) put_sums<V, NV, TPR>(a.partial + (int64_t)blockIdx.x * C, dw, C, cols);
+    if (a.dweight) put_sums(a.partial + (int64_t)blockIdx.x * C, dw, C, cols);
 }
 
 // ---------------------------------------------------------------- residual sum with norms
@@ -327,18 +365,16 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_bwd(ResidualNormA
     constexpr int RPB = kBlock<TPR> / TPR;
     constexpr bool AHEAD = TPR <= 512;
     __shared__ float red[2][kBlock<TPR> / 64];
-    __shared__ float cols[RPB > 1 ? RPB * NV * TPR * V : 1];
+    constexpr bool SHARED = TPR == 1024;
+    __shared__ __attribute__((aligned(16))) float cols[RPB > 1 ? RPB * NV * TPR * V : SHARED ? 2 * NV * TPR * V : 1];
     int slot = 0;
     const int C = a.p.cols, l = threadIdx.x % TPR, p32 = a.p.param_dtype == GDR_F32, s32 = a.p.stream_dtype == GDR_F32;
     const int dy32 = a.p.dy_dtype == GDR_F32, dh32 = a.p.dh_dtype == GDR_F32;
     const bool post = a.x_weight != nullptr, token = a.p.gate == GDR_GATE_TOKEN, chan = a.p.gate == GDR_GATE_CHANNEL;
     const Param<T, V, NV, TPR, TPR <= 512> w(a.weight, C, p32, 1.f), xw(a.x_weight, C, p32, 1.f), gc(chan ? a.gate : nullptr, C, p32, 1.f);
     const float inv = 1.f / (float)C;
-    float dw[NV][V], dxw[NV][V], dg[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = dxw[i][v] = dg[i][v] = 0.f;
+    Sums<V, NV, TPR, SHARED> dw(cols), dxw(cols + NV * TPR * V * SHARED);
+    Sums<V, NV, TPR, false> dg(nullptr);
     typename Raw<T, V>::type rx[NV], rg[NV];
     AnyPiece<V> rh[NV], ry[NV], rd[NV];
     float r1 = 0.f, r2 = 1.f;
@@ -383,33 +419,35 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_bwd(ResidualNormA
         if (AHEAD) fetch(r + step);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[V];
+            float f[V], e[V];
             w.get(i, f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                dw[i][v] = __builtin_fmaf(c1[i][v], h[i][v], dw[i][v]);
+                e[v] = c1[i][v] * h[i][v];
                 c1[i][v] *= f[v];
                 s = __builtin_fmaf(c1[i][v], h[i][v], s);
             }
+            dw.add(i, e);
         }
         s = row_sum<TPR>(s, red, slot) * inv;
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + l) * V;
-            float f[V], k[V];
+            float f[V], k[V], e[V];
             xw.get(i, f);
             gc.get(i, k);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 d[i][v] = __builtin_fmaf(rstd, c1[i][v] - h[i][v] * s, d[i][v]);       // dh
                 const float m = a.p.scale * (k[v] * g[i][v]) * d[i][v];
-                dxw[i][v] = __builtin_fmaf(m, x[i][v], dxw[i][v]);
+                e[v] = m * x[i][v];
                 g[i][v] = a.p.scale * d[i][v] * x[i][v] * f[v];                        // dgate
-                dg[i][v] += g[i][v];
                 h[i][v] = m * f[v];
                 t = __builtin_fmaf(h[i][v], x[i][v], t);
             }
+            dxw.add(i, e);
+            dg.add(i, g[i]);
             if (!live || c >= C) continue;
             store_any<T, V, ONCE>(a.dresidual, r * C, c, C, a.p.dres_dtype == GDR_F32, d[i]);
             if (token && a.dgate) store_any<T, V, ONCE>(a.dgate, r * C, c, C, a.p.grad_dtype == GDR_F32, g[i]);
@@ -427,9 +465,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void k_residual_norm_bwd(ResidualNormA
         }
     }
     float* part = a.partial + (int64_t)blockIdx.x * 3 * C;
-    put_sums<V, NV, TPR>(part, dw, C, cols);
-    if (post) put_sums<V, NV, TPR>(part + C, dxw, C, cols);
-    if (chan) put_sums<V, NV, TPR>(part + 2 * (int64_t)C, dg, C, cols);
+    put_sums(part, dw, C, cols);
+    if (post) put_sums(part + C, dxw, C, cols);
+    if (chan) put_sums(part + 2 * (int64_t)C, dg, C, cols);
 }
 
 struct OneSum {
@@ -493,8 +531,7 @@ unsigned fwd_blocks(int64_t rows, int TPR) {
     return (unsigned)(n < most ? n : most);
 }
 // Backward, each workgroup leaves its sums for the parameters: rows of 1,024 took 274 us in
-// 256 workgroups, 201 in 512 and 205 in 1,024, rows of 4,096 188, 192 and 201, and rows of
-// 8,192 151, 172 and 218.
+// 256 workgroups, 201 in 512 and 205 in 1,024, rows of 4,096 188, 192 and 201.
 int bwd_blocks(int64_t rows, bool bf, int C) {
     const int TPR = shape_of(bf, C).TPR;
     const int64_t n = row_blocks(rows, TPR), most = TPR < 256 ? 512 : 256;
