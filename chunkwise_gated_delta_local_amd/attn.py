@@ -122,6 +122,8 @@ def window_attn_bwd(q, k, v, o, lse, d_o, window, sinks=0, scale=None, cu_seqlen
     _check_window(window, sinks, scale)
     io, grad = q.dtype, _grad_dtype(grad_dtype, q.dtype)
     N, cu, host = _seqs(q.shape[0], cu_seqlens, cu_seqlens_cpu, dev)
+    if o is None or lse is None or d_o is None:
+        raise ValueError("o, lse and d_o are required")
     shape = q.shape[:3] + v.shape[3:]
     _dense(o, "o", shape, (io, torch.float32), dev)
     _dense(d_o, "d_o", shape, (io, torch.float32), dev)

@@ -463,6 +463,8 @@ struct Plan {
     size_t rows, d_o16, table, part;   // bytes
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
+// A sequence has no more sinks than tokens
+int sinks_of(const gdr_attn_problem_t& p) { return p.sinks < p.seq_len ? p.sinks : (int)p.seq_len; }
 Plan plan_of(const gdr_attn_problem_t& p) {
     Plan x{};
     const int64_t T = p.batch * p.seq_len, W = p.window;
@@ -474,7 +476,8 @@ Plan plan_of(const gdr_attn_problem_t& p) {
         const int64_t longer = T / (W + 1);                        // sequences that can be longer than a window
         x.slots = T / x.run + 2 * (longer < p.num_seqs ? longer : p.num_seqs) + 1;
         x.table = up(((size_t)p.num_seqs + 1) * 4);
-        x.part = up((size_t)x.slots * p.sinks * p.num_kv_heads * (p.head_dim_qk + p.head_dim_v) * 4);
+        const double rows = (double)x.slots * sinks_of(p) * p.num_kv_heads;      // more than a launch takes: any number
+        x.part = up((rows < 0x1p40 ? (size_t)rows : (size_t)1 << 40) * (p.head_dim_qk + p.head_dim_v) * 4);
     }
     return x;
 }
@@ -490,6 +493,7 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
     AttnArgs a = in;
     if (a.Ttot == 0) return hipSuccess;
     const Plan x = plan_of(a.p);
+    a.p.sinks = sinks_of(a.p);
     char* ws = reinterpret_cast<char*>(a.ws);
     a.rows = reinterpret_cast<float*>(ws);
     a.d_o16 = x.d_o16 ? ws + x.rows : nullptr;
@@ -507,7 +511,7 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
         const RowBlock rq = row_block(32 * NQ, G), rk = row_block(QT, G);
         const int64_t bq = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, rq.TPB), wq = bq * Nk * rq.HC;
         const int64_t bk = token_blocks(a.p.batch, a.p.seq_len, a.p.num_seqs, packed, KB), wm = bk * Nk;
-        const int64_t wk = wm + x.slots * Nk * ((a.p.sinks + KB - 1) / KB);
+        const int64_t wk = wm + x.slots * Nk * (((int64_t)a.p.sinks + KB - 1) / KB);
         if (wq >= (int64_t)1 << 31 || wk >= (int64_t)1 << 31 || !grid_fits(wq + 8, 64 * NQ) || !grid_fits(wk + 8, 64 * NK)) {
             e = hipErrorInvalidConfiguration;
             return;
