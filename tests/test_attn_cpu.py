@@ -418,3 +418,52 @@ def test_rows_of_a_block(model):
             assert heads * tokens <= rows and tokens >= 1 and (blocks - 1) * heads < G <= blocks * heads
             for r in range(heads * tokens):                # the division by multiplication that the kernels make
                 assert (r * ((65536 + heads - 1) // heads)) >> 16 == r // heads
+
+
+# ---------------------------------------------------------------- the bounds notice mistakes
+MISTAKES = {
+    "window one longer": lambda p, j, W, S: (j <= p) & ((p - j < W + 1) | (j < S)),
+    "window one shorter": lambda p, j, W, S: (j <= p) & ((p - j < max(W - 1, 1)) | (j < S)),
+    "one sink less": lambda p, j, W, S: (j <= p) & ((p - j < W) | (j < S - 1)),
+    "sinks of the first tokens alone": lambda p, j, W, S: (j <= p) & ((p - j < W) | ((j < S) & (p < 2 * W))),
+    "a token ahead": lambda p, j, W, S: (j <= p + 1) & ((p - j < W) | (j < S)),
+    "not itself": lambda p, j, W, S: ((j < p) | (j == 0)) & ((p - j < W) | (j < S)),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mistake", sorted(MISTAKES))
+def test_bounds_notice_a_wrong_mask(monkeypatch, mistake, dtype):
+    import numpy as np
+    import attn_common as ac
+    c = ac.attn_case(dtype, [70, 23], 4, 2, 32, 24, 12, 2, seed=3)
+    o, lse, eo, el, _ = ac.forward_reference(c)
+    grads = ac.backward_reference(c, o, lse)
+    monkeypatch.setattr(ac.oa, "sees", MISTAKES[mistake])
+    o2, lse2 = ac.forward_reference(c)[:2]
+    half = torch.finfo(c["q"].dtype).eps / 2
+    assert (np.abs(o2 - o) > 4 * (eo + half * np.abs(o))).any() and (np.abs(lse2 - lse) > 4 * el).any()
+    wrong = ac.backward_reference(c, o, lse)
+    for name, (g, e) in grads.items():
+        assert (np.abs(wrong[name][0] - g) > 4 * (e + half * np.abs(g))).any(), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bounds_notice_a_lost_key_and_a_wrong_head(dtype):
+    """A key that is left out of one row, a tile's sums that are not rescaled, a neighbour's key head."""
+    import numpy as np
+    import attn_common as ac
+    c = ac.attn_case(dtype, [90], 4, 2, 32, 32, 64, 1, seed=4)
+    o, lse, eo, el, _ = ac.forward_reference(c)
+    half = torch.finfo(c["q"].dtype).eps / 2
+    q, k, v = ac.f64(c["q"])[0], ac.f64(c["k"])[0], ac.f64(c["v"])[0]
+    at = np.arange(90)
+    _, _, p = ac.oa.attend(q[:, 0], k[:, 0], v[:, 0], at, at, 64, 1, c["scale"])
+    limit = 4 * (eo[:, 0] + half * np.abs(o[:, 0]))
+    lost = p.copy()
+    lost[89, 60] = 0
+    assert (np.abs(lost @ v[:, 0] - o[:, 0])[89] > limit[89]).any()
+    part = p.copy()
+    part[:, :32] *= 2.0                                  # the reference moved by one in the exponent
+    assert (np.abs((part / part.sum(1, keepdims=True)) @ v[:, 0] - o[:, 0]) > limit).any()
+    assert (np.abs(p @ v[:, 1] - o[:, 0]) > limit).any()
