@@ -289,3 +289,31 @@ def test_empty_calls():
     y, h, r, xr = gdr.residual_norm_fwd(z, z, w, x_weight=w, gate=w)
     g = gdr.residual_norm_bwd(z, h, z, r, w, x_weight=w, x_rstd=xr, gate=w)
     assert y.shape == h.shape == (0, 64) and not g["dweight"].any() and not g["dx_weight"].any() and not g["dgate"].any()
+
+
+@pytest.mark.parametrize("dtype,R,C", [("bf16", 5, 700), ("f32", 7, 900), ("bf16", 1100, 4500), ("f32", 1030, 6000), ("bf16", 301, 8192),
+                                       ("bf16", 259, 12000), ("f32", 263, 9000), ("bf16", 2049, 2050), ("f32", 515, 2100)])
+def test_rows_that_go_round_the_grid(dtype, R, C):
+    """More rows than workgroups take at a time: rows alone give the same bits, and the parameters' gradients are sums over
+    all rows."""
+    c = residual_case(R, C, dtype, dtype, "f32", True, "token")
+    x, res, w, xw, gate = (dev(c[k]) for k in ("x", "res", "w", "xw", "g"))
+    kw = dict(x_weight=xw, scale=0.6)
+    y, h, r, xr = gdr.residual_norm_fwd(x, res, w, gate=gate, **kw)
+    n, nr = gdr.gated_norm_fwd(x, res, w)
+    g = gdr.residual_norm_bwd(x, h, y, r, w, d_h=h, x_rstd=xr, gate=gate, **kw)
+    gg = gdr.gated_norm_bwd(x, res, y, nr, w)
+    for s in (slice(0, 1), slice(R // 2, R // 2 + 2), slice(R - 1, R)):
+        ys, hs, rs, xs = gdr.residual_norm_fwd(x[s], res[s], w, gate=gate[s], **kw)
+        assert torch.equal(ys, y[s]) and torch.equal(hs, h[s]) and torch.equal(rs, r[s]) and torch.equal(xs, xr[s])
+        assert torch.equal(gdr.gated_norm_fwd(x[s], res[s], w)[0], n[s])
+        gs = gdr.residual_norm_bwd(x[s], hs, ys, rs, w, d_h=hs, x_rstd=xs, gate=gate[s], **kw)
+        assert all(torch.equal(gs[k], g[k][s]) for k in ("dx", "dresidual", "dgate"))
+        gs = gdr.gated_norm_bwd(x[s], res[s], ys, nr[s], w)
+        assert torch.equal(gs["dx"], gg["dx"][s]) and torch.equal(gs["dz"], gg["dz"][s])
+    hat = f64(h) * f64(r)[:, None]
+    close("dweight", g["dweight"], (f64(y) * hat).sum(0), np.abs(f64(y) * hat).sum(0), R + 30)
+    xh, dh = f64(x) * f64(xr)[:, None], f64(g["dresidual"])
+    m = float(np.float32(0.6)) * f64(gate) * dh
+    # the gradient of h is itself rounded once to fp32 where it was written
+    close("dx_weight", g["dx_weight"], (m * xh).sum(0), np.abs(m * xh).sum(0), R + 40)
