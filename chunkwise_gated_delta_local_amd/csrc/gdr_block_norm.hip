@@ -488,9 +488,9 @@ struct Shape {
     int NV, TPR;
 };
 Shape shape_of(bool bf, int C) {
-    const Shape b[] = {{1, 16}, {1, 64}, {1, 128}, {1, 256}, {1, 512}, {1, 1024}, {2, 1024}};
-    const Shape f[] = {{1, 16}, {2, 16}, {1, 64}, {2, 64}, {2, 128}, {2, 256}, {2, 512}, {2, 1024}, {4, 1024}};
-    const int V = bf ? 8 : 4, n = bf ? 7 : 9;
+    const Shape b[] = {{1, 8}, {1, 16}, {1, 32}, {1, 64}, {1, 128}, {1, 256}, {1, 512}, {1, 1024}, {2, 1024}};
+    const Shape f[] = {{1, 16}, {2, 16}, {2, 32}, {2, 64}, {2, 128}, {2, 256}, {2, 512}, {2, 1024}, {4, 1024}};
+    const int V = bf ? 8 : 4, n = 9;
     for (int i = 0; i < n; ++i) {
         const Shape s = bf ? b[i] : f[i];
         if (C <= V * s.NV * s.TPR) return s;
@@ -508,10 +508,10 @@ hipError_t by_shape(bool bf, int C, F f) {
         return hipGetLastError();                                                                                     \
     }
     if (bf) {
-        GDR_SHAPE(bf16, 8, 1, 16) GDR_SHAPE(bf16, 8, 1, 64) GDR_SHAPE(bf16, 8, 1, 128) GDR_SHAPE(bf16, 8, 1, 256)
-        GDR_SHAPE(bf16, 8, 1, 512) GDR_SHAPE(bf16, 8, 1, 1024) GDR_SHAPE(bf16, 8, 2, 1024)
+        GDR_SHAPE(bf16, 8, 1, 8) GDR_SHAPE(bf16, 8, 1, 16) GDR_SHAPE(bf16, 8, 1, 32) GDR_SHAPE(bf16, 8, 1, 64)
+        GDR_SHAPE(bf16, 8, 1, 128) GDR_SHAPE(bf16, 8, 1, 256) GDR_SHAPE(bf16, 8, 1, 512) GDR_SHAPE(bf16, 8, 1, 1024) GDR_SHAPE(bf16, 8, 2, 1024)
     } else {
-        GDR_SHAPE(float, 4, 1, 16) GDR_SHAPE(float, 4, 2, 16) GDR_SHAPE(float, 4, 1, 64) GDR_SHAPE(float, 4, 2, 64)
+        GDR_SHAPE(float, 4, 1, 16) GDR_SHAPE(float, 4, 2, 16) GDR_SHAPE(float, 4, 2, 32) GDR_SHAPE(float, 4, 2, 64)
         GDR_SHAPE(float, 4, 2, 128) GDR_SHAPE(float, 4, 2, 256) GDR_SHAPE(float, 4, 2, 512) GDR_SHAPE(float, 4, 2, 1024)
         GDR_SHAPE(float, 4, 4, 1024)
     }
@@ -523,11 +523,14 @@ int64_t row_blocks(int64_t rows, int TPR) {
     const int rpb = TPR < 256 ? 256 / TPR : 1;
     return (rows + rpb - 1) / rpb;
 }
-// Workgroups that the rows go round. With fewer a workgroup's next row is on its way while
-// it works, with more the card has more rows in flight: rows of 1,024 (bf16) took 132 us in
-// 512 workgroups, 111 in 8,192, and 111 in 16,384; rows of 4,096 102, 115 and 124.
-unsigned fwd_blocks(int64_t rows, int TPR) {
-    const int64_t n = row_blocks(rows, TPR), most = TPR < 256 ? 8192 : 1024;
+// Workgroups that the rows go round, forward. With one parameter a workgroup for the rows
+// that it takes at a time: 2,097,152 gated rows of 128 took 276 us so and 310 in 8,192
+// workgroups; sums onto a stream in fp32, 256 MB of rows of 512, 312 and 386. With more of
+// them a workgroup that reads them all for one row pays: with both norms and a gate per
+// channel 256 MB of rows of 512 took 242 us so, 197 in 8,192 workgroups, 212 in 2,048; rows
+// of 4,096 245, 206 and 196, and 64 MB of these 61, 60, 52 and in 1,024 49.
+unsigned fwd_blocks(int64_t rows, int TPR, bool one) {
+    const int64_t n = row_blocks(rows, TPR), most = one ? (int64_t)1 << 21 : TPR < 256 ? 8192 : 1024;
     return (unsigned)(n < most ? n : most);
 }
 // Backward, each workgroup leaves its sums for the parameters: rows of 1,024 took 274 us in
@@ -557,7 +560,7 @@ hipError_t launch_gated_norm_fwd(const GatedNormArgs& a) {
     if (a.p.rows == 0) return hipSuccess;
     const bool once = beyond_caches(a.p.rows * a.p.cols * (2 * size_of(a.p.io_dtype) + size_of(a.p.out_dtype)));
     return by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
-        GDR_LAUNCH(k_gated_norm_fwd, fwd_blocks(a.p.rows, TPR), once, a);
+        GDR_LAUNCH(k_gated_norm_fwd, fwd_blocks(a.p.rows, TPR, true), once, a);
     });
 }
 
@@ -577,10 +580,11 @@ hipError_t launch_gated_norm_bwd(const GatedNormArgs& a) {
 hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a) {
     if (a.p.rows == 0) return hipSuccess;
     const int token = a.p.gate == GDR_GATE_TOKEN;
+    const bool one = !a.x_weight && a.p.gate != GDR_GATE_CHANNEL;
     const bool once = beyond_caches(a.p.rows * a.p.cols * ((1 + token) * size_of(a.p.io_dtype) + size_of(a.p.out_dtype) +
                                                            2 * size_of(a.p.stream_dtype)));
     return by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, [&](auto type, auto vec, auto nv, auto tpr) {
-        GDR_LAUNCH(k_residual_norm_fwd, fwd_blocks(a.p.rows, TPR), once, a);
+        GDR_LAUNCH(k_residual_norm_fwd, fwd_blocks(a.p.rows, TPR, one), once, a);
     });
 }
 
