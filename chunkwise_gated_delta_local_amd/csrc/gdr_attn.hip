@@ -681,6 +681,17 @@ __global__ __launch_bounds__(256) void k_window_keep(AttnArgs a) {
 
 // ---------------------------------------------------------------- launches
 // Many rows: 32 a wavefront; few rows: 32 a workgroup, whose wavefronts share the keys.
+// Four wavefronts a workgroup for many rows: eight read the keys half as often, but leave
+// compute units idle (65,536 tokens of 32 heads the same, 65,536 of 16 heads of 64 over a window of
+// 1,024 823 us with four and 1,023 with eight, 8,191 packed ones 55 and 65).
+// Shared keys against many rows, 6 heads over 2, us, by blocks of 32 rows:
+//   bf16, 128 x 128, window 512     137: 16 23   273: 25 23   546: 42 24   820: 58 24
+//                    window 2,048   137: 16 22   273: 31 35   546: 61 54   820: 91 55
+//   fp32, 128 x 128, window 512     137: 43 93   273: 58 94   546: 105 95  820: 152 97   1,093: 196 166
+//                    window 2,048   273: 81 192  546: 194 306 820: 307 309 1,093: 414 542 1,639: 637 544
+//   fp32, 64 x 64, window 512       273: 31 54   546: 48 55   820: 67 55   1,093: 82 89  1,639: 116 91
+// In bf16 a compute unit's share of 256 blocks decides, in fp32 sharing pays up to 512 blocks,
+// and beyond while n / 256 rounds of tiles / 4 + 5 are less than n / 1,024 rounds of tiles + 2.
 constexpr int kRowWaves = 4;
 template <typename T> constexpr int kSplitWaves = sizeof(T) == 2 ? 8 : 4;
 struct Plan {
@@ -701,6 +712,11 @@ Plan plan_of(const gdr_attn_problem_t& p) {
     blocks(32);
     x.splits = 1;
     x.split = x.nwork <= (bf ? 256 : 512);
+    if (!bf && !x.split && x.nwork < 4096) {
+        const int64_t all = (int64_t)p.sinks + p.window, len = p.seq_len / (packed && p.num_seqs > 0 ? p.num_seqs : 1);
+        const int64_t tiles = ((all < len ? all : len) + 31) / 32;
+        x.split = x.nwork * (tiles + 20) < 1024 * ((x.nwork + 1023) / 1024) * (tiles + 2);
+    }
     if (x.split) {
         // workgroups share the keys too where a wavefront had 16 tiles of them and more
         const int64_t tiles = ((int64_t)p.sinks + p.window + 31) / 32, each = tiles / (bf ? 8 : 4) / 16;

@@ -74,6 +74,12 @@ def test_problems(lib, op, kw, code):
     assert lib.gdr_last_error_message()
 
 
+def test_a_size_for_no_sequences(lib):
+    """Tokens of no sequence are refused by the calls; the sizes are asked for before."""
+    for op in ("fwd", "bwd"):
+        assert size(lib, op, attn(io_dtype=0, out_dtype=0, do_dtype=0, batch=1, num_seqs=0, seq_len=100000))[0] == 0
+
+
 def test_strides_of_prompts_and_steps(lib):
     """The tiles of prompts address a few tokens in 32 bits, single tokens are addressed in 64."""
     wide = attn(q_stride=1 << 30, k_stride=1 << 30, v_stride=1 << 30)

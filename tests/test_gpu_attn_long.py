@@ -18,6 +18,7 @@ FWD = {
     "most_parts_empty_f32": dict(dtype="f32", lens=[33], past=None, Nq=1, Nk=1, dk=64, dv=64, window=1 << 30, sinks=9),
     "sinks_shared": dict(dtype="bf16", lens=[40], past=[9000], Nq=2, Nk=1, dk=64, dv=32, window=16, sinks=8500),
     "ring_turned": dict(dtype="bf16", lens=[31, 31], past=[8191, 8250], Nq=2, Nk=1, dk=64, dv=64, window=8192, sinks=1, batch=True),
+    "many_rows_f32": dict(dtype="f32", lens=[3001], past=None, Nq=6, Nk=2, dk=64, dv=64, window=2000, sinks=2),
     "odd": dict(dtype="bf16", lens=[9], past=[8300], Nq=3, Nk=1, dk=21, dv=11, window=8200, sinks=5, pad=3),
 }
 
