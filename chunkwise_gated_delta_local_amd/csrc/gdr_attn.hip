@@ -298,8 +298,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_spli
     const lds_c mine_v = lds_of(&Vs[0][0]) + w * 32 * DV * (int)sizeof(T);
     // this wavefront's share of the keys, in tiles
     const int all = keys.total(), parts = splits * NW, part = sp * NW + w;
-    const int share = ((all + parts - 1) / parts + 31) / 32 * 32;
-    int64_t first = (int64_t)share * part;
+    const int64_t share = (((int64_t)all + parts - 1) / parts + 31) / 32 * 32, first = share * part;
     int left = first >= all ? 0 : (int)(all - first < share ? all - first : share);
     if (left > 0) keys.skip((int)first);
     if (left > 0) {
@@ -481,7 +480,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_step(AttnArgs a, int spli
     typename Vec<T>::v8 qf[KS];
 #pragma unroll
     for (int t = 0; t < KS; ++t) qf[t] = load8<T, VEC, false>(qn, 32 * t + 8 * qd, dk);
-    const int p = __builtin_amdgcn_readfirstlane(a.lens[n]);
+    const int len = __builtin_amdgcn_readfirstlane(a.lens[n]), p = len < kMostLen ? len : kMostLen;
     const bool idle = p < 0;
     const int64_t cap = (int64_t)S + W;
     const int rows = (int64_t)p + 1 < cap ? p + 1 : (int)cap, own = p < S ? p : S + (p - S) % W;
@@ -570,7 +569,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_step(AttnArgs a, int spli
             m = mn;
             mc = mcn;
         }
-        // as in absorb
+        // as in weigh
         const float m0 = m == kNegInf ? 0.f : m, mc0 = m == kNegInf ? 0.f : mc;
         const bool far = __any(fabsf(mc0) > 16777216.f);
 #pragma unroll

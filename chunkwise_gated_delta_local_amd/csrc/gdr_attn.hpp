@@ -500,9 +500,11 @@ __device__ __forceinline__ Query query_of(const Block& b, const RowBlock& rb, in
     q.p = len + b.t0 + tc;
     return q;
 }
+// A single token's position at most; positions and a tile of keys behind them fit 31 bits
+constexpr int kMostLen = 0x7fffffff - 65;
 __device__ __forceinline__ int past_len(const AttnArgs& a, int n) {
     if (!a.lens) return 0;
-    const int len = __builtin_amdgcn_readfirstlane(a.lens[n]), most = 0x7fffffff - 64 - (int)a.p.seq_len;
+    const int len = __builtin_amdgcn_readfirstlane(a.lens[n]), most = kMostLen + 1 - (int)a.p.seq_len;
     return len < 0 ? 0 : len < most ? len : most;
 }
 

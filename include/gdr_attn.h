@@ -24,7 +24,7 @@
  * lies in row t if t < sinks, else in row sinks + (t - sinks) % window. lens
  * [num_seqs] (device, int32) are the tokens of each sequence before the call;
  * they are read only, so that the layers of a stack can share them, and the
- * caller advances them. lens + seq_len has to stay below 2^31; a value out of
+ * caller advances them. lens + seq_len has to stay below 2^31 - 64; a value out of
  * range gives unspecified results, but every access stays in its buffer. Rows of a
  * cache that hold no visible token are never read into a result: they may hold
  * anything, NaN among it.

@@ -111,3 +111,33 @@ def test_shared_rows_in_two_graphs_and_on_two_streams():
         for (_, _, want), got in zip(todo, outs):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), turn
         randn(torch.Generator().manual_seed(turn), 100).cuda().sum()
+
+
+def test_lens_out_of_range_stay_in_their_buffers():
+    """Results are unspecified, but nothing beside the caches is written and the call returns."""
+    W, S, N = 20, 3, 2
+    for lens in (2 ** 31 - 1, 2 ** 31 - 70):
+        gen = torch.Generator().manual_seed(1)
+        whole = [torch.full((N + 2, S + W, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        cache = tuple(x[1:-1] for x in whole)
+        past = torch.full((N,), lens, dtype=torch.int32, device="cuda")
+        new = lambda *s: randn(gen, *s, dtype=torch.bfloat16).cuda()
+        gdr.window_attn_step(new(N, 4, 64), new(N, 2, 64), new(N, 2, 64), cache, past, W, S)
+        gdr.window_attn_fwd(new(N, 40, 4, 64), new(N, 40, 2, 64), new(N, 40, 2, 64), W, S, cache=cache, lens=past)
+        for x in whole:
+            assert (x[0] == 7).all() and (x[-1] == 7).all()
+
+
+def test_caches_of_two_billion_tokens():
+    """A window of 2^31 - 66 tokens of one element: one key far above the others, at the end of the cache, gives its value."""
+    W, past, at = 2 ** 31 - 66, 2 ** 31 - 80, 2 ** 31 - 83
+    cache = tuple(torch.zeros(1, W, 1, 1, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache[0][0, at], cache[1][0, at] = 100.0, 5.0
+    lens = torch.tensor([past], dtype=torch.int32, device="cuda")
+    one = torch.ones(1, 1, 1, dtype=torch.bfloat16, device="cuda")
+    assert float(gdr.window_attn_step(one, 0 * one, 2 * one, cache, lens, W, scale=1.0)) == 5.0
+    assert float(cache[1][0, past]) == 2.0 and float(cache[1][0, past - 1]) == 0.0
+    o, lse = gdr.window_attn_fwd(*(x * torch.ones(1, 3, 1, 1, dtype=torch.bfloat16, device="cuda") for x in (1, 0, 2)), W,
+                                 scale=1.0, cache=cache, lens=lens)
+    assert (o == 5).all() and ((lse - 100).abs() < 1e-4).all()
+    assert (cache[1][0, past:past + 3] == 2).all()
