@@ -187,11 +187,16 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, const Query& q, co
 // A workgroup of NW wavefronts takes 32 NW rows (tokens times heads of one key head)
 // and walks the keys they see in tiles of KT, keys and values in LDS, two tiles in
 // turn; the next tile's loads are under way during a tile's products.
-template <typename T> constexpr int kTileKeys = sizeof(T) == 2 ? 64 : 32;
-
-template <typename T, int DK, int DV, int NW, bool VEC>
+//
+// The matrix cores and the vector operations bound it, a wavefront's one against the
+// other's: 65,536 tokens of 32 heads over 8, 128 x 128, window 4,096, take 4.2 ms, 1,010
+// TFLOP/s of what is seen, 80 % of a large library product's rate here, with the matrix cores
+// busy 54 % of the cycles and 7.6 vector operations to a product of 32 cycles, of which
+// the exponentials take four times as long. With dims of 64 a product does half for the
+// same exponentials: 65,536 tokens of 16 heads, window 2,048, 708 us, 760 TFLOP/s.
+template <typename T, int DK, int DV, int NW, int KT, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_rows(AttnArgs a, RowBlock rb, int nblk, int nwork) {
-    constexpr int KT = kTileKeys<T>, NT = KT / 32, KF = DK / (2 * kUnit<T>);
+    constexpr int NT = KT / 32, KF = DK / (2 * kUnit<T>);
     __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK], Vs[2][KT * DV];
     // the finite values of a tile at an edge: all wavefronts that need them write the same
     __shared__ __attribute__((aligned(16))) T Clean[KT * DV];
@@ -792,8 +797,23 @@ hipError_t launch_attn_fwd(const AttnArgs& a) {
             }
         } else {
             const dim3 grid((unsigned)((x.nwork + 7) / 8 * 8));
-            if (a.vec) k_window_rows<T, DK, DV, NR, true><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
-            else k_window_rows<T, DK, DV, NR, false><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            auto go = [&](auto tile) {
+                constexpr int KT = decltype(tile)::value;
+                if (a.vec)
+                    k_window_rows<T, DK, DV, NR, KT, true><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+                else
+                    k_window_rows<T, DK, DV, NR, KT, false><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
+            };
+            // Keys of a tile, bf16, 16 heads over 4, us with 32 and 64: dims of 64, 8,191 tokens, window 512: 40
+            // 48; 65,536, 256: 185 220; 65,536, 2,048: 708 715. Dims of 128, 65,536, 256: 311 356; 32,768, 1,024:
+            // 352 366; 8,191, 512: 68 65; 8,191, 2,048: 179 147; 65,536 of 32 heads, 4,096: 4,419 4,175. Tiles of
+            // 64 meet in barriers half as often, tiles of 32 leave less at a window's edges.
+            if constexpr (sizeof(T) == 2 && DK + DV > 128) {
+                if ((int64_t)a.p.sinks + a.p.window >= 2048) go(std::integral_constant<int, 64>{});
+                else go(std::integral_constant<int, 32>{});
+            } else {
+                go(std::integral_constant<int, 32>{});
+            }
         }
         e = hipGetLastError();
         if (e == hipSuccess && a.kc) {

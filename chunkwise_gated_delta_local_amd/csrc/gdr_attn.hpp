@@ -41,7 +41,7 @@ struct AttnArgs {
     void* d_o16;               // d_o rounded to the io type, where it comes in fp32
     int32_t* slots;            // [num_seqs + 1]: first slot of each sequence
     float* sink_part;          // [slots][sinks][Nk][dk + dv]
-    int32_t max_slots, sink_run;
+    int32_t max_slots;
     hipStream_t stream;
 };
 

@@ -8,7 +8,7 @@
 // owns in registers, so that no sum crosses workgroups and its order is fixed. The
 // first also forms delta and leaves it for the second.
 // The first tokens alone are seen by queries of the whole sequence: those behind
-// the ones that a key block meets anyway are shared out in runs of sink_run tokens,
+// the ones that a key block meets anyway are shared out in runs of tokens,
 // whose sums go to slots in memory and are added up by k_window_sinks.
 #include "gdr_attn.hpp"
 
@@ -16,8 +16,14 @@ namespace gdr {
 
 namespace {
 
+// Tokens of a run: 64 runs to a sequence, but not too short and not too long ones. By the
+// sequence's own length, so that its gradients do not depend on what it is packed with.
+__host__ __device__ inline int64_t sink_run(int64_t len) {
+    const int64_t n = len / 64;
+    return n < 256 ? 256 : n < 4096 ? n : 4096;
+}
 // First slot of each sequence, by one wavefront: a slot for the own sums of the key blocks
-// with sinks, and one for each run of sink_run tokens behind a window.
+// with sinks, and one for each run of tokens behind a window.
 __device__ void count_slots(const AttnArgs& a) {
     const int lane = threadIdx.x & 63;
     int base = 0;
@@ -27,8 +33,8 @@ __device__ void count_slots(const AttnArgs& a) {
         if (n < a.p.num_seqs) {
             int64_t s, e;
             seq_range(a.cu, n, a.p.seq_len, a.Ttot, &s, &e);
-            const int64_t behind = e - s - a.p.window;
-            if (behind > 0) m = (int)((behind + a.sink_run - 1) / a.sink_run) + 1;
+            const int64_t behind = e - s - a.p.window, run = sink_run(e - s);
+            if (behind > 0) m = (int)((behind + run - 1) / run) + 1;
         }
         int sum = m;
 #pragma unroll
@@ -60,7 +66,7 @@ __global__ __launch_bounds__(256) void k_window_round(const float* from, T* to, 
 // ---------------------------------------------------------------- dq
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = KT / 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
+    constexpr int KT = 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
     __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK], Vs[2][KT * DV];
     const lds_c K0 = lds_of(Ks[0]), K1 = lds_of(Ks[1]), V0 = lds_of(Vs[0]), V1 = lds_of(Vs[1]);
     if (blockIdx.x == 0 && threadIdx.x < 64 && a.slots) count_slots(a);
@@ -134,33 +140,30 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
         if (pos0 <= pb && (pos0 < S || pos0 + n - 1 > pa - W)) {
             const bool partial = n < KT || pos0 + KT - 1 > pa || (pos0 <= pb - W && pos0 + KT > S);
             const Sight sees{pos0, n, q.p, W, S};
+            f32x16 s = zero16(), g = zero16();
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                f32x16 s = zero16(), g = zero16();
-                __builtin_amdgcn_s_setprio(1);
+            for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 0, t, ro), qf[t], s);
+            feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
 #pragma unroll
-                for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K, 32 * k, t, ro), qf[t], s);
-                feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
+            for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 0, t, rv), gf[t], g);
+            feed<VF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
+            __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-                for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 32 * k, t, rv), gf[t], g);
-                feed<VF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
-                __builtin_amdgcn_s_setprio(0);
+            for (int i = 0; i < 16; ++i)
+                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
+            if (partial) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
-                if (partial) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = sees(32 * k + 8 * (i >> 2) + 4 * h + (i & 3)) ? s[i] : 0.f;
-                }
-                __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const auto x = acc_frag<T>(s, e);
-#pragma unroll
-                    for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<T, DK>(K, 32 * k + 16 * e, t, co), x, acc[t]);
-                }
-                __builtin_amdgcn_s_setprio(0);
+                for (int i = 0; i < 16; ++i) s[i] = sees(8 * (i >> 2) + 4 * h + (i & 3)) ? s[i] : 0.f;
             }
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto x = acc_frag<T>(s, e);
+#pragma unroll
+                for (int t = 0; t < DK / 32; ++t) acc[t] = mma(col_frag<T, DK>(K, 16 * e, t, co), x, acc[t]);
+            }
+            __builtin_amdgcn_s_setprio(0);
         }
         land(Kn, Vn);
     };
@@ -244,8 +247,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
         keys = b.len - b.t0 < keys ? b.len - b.t0 : keys;
         // the key block's own run ends where its last key's window does
         const int own = (b.len - b.t0 < KB ? b.len - b.t0 : KB);
-        const int64_t from = (int64_t)b.t0 + own - 1 + W, first = W + (int64_t)(run - 1) * a.sink_run;
-        int64_t x = first > from ? first : from, y = first + a.sink_run;
+        const int64_t from = (int64_t)b.t0 + own - 1 + W, each = sink_run(b.len), first = W + (run - 1) * each;
+        int64_t x = first > from ? first : from, y = first + each;
         // the last run takes what is left; all runs begin behind the first window
         x = x < b.len ? x : b.len;
         y = y < b.len ? y : b.len;
@@ -458,7 +461,6 @@ __global__ __launch_bounds__(256) void k_window_sinks(AttnArgs a) {
 }
 
 struct Plan {
-    int run;                   // queries of a slot
     int64_t slots;
     size_t rows, d_o16, table, part;   // bytes
 };
@@ -470,11 +472,11 @@ Plan plan_of(const gdr_attn_problem_t& p) {
     const int64_t T = p.batch * p.seq_len, W = p.window;
     x.rows = up((size_t)T * p.num_q_heads * 8);
     if (p.do_dtype != p.io_dtype) x.d_o16 = up((size_t)T * p.num_q_heads * p.head_dim_v * size_of(p.io_dtype));
-    const int64_t run = p.seq_len / 64;
-    x.run = (int)(run < 256 ? 256 : run < 4096 ? run : 4096);
     if (p.sinks > 0 && T > W) {
-        const int64_t longer = T / (W + 1);                        // sequences that can be longer than a window
-        x.slots = T / x.run + 2 * (longer < p.num_seqs ? longer : p.num_seqs) + 1;
+        const int64_t most = T / (W + 1), longer = most < p.num_seqs ? most : p.num_seqs;    // than a window
+        // runs of 256 tokens at least, and up to 65 to a sequence or runs of 4,096
+        const int64_t runs = T / 256 < 65 * longer + T / 4096 ? T / 256 : 65 * longer + T / 4096;
+        x.slots = runs + 2 * longer + 1;
         x.table = up(((size_t)p.num_seqs + 1) * 4);
         const double rows = (double)x.slots * sinks_of(p) * p.num_kv_heads;      // more than a launch takes: any number
         x.part = up((rows < 0x1p40 ? (size_t)rows : (size_t)1 << 40) * (p.head_dim_qk + p.head_dim_v) * 4);
@@ -500,7 +502,6 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
     a.slots = x.slots ? reinterpret_cast<int32_t*>(ws + x.rows + x.d_o16) : nullptr;
     a.sink_part = x.slots ? reinterpret_cast<float*>(ws + x.rows + x.d_o16 + x.table) : nullptr;
     a.max_slots = (int32_t)x.slots;
-    a.sink_run = x.run;
     const int G = group(a.p), Nk = a.p.num_kv_heads;
     const bool packed = a.cu != nullptr;
     hipError_t e = hipSuccess;
