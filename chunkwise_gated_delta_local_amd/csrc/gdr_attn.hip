@@ -814,12 +814,17 @@ hipError_t launch_attn_fwd(const AttnArgs& a) {
                 else
                     k_window_rows<T, DK, DV, NR, KT, false><<<grid, 64 * NR, 0, a.stream>>>(a, x.rb, (int)x.nblk, (int)x.nwork);
             };
-            // Keys of a tile, bf16, 16 heads over 4, us with 32 and 64: dims of 64, 8,191 tokens, window 512: 40
-            // 48; 65,536, 256: 185 220; 65,536, 2,048: 708 715. Dims of 128, 65,536, 256: 311 356; 32,768, 1,024:
-            // 352 366; 8,191, 512: 68 65; 8,191, 2,048: 179 147; 65,536 of 32 heads, 4,096: 4,419 4,175. Tiles of
-            // 64 meet in barriers half as often, tiles of 32 leave less at a window's edges.
+            // Keys of a tile, bf16, 16 heads over 4, us with 32 and 64. Dims of 64: 8,191 tokens, window 512:
+            // 40 48; 65,536, 256: 185 220; 65,536, 2,048: 708 715. Dims of 128 by windows of
+            //   65,536 tokens   256: 302 360   1,024: 703 749   2,048: 1,244 1,248   4,096: 2,262 2,197
+            //   16,384          512: 108 118   1,024: 172 175   2,048: 303 294       4,096: 547 516
+            //   8,191           512: 68 63     1,024: 103 89    2,048: 176 144       4,096: 316 247
+            // Tiles of 32 leave less at a window's edges, and registers for three wavefronts a SIMD in
+            // place of two, of which up to 1,024 workgroups fill a second round to a third; tiles of 64
+            // meet in barriers half as often. v of 64 dims, 65,536 tokens, 4,096: 1,789 1,827; 8,191, 2,048: 134 121.
             if constexpr (sizeof(T) == 2 && DK + DV > 128) {
-                if ((int64_t)a.p.sinks + a.p.window >= 2048) go(std::integral_constant<int, 64>{});
+                const int64_t sight = (int64_t)a.p.sinks + a.p.window;
+                if ((x.nwork <= 1024 && sight >= 1024) || (DK + DV == 256 && sight >= 2048)) go(std::integral_constant<int, 64>{});
                 else go(std::integral_constant<int, 32>{});
             } else {
                 go(std::integral_constant<int, 32>{});
