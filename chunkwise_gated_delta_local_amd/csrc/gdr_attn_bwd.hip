@@ -206,8 +206,8 @@ constexpr int kQueryTile = 32;
 // `main` on are the runs of queries that see sinks alone.
 // LDS and the matrix cores bound it alike: a tile's 32 rows of q and d_o are read twice each
 // and v once, 42 KB to 32 products of 32 cycles for each of eight wavefronts. The loads
-// are covered: with key blocks in an order in which an XCD's cache serves them (155 MB from
-// beyond it in place of 613) the time was the same.
+// are covered: with tiles in an order in which an XCD's cache serves them (a quarter of the
+// bytes from beyond it) the time was the same.
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(AttnArgs a, RowBlock rb, int nblk,
                                                                                 int main, int nwork) {
