@@ -42,6 +42,7 @@ __device__ __forceinline__ void store_piece(T* row, int c, int C, const float (&
 // V elements of a tensor that is fp32 or T, as they were read: the choice is the same
 // for a whole launch, and the values are not looked at before they are unpacked, so
 // that the loads of several tensors are on their way together.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 template <int V> struct AnyPiece {
     f32x4 x[V / 4];
 };
@@ -55,7 +56,10 @@ __device__ __forceinline__ void load_any(AnyPiece<V>& r, const void* p, int64_t 
             else r.x[i / 4] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     } else if constexpr (sizeof(T) == 2) {
-        r.x[0] = __builtin_bit_cast(f32x4, load_piece<T, V, ONCE>((const T*)p + row, c, C));
+        typedef typename Raw<T, V>::type raw;
+        const raw x = load_piece<T, V, ONCE>((const T*)p + row, c, C);
+        if constexpr (sizeof(raw) == 16) r.x[0] = __builtin_bit_cast(f32x4, x);
+        else r.x[0] = __builtin_shufflevector(__builtin_bit_cast(f32x2, x), f32x2{}, 0, 1, 2, 3);
     }
 }
 template <typename T, int V>
@@ -64,7 +68,9 @@ __device__ __forceinline__ void unpack_any(const AnyPiece<V>& r, int f32, float 
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = r.x[i / 4][i % 4];
     } else if constexpr (sizeof(T) == 2) {
-        unpack<T, V>(__builtin_bit_cast(typename Raw<T, V>::type, r.x[0]), f);
+        typedef typename Raw<T, V>::type raw;
+        if constexpr (sizeof(raw) == 16) unpack<T, V>(__builtin_bit_cast(raw, r.x[0]), f);
+        else unpack<T, V>(__builtin_bit_cast(raw, __builtin_shufflevector(r.x[0], r.x[0], 0, 1)), f);
     }
 }
 template <typename T, int V, bool ONCE = false>
