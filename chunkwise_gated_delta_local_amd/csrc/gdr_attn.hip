@@ -81,7 +81,8 @@ __device__ __forceinline__ uint32_t copy_finite(lds_c from, lds_c to) {
 // Weights are exp2(c s - mc). m follows the maximum only when that has grown by more
 // than 8 in the exponent: weights then stay below 2^9 and the sums, in fp32, hardly
 // notice, while most tiles are spared the product of o with the change. Beyond 2^24 the
-// rounding of mc reaches the exponent's units, and the difference is formed first.
+// rounding of mc reaches the exponent's units, and the difference is formed first. Both are
+// a query's own choice: what the others of its wavefront score does not change its bits.
 template <int DV, int NT>
 __device__ __forceinline__ void weigh(State<DV>& st, f32x16 (&s)[NT], float c, bool partial, const Sight& sees) {
     const int h = (threadIdx.x >> 5) & 1;
@@ -99,8 +100,9 @@ __device__ __forceinline__ void weigh(State<DV>& st, f32x16 (&s)[NT], float c, b
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, s[k][i]);
     top = pair_max(top);
-    if (__any((top - st.m) * c > 8.f)) {
-        const float m = fmaxf(st.m, top), mc = m * c, f = refer(st.mc, mc);
+    const bool grown = (top - st.m) * c > 8.f;
+    if (__any(grown)) {
+        const float m = grown ? top : st.m, mc = grown ? m * c : st.mc, f = grown ? refer(st.mc, mc) : 1.f;
         st.l *= f;
 #pragma unroll
         for (int t = 0; t < DV / 32; ++t) st.o[t] = st.o[t] * f;
@@ -109,14 +111,15 @@ __device__ __forceinline__ void weigh(State<DV>& st, f32x16 (&s)[NT], float c, b
         arrived(st.o);
     }
     float mc = st.m == kNegInf ? 0.f : st.mc;
-    if (__any(fabsf(mc) > 16777216.f)) {
+    const bool far = fabsf(mc) > 16777216.f;
+    if (__any(far)) {
         asm volatile("");
-        const float m = st.m == kNegInf ? 0.f : st.m;
+        const float m = far ? st.m : 0.f;
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[k][i] -= m;
-        mc = 0.f;
+        mc = far ? 0.f : mc;
     }
 #pragma unroll
     for (int k = 0; k < NT; ++k)
@@ -573,8 +576,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_step(AttnArgs a, int spli
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = __builtin_elementwise_maximum(top, s[i >> 2][i & 3]);
         top = quad_max(top);
-        if (__any((top - m) * c > 8.f)) {
-            const float mn = fmaxf(m, top), mcn = mn * c, f = refer(mc, mcn);
+        const bool grown = (top - m) * c > 8.f;
+        if (__any(grown)) {
+            const float mn = grown ? top : m, mcn = grown ? mn * c : mc, f = grown ? refer(mc, mcn) : 1.f;
             l *= f;
 #pragma unroll
             for (int t = 0; t < VS; ++t) o[t] = o[t] * f;
@@ -582,12 +586,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_step(AttnArgs a, int spli
             mc = mcn;
         }
         // as in weigh
-        const float m0 = m == kNegInf ? 0.f : m, mc0 = m == kNegInf ? 0.f : mc;
-        const bool far = __any(fabsf(mc0) > 16777216.f);
+        float mc0 = m == kNegInf ? 0.f : mc;
+        const bool far = fabsf(mc0) > 16777216.f;
+        if (__any(far)) {
+            asm volatile("");
+            const float m0 = far ? m : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i >> 2][i & 3] -= m0;
+            mc0 = far ? 0.f : mc0;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = s[i >> 2][i & 3], e = far ? (x - m0) * c : __builtin_fmaf(x, c, -mc0);
-            s[i >> 2][i & 3] = __builtin_amdgcn_exp2f(e);
+            s[i >> 2][i & 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], c, -mc0));
             l += s[i >> 2][i & 3];
         }
         const auto wt = acc_to_pair<T>(s[0], s[1]);
