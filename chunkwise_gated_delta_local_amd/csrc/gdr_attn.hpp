@@ -38,6 +38,7 @@ struct AttnArgs {
     const float* lse_in;
     void *dq, *dk, *dv;
     float* rows;               // [Ttot][Nq][2]: lse log2(e), sum of d_o o
+    float* tops;               // [Ttot][Nq]: the largest score where lse is formed from there, else 0
     void* d_o16;               // d_o rounded to the io type, where it comes in fp32
     int32_t* slots;            // [num_seqs + 1]: first slot of each sequence
     float* sink_part;          // [slots][sinks][Nk][dk + dv]

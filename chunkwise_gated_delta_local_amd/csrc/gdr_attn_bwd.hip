@@ -7,6 +7,14 @@
 // queries, k_window_dkv the queries of a block of keys, each summing what it
 // owns in registers, so that no sum crosses workgroups and its order is fixed. The
 // first also forms delta and leaves it for the second.
+// P is exp2(c s - lse log2(e)) with c = scale log2(e). fp32 holds a large lse coarsely: at
+// 2^24 an ulp of it is a factor in P, and a row of one key would not weigh one. Where
+// |lse log2(e)| is beyond kFarLse, the rounding of lse to fp32 and its few operations (about
+// 4 ulps) would cost P more than 2^-12, as much as a score's own rounding does; k_window_dq
+// then goes over the row's scores first, as the forward pass did, and P is exp2(c (s - top)
+// - log2(sum of exp2(c (s - top)))), in both kernels. A row's own choice, from its lse alone.
+// Where no row is far this costs up to 2 % of the gradients' time (4 x 4,096 tokens of 16 heads, 128 x
+// 128, 486 us without it, 488 with it; rows that are not 16-byte aligned 5 %).
 // The first tokens alone are seen by queries of the whole sequence: those behind
 // the ones that a key block meets anyway are shared out in runs of tokens,
 // whose sums go to slots in memory and are added up by k_window_sinks.
@@ -48,6 +56,12 @@ __device__ void count_slots(const AttnArgs& a) {
     }
 }
 
+constexpr float kFarLse = 1024.f;
+// a row's scores as exponents refer to them: its largest one (0: they do not) is taken off
+__device__ __forceinline__ float below_top(float s, float top) {
+    return top != 0.f ? __builtin_elementwise_minimum(s - top, 0.f) : s;
+}
+
 // A d_o in fp32 in the io type, 4 elements a thread
 template <typename T>
 __global__ __launch_bounds__(256) void k_window_round(const float* from, T* to, int64_t n) {
@@ -75,6 +89,7 @@ template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
     __shared__ __attribute__((aligned(16))) T Ks[2][KT * DK], Vs[2][KT * DV];
+    __shared__ int far_rows[NW];
     const lds_c K0 = lds_of(Ks[0]), K1 = lds_of(Ks[1]), V0 = lds_of(Vs[0]), V1 = lds_of(Vs[1]);
     if (blockIdx.x == 0 && threadIdx.x < 64 && a.slots) count_slots(a);
     const int per = (nwork + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
@@ -94,8 +109,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
 #pragma unroll
     for (int t = 0; t < VF; ++t) gf[t] = load_frag_row<T, VEC>((const T*)a.d_o + row * dv, 2 * t + h, dv, q.live);
     // lse in units of log 2, and delta: here for the lane's query, in memory for k_window_dkv
-    const float lse = a.lse_in[row] * kLog2e, c = a.p.scale * kLog2e;
-    float delta = 0.f;
+    float lse = a.lse_in[row] * kLog2e, top = 0.f, delta = 0.f;
+    const float c = a.p.scale * kLog2e;
+    const bool far = fabsf(lse) > kFarLse;
 #pragma unroll
     for (int t = 0; t < VF; ++t) {
         const int d0 = (2 * t + h) * kUnit<T>;
@@ -112,10 +128,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
         for (int e = 0; e < kUnit<T>; ++e) delta = __builtin_fmaf(q.live ? o[e] : 0.f, to_f(gf[t][e]), delta);
     }
     delta = pair_sum(delta);
-    if (q.live && h == 0) {
-        a.rows[2 * row] = lse;
-        a.rows[2 * row + 1] = delta;
-    }
+    if (lane == 0) far_rows[w] = 0;
+    if (far && q.live) far_rows[w] = 1;
     f32x16 acc[DK / 32];
 #pragma unroll
     for (int t = 0; t < DK / 32; ++t) acc[t] = zero16();
@@ -139,6 +153,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
         }
         landed();
     };
+    int some = 0;                                                  // whether a row of the block is far
     auto turn = [&](lds_c K, lds_c V, lds_c Kn, lds_c Vn) {
         const int pos0 = pos, n = cnt;
         const int ro = fresh(row_offset<T, DK>(lane)), rv = DK == DV ? ro : fresh(row_offset<T, DV>(lane)),
@@ -156,6 +171,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
             for (int t = 0; t < VF; ++t) g = mma(row_frag<T, DV>(V, 0, t, rv), gf[t], g);
             feed<VF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
             __builtin_amdgcn_s_setprio(0);
+            if (some) {
+                asm volatile("");
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = below_top(s[i], top);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (g[i] - delta);
@@ -178,12 +198,58 @@ __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock r
     arrived(qf);
     arrived(gf);
     land(K0, V0);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) some |= far_rows[i];
+    some = __builtin_amdgcn_readfirstlane(some);
+    if (some) {
+        // the largest score and the sum of each row, while the first tile waits in K0 and V0
+        Keys all(b.t0, b.t0 + b.tn - 1, 0, W, S);
+        Copy<T, DK, KT, 64 * NW, VEC> ca;
+        float m = kNegInf, l = 0.f;
+        for (;;) {
+            int p0, n, r0;
+            bool old;
+            all.next(KT, &p0, &n, &r0, &old);
+            if (n == 0) break;
+            const Source<T> x = source<T>(a, b, hk, r0, false);
+            ca.start(K1, x.k, x.kld, n, dk, tid);
+            ca.finish(K1, tid);
+            landed();
+            const Sight sees{p0, n, q.p, W, S};
+            f32x16 s = zero16();
+#pragma unroll
+            for (int t = 0; t < KF; ++t) s = mma(row_frag<T, DK>(K1, 0, t, row_offset<T, DK>(lane)), qf[t], s);
+            float most = m, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = sees(8 * (i >> 2) + 4 * h + (i & 3)) ? s[i] : kNegInf;
+                most = __builtin_elementwise_maximum(most, s[i]);
+            }
+            const float ref = most == kNegInf ? 0.f : most;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += __builtin_amdgcn_exp2f((s[i] - ref) * c);
+            l = __builtin_fmaf(l, __builtin_amdgcn_exp2f((m - ref) * c), sum);
+            m = most;
+            __syncthreads();
+        }
+        const float most = pair_max(m);
+        l = pair_sum(l * (m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - most) * c)));
+        if (far) {
+            top = most;
+            lse = __builtin_amdgcn_logf(l);
+        }
+    }
     while (cnt > 0) {
         turn(K0, V0, K1, V1);
         if (cnt == 0) break;
         turn(K1, V1, K0, V0);
     }
     if (!q.live) return;
+    if (h == 0) {
+        a.rows[2 * row] = lse;
+        a.rows[2 * row + 1] = delta;
+        a.tops[row] = top;
+    }
 #pragma unroll
     for (int t = 0; t < DK / 32; ++t)
 #pragma unroll
@@ -214,7 +280,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
     constexpr int QT = kQueryTile, KB = 32 * NW, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);
     constexpr bool VLDS = sizeof(T) == 2;
     __shared__ __attribute__((aligned(16))) T Vb[VLDS ? KB * DV : 1], Qs[2][QT * DK], Gs[2][QT * DV];
-    __shared__ __attribute__((aligned(16))) float Rs[2][2 * QT];               // lse of the rows, then delta
+    __shared__ __attribute__((aligned(16))) float Rs[2][4 * QT];               // lse of the rows, delta, top, unused
     const lds_c Vk = lds_of(Vb), Q0 = lds_of(Qs[0]), Q1 = lds_of(Qs[1]), G0 = lds_of(Gs[0]), G1 = lds_of(Gs[1]);
     const lds_c R0 = lds_of(Rs[0]), R1 = lds_of(Rs[1]);
     // consecutive key blocks of a head on one XCD; the runs are dealt to all of them
@@ -325,6 +391,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             static_assert(QT == 32, "lse and delta of a tile in 64 lanes");
             copy4_to_lds(raw_rsrc(a.rows + 2 * (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 8), R,
                          r < span ? (x * Nq + g) * 8 + 4 * h : kOutside);
+        } else if (w == 1) {
+            const int r = lane & 31, x = (r * magic) >> 16, g = r - x * rb.HPB;
+            copy4_to_lds(raw_rsrc(a.tops + (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 4), R + 8 * QT,
+                         r < span && h == 0 ? (x * Nq + g) * 4 : kOutside);
         }
         p0 = t;
         p1 = t + n - 1;
@@ -356,10 +426,20 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
             for (int u = 0; u < KF; ++u) s = mma(row_frag<T, DK>(Q, 0, u, rq), kf[u], s);
             feed<KF, 1, sizeof(T) == 2 ? 1 : 4, 4>();
             __builtin_amdgcn_sched_barrier(0);
+            const float tops = *(lds_p<float>)(R + 8 * QT + 4 * (lane & 31));
 #pragma unroll
             for (int u = 0; u < VF; ++u) g = mma(row_frag<T, DV>(Gr, 0, u, rg), v_frag(u, rg), g);
             __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
+            if (__any(tops != 0.f)) {
+                asm volatile("");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 M = *(lds_p<f32x4>)(R + 8 * QT + 32 * i + 16 * h);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[4 * i + j] = below_top(s[4 * i + j], M[j]);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 L = *(lds_p<f32x4>)(R + 32 * i + 16 * h), D = *(lds_p<f32x4>)(R + 4 * QT + 32 * i + 16 * h);
@@ -473,7 +553,7 @@ __global__ __launch_bounds__(256) void k_window_sinks(AttnArgs a) {
 
 struct Plan {
     int64_t slots;
-    size_t rows, d_o16, table, part;   // bytes
+    size_t rows, tops, d_o16, table, part;   // bytes
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // A sequence has no more sinks than tokens
@@ -482,6 +562,7 @@ Plan plan_of(const gdr_attn_problem_t& p) {
     Plan x{};
     const int64_t T = p.batch * p.seq_len, W = p.window;
     x.rows = up((size_t)T * p.num_q_heads * 8);
+    x.tops = up((size_t)T * p.num_q_heads * 4);
     if (p.do_dtype != p.io_dtype) x.d_o16 = up((size_t)T * p.num_q_heads * p.head_dim_v * size_of(p.io_dtype));
     if (p.sinks > 0 && T > W) {
         const int64_t most = T / (W + 1), longer = most < p.num_seqs ? most : p.num_seqs;    // than a window
@@ -499,7 +580,7 @@ Plan plan_of(const gdr_attn_problem_t& p) {
 
 size_t attn_bwd_workspace(const gdr_attn_problem_t& p) {
     const Plan x = plan_of(p);
-    return x.rows + x.d_o16 + x.table + x.part;
+    return x.rows + x.tops + x.d_o16 + x.table + x.part;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& in) {
@@ -509,9 +590,12 @@ hipError_t launch_attn_bwd(const AttnArgs& in) {
     a.p.sinks = sinks_of(a.p);
     char* ws = reinterpret_cast<char*>(a.ws);
     a.rows = reinterpret_cast<float*>(ws);
-    a.d_o16 = x.d_o16 ? ws + x.rows : nullptr;
-    a.slots = x.slots ? reinterpret_cast<int32_t*>(ws + x.rows + x.d_o16) : nullptr;
-    a.sink_part = x.slots ? reinterpret_cast<float*>(ws + x.rows + x.d_o16 + x.table) : nullptr;
+    a.tops = reinterpret_cast<float*>(ws += x.rows);
+    ws += x.tops;
+    a.d_o16 = x.d_o16 ? ws : nullptr;
+    ws += x.d_o16;
+    a.slots = x.slots ? reinterpret_cast<int32_t*>(ws) : nullptr;
+    a.sink_part = x.slots ? reinterpret_cast<float*>(ws + x.table) : nullptr;
     a.max_slots = (int32_t)x.slots;
     const int G = group(a.p), Nk = a.p.num_kv_heads;
     const bool packed = a.cu != nullptr;

@@ -80,7 +80,10 @@ gdr_status_t gdr_window_attn_step(const gdr_attn_problem_t* problem, const void*
                                   size_t workspace_bytes, void* stream);
 
 /* Gradients of gdr_window_attn_fwd from empty caches, for dL/do (d_o, dense) and
- * the forward's o (out_dtype) and lse: dq, dk and dv dense like q, k and v. */
+ * the forward's o (out_dtype) and lse: dq, dk and dv dense like q, k and v. The
+ * weights are exp(s - lse); of rows with |lse| beyond 1,024 ln 2, which fp32 holds
+ * too coarsely for that, they are formed again from the scores. Below, the
+ * rounding of lse leaves a weight within 2^-12 of itself. */
 gdr_status_t gdr_window_attn_bwd_workspace_size(const gdr_attn_problem_t* problem, size_t* bytes);
 gdr_status_t gdr_window_attn_bwd(const gdr_attn_problem_t* problem, const void* q, const void* k, const void* v,
                                  const void* o, const float* lse, const void* d_o, const int32_t* cu_seqlens_dev,
