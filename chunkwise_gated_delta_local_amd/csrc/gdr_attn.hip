@@ -721,7 +721,11 @@ struct Plan {
     RowBlock rb;
     int64_t nblk, nwork;
 };
-Plan plan_of(const gdr_attn_problem_t& p) {
+// behind: there may be cached tokens in front of the call's. A query then sees sinks + window
+// keys, else no more than its sequence has (350 pieces of 64 tokens on caches, fp32, 64 x 64, window
+// 4,096: shared 356 us, not shared 812; a prompt of 512 tokens, 2 heads of 64 in bf16, under a window
+// of 65,536: 9.4 us in a workgroup each and 16.2 in 16, of which 2 have keys).
+Plan plan_of(const gdr_attn_problem_t& p, bool behind) {
     Plan x{};
     const int G = group(p);
     const bool bf = p.io_dtype == GDR_BF16, packed = p.batch == 1 && p.num_seqs != 1;
@@ -730,17 +734,18 @@ Plan plan_of(const gdr_attn_problem_t& p) {
         x.nblk = token_blocks(p.batch, p.seq_len, p.num_seqs, packed, x.rb.TPB);
         x.nwork = x.nblk * p.num_kv_heads * x.rb.HC;
     };
+    const int64_t all = (int64_t)p.sinks + p.window;
+    auto tiles_of = [&](int64_t len) { return ((behind || all < len ? all : len) + 31) / 32; };
     blocks(32);
     x.splits = 1;
     x.split = x.nwork <= (bf ? 256 : 512);
     if (!bf && !x.split && x.nwork < 4096) {
-        const int64_t all = (int64_t)p.sinks + p.window, len = p.seq_len / (packed && p.num_seqs > 0 ? p.num_seqs : 1);
-        const int64_t tiles = ((all < len ? all : len) + 31) / 32;
+        const int64_t tiles = tiles_of(p.seq_len / (packed && p.num_seqs > 0 ? p.num_seqs : 1));
         x.split = x.nwork * (tiles + 20) < 1024 * ((x.nwork + 1023) / 1024) * (tiles + 2);
     }
     if (x.split) {
         // workgroups share the keys too where a wavefront had 16 tiles of them and more
-        const int64_t tiles = ((int64_t)p.sinks + p.window + 31) / 32, each = tiles / (bf ? 8 : 4) / 16;
+        const int64_t each = tiles_of(p.seq_len) / (bf ? 8 : 4) / 16;
         const int64_t want = x.nwork > 0 ? 256 / x.nwork : 1, s = want < each ? want : each;
         x.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
     } else {
@@ -765,9 +770,10 @@ int step_splits(const gdr_attn_problem_t& p) {
 }  // namespace
 
 size_t attn_fwd_workspace(const gdr_attn_problem_t& p) {
-    const Plan x = plan_of(p);
-    if (x.splits <= 1) return 0;
-    return (size_t)x.splits * p.batch * p.seq_len * p.num_q_heads * (p.head_dim_v + 2) * 4;
+    // the size is asked for without the caches: it does for a call with them and for one without
+    const int a = plan_of(p, false).splits, b = plan_of(p, true).splits, splits = a > b ? a : b;
+    if (splits <= 1) return 0;
+    return (size_t)splits * p.batch * p.seq_len * p.num_q_heads * (p.head_dim_v + 2) * 4;
 }
 
 hipError_t launch_attn_step(const AttnArgs& a) {
@@ -800,7 +806,7 @@ size_t attn_step_workspace(const gdr_attn_problem_t& p) {
 
 hipError_t launch_attn_fwd(const AttnArgs& a) {
     if (a.Ttot == 0) return hipSuccess;
-    const Plan x = plan_of(a.p);
+    const Plan x = plan_of(a.p, a.kc && a.lens);
     const int64_t waves = x.split ? (a.p.io_dtype == GDR_BF16 ? kSplitWaves<bf16> : kSplitWaves<float>) : kRowWaves;
     if (x.nwork >= (int64_t)1 << 31 || !grid_fits(x.nwork * x.splits + 8, 64 * (int)waves)) return hipErrorInvalidConfiguration;
     hipError_t e = hipSuccess;
