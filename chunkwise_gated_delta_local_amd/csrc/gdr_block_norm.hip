@@ -1,8 +1,8 @@
 // The RMS norm with a gate and the residual sum with its norms, forward and backward
 // (include/gdr_mixer.h). A few operations an element: HBM bounds them, so a row is
 // read once and stays in registers between its sums and its outputs. TPR threads share
-// a row, each holding NV pieces of V = 16 bytes of the io type; rows go round the
-// grid, and up to 512 threads a row (forward up to 1,024, one piece each) the next row
+// a row, each holding NV pieces of V elements: 16 bytes of the io type, or four elements
+// in bf16 beside a stream in fp32 (in_fours); rows go round the grid, and up to 512 threads a row (forward up to 1,024, one piece each) the next row
 // is on its way while one is worked on, with the parameters in registers. A thread holds
 // one piece where it can: 4,096 rows of 8,192 took the backward pass 276 us with four pieces
 // and 256 threads, 152 with one, 132 with the parameters' sums in LDS. Rows beyond 8,192
@@ -498,10 +498,22 @@ Shape shape_of(bool bf, int C) {
     return {0, 0};
 }
 
-// f(io type, V, NV, TPR). FOURS: bf16 rows beside a stream in fp32 in pieces of four, so that
-// a wavefront's accesses to the stream lie side by side (256 MB of rows of 4,096 with both norms and a gate
-// per channel: 408 us with eight elements a piece, 305 with four; of 2,048 without them 379 and 302;
-// of 200 331 and 362, for pieces that the row's end cuts are more of a row then).
+// Whether bf16 rows beside a stream in fp32 go in pieces of four elements, so that a
+// wavefront's accesses to the stream lie side by side, or of eight. us for 256 MB of x, eight and four:
+//   both norms, gate per channel    56: 386 321    104: 386 426   192: 367 298   264: 422 367   640: 367 302
+//                                   1,024: 407 294   4,096: 404 302   8,192: 403 303   10,000: 567 521
+//   one parameter                   56: 323 274    104: 327 372   120: 322 350   200: 332 360   264: 429 486
+//                                   448: 325 323   640: 378 421   896: 346 327   1,024: 339 297   4,096: 348 308
+//                                   8,192: 390 357   10,000: 1,071 1,264   16,384: 752 821
+// and 4 MB of rows of 100, whose end cuts a piece of eight: 9.1 and 7.9; of others up to 960 eights are 0
+// to 6 % faster there, of 8,200 15 %. Four for wide rows, for ones that fill the threads of their
+// variant or nearly so, for ones that eights cut, and where several parameters are kept.
+bool in_fours(int C, bool one) {
+    if (C > 8192) return false;
+    return C >= 1024 || C % 8 != 0 || C >= 7 * shape_of(true, C).TPR || (!one && C > 128);
+}
+
+// f(io type, V, NV, TPR). FOURS: bf16 rows in pieces of four, up to 8,192 columns
 template <bool FOURS = false, typename F>
 hipError_t by_shape(bool bf, int C, F f) {
     const Shape s = shape_of(bf && !FOURS, C);
@@ -512,9 +524,9 @@ hipError_t by_shape(bool bf, int C, F f) {
     }
 #define GDR_FOURS(T)                                                                                                   \
     GDR_SHAPE(T, 4, 1, 16) GDR_SHAPE(T, 4, 2, 16) GDR_SHAPE(T, 4, 2, 32) GDR_SHAPE(T, 4, 2, 64) GDR_SHAPE(T, 4, 2, 128) \
-    GDR_SHAPE(T, 4, 2, 256) GDR_SHAPE(T, 4, 2, 512) GDR_SHAPE(T, 4, 2, 1024) GDR_SHAPE(T, 4, 4, 1024)
+    GDR_SHAPE(T, 4, 2, 256) GDR_SHAPE(T, 4, 2, 512) GDR_SHAPE(T, 4, 2, 1024)
     if (!bf) {
-        GDR_FOURS(float)
+        GDR_FOURS(float) GDR_SHAPE(float, 4, 4, 1024)
     } else if constexpr (FOURS) {
         GDR_FOURS(bf16)
     } else {
@@ -594,7 +606,8 @@ hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a) {
     auto go = [&](auto type, auto vec, auto nv, auto tpr) {
         GDR_LAUNCH(k_residual_norm_fwd, fwd_blocks(a.p.rows, TPR, one), once, a);
     };
-    if (a.p.io_dtype == GDR_BF16 && a.p.stream_dtype == GDR_F32) return by_shape<true>(true, a.p.cols, go);
+    if (a.p.io_dtype == GDR_BF16 && a.p.stream_dtype == GDR_F32 && in_fours(a.p.cols, one))
+        return by_shape<true>(true, a.p.cols, go);
     return by_shape(a.p.io_dtype == GDR_BF16, a.p.cols, go);
 }
 

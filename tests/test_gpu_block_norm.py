@@ -138,6 +138,13 @@ def test_residual_norm(R, C, dtype, stream, param, post, kind):
         assert ("dgate" in g) == (kind != "none") and ("dx_weight" in g) == post
 
 
+@pytest.mark.parametrize("post,kind", [(False, "none"), (False, "token"), (True, "none"), (True, "channel")])
+@pytest.mark.parametrize("C", [8, 24, 56, 60, 72, 100, 112, 120, 136, 224, 232, 264, 448, 456, 520, 768, 896, 904, 1023, 1024, 12000])
+def test_widths_beside_a_stream_in_fp32(C, post, kind):
+    """Rows that are moved in pieces of four and of eight elements."""
+    test_residual_norm(21, C, "bf16", "f32", "bf16", post, kind)
+
+
 def test_axes_and_vectors():
     """Any number of leading axes; x of one axis is one row, with a gate in another dtype than its own a channel's."""
     gen = torch.Generator().manual_seed(3)
