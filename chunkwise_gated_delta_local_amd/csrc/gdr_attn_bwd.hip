@@ -14,7 +14,7 @@
 // then goes over the row's scores first, as the forward pass did, and P is exp2(c (s - top)
 // - log2(sum of exp2(c (s - top)))), in both kernels. A row's own choice, from its lse alone.
 // Where no row is far this costs up to 2 % of the gradients' time (4 x 4,096 tokens of 16 heads, 128 x
-// 128, 486 us without it, 488 with it; rows that are not 16-byte aligned 5 %).
+// 128, 486 us without it, 488 with it; rows that are not 16-byte aligned 5 %), where all are 34 %.
 // The first tokens alone are seen by queries of the whole sequence: those behind
 // the ones that a key block meets anyway are shared out in runs of tokens,
 // whose sums go to slots in memory and are added up by k_window_sinks.
@@ -82,9 +82,10 @@ __global__ __launch_bounds__(256) void k_window_round(const float* from, T* to, 
 // turn. A lane owns a query, so that lse and delta are its own registers. Of the five products
 // that gradients need at least, seven are formed in the two kernels (s and dP twice), with no
 // sums across workgroups for it. 4 x 4,096 tokens of 16 heads over 4, 128 x 128, window 1,024:
-// 235 us here and 296 in k_window_dkv, 600 TFLOP/s of the five; matrix cores busy 45 % of
-// the cycles in both. 128 rows a workgroup against 256: 240 us and 256, packed prompts of
-// 353 tokens 24 and 29. Tiles of 64 keys: 240.
+// 231 us here and 293 in k_window_dkv, 600 TFLOP/s of the five; matrix cores busy 42 and 46 % of
+// the cycles. fp32, 2 x 2,048 tokens of them: 1,538 us in all, 42 TFLOP/s; 64 x 64 819 us. 128
+// rows a workgroup against 256: 240 us and 256, packed prompts of 353 tokens 24 and 29. Tiles of
+// 64 keys: 240.
 template <typename T, int DK, int DV, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_window_dq(AttnArgs a, RowBlock rb, int nblk, int nwork) {
     constexpr int KT = 32, KF = DK / (2 * kUnit<T>), VF = DV / (2 * kUnit<T>);

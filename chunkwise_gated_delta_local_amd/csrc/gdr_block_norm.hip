@@ -2,17 +2,23 @@
 // (include/gdr_mixer.h). A few operations an element: HBM bounds them, so a row is
 // read once and stays in registers between its sums and its outputs. TPR threads share
 // a row, each holding NV pieces of V elements: 16 bytes of the io type, or four elements
-// in bf16 beside a stream in fp32 (in_fours); rows go round the grid, and up to 512 threads a row (forward up to 1,024, one piece each) the next row
-// is on its way while one is worked on, with the parameters in registers. A thread holds
-// one piece where it can: 4,096 rows of 8,192 took the backward pass 276 us with four pieces
-// and 256 threads, 152 with one, 132 with the parameters' sums in LDS. Rows beyond 8,192
-// overflow into scratch all the same (16,384, forward and backward: gated 83 and 260 us, where a
-// copy would take 68 and 113; residual sums 205 and 573, 113 and 181), but for the gated forward pass.
+// in bf16 beside a stream in fp32 (in_fours). Rows go round the grid, and up to 512 threads
+// a row (forward wherever a thread holds eight elements at most) the next row is on its way
+// while one is worked on, with the parameters in registers. A thread holds eight elements
+// where it can, one piece in bf16, two of four otherwise: 4,096 rows of 8,192 took the backward
+// pass 276 us with four pieces and 256 threads, 152 with one, 132 with the parameters' sums in
+// LDS. Rows beyond 8,192 overflow into scratch all the same, 212 to 832 bytes a thread (4,096 rows
+// of 16,384 in bf16, forward and backward: gated 91 and 257 us, where a copy would take 68 and 113;
+// residual sums 198 and 573, 91 and 181), but for the gated forward pass; residual sums' backward
+// pass from 4,097 columns on, 84 to 88 bytes.
 //
-// Measured in bf16, at the rate of a copy (5.92 TB/s) in brackets: gated rows of 128,
-// 2,097,152 of them, 302 us (274), 524,288 backward 113 us (114); residual sums of rows of
-// 4,096, 16,384 of them, with both norms and a gate per channel 103 us (91), backward with a
-// gate per token 188 us (181); 256 rows 5.0 us replayed from a graph.
+// Measured, at the rate of a copy (5.92 TB/s) in brackets. bf16: gated rows of 128, 2,097,152 of
+// them, 279 us (274), 524,288 backward 114 us (114); residual sums of rows of 4,096, 16,384 of them, with
+// both norms and a gate per channel 101 us (91), backward with a gate per token 185 us (181); 256
+// rows 5.0 us replayed from a graph. fp32: gated rows of 128, 1,048,576 of them, 263 us (273), 262,144
+// backward 121 us (114); residual sums of 16,384 rows of 4,096 as above 185 us (181), 8,192 backward
+// 183 us (181). Backward, rows of 1,025 to 2,048 have one workgroup of 256 threads to a compute unit:
+// 32,768 of 2,048 in bf16 gated 160 us (113), residual 252 us (136).
 #include <type_traits>
 
 #include "gdr_norm.hpp"

@@ -83,7 +83,12 @@ gdr_status_t gdr_window_attn_step(const gdr_attn_problem_t* problem, const void*
  * the forward's o (out_dtype) and lse: dq, dk and dv dense like q, k and v. The
  * weights are exp(s - lse); of rows with |lse| beyond 1,024 ln 2, which fp32 holds
  * too coarsely for that, they are formed again from the scores. Below, the
- * rounding of lse leaves a weight within 2^-12 of itself. */
+ * rounding of lse leaves a weight within 2^-12 of itself. A d_o in fp32 beside bf16
+ * inputs is rounded to bf16 first. The workspace holds 12 bytes a token and query
+ * head, that rounded d_o, and with sinks, where there are more tokens than the
+ * window, up to tokens / 256 + 2 num_seqs + 1 partial sums of
+ * min(sinks, seq_len) x num_kv_heads x (head_dim_qk + head_dim_v) floats: gigabytes
+ * for thousands of sinks. */
 gdr_status_t gdr_window_attn_bwd_workspace_size(const gdr_attn_problem_t* problem, size_t* bytes);
 gdr_status_t gdr_window_attn_bwd(const gdr_attn_problem_t* problem, const void* q, const void* k, const void* v,
                                  const void* o, const float* lse, const void* d_o, const int32_t* cu_seqlens_dev,
