@@ -389,7 +389,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_window_dkv(
                  [&](int r) { return row_at(r, g_ld, dv); }, dv, tid);
         if (w == 0) {
             const int r = lane & 31, x = (r * magic) >> 16, g = r - x * rb.HPB;
-            static_assert(QT == 32, "lse and delta of a tile in 64 lanes");
+            static_assert(QT == 32 && NW > 1, "lse and delta of a tile in 64 lanes, top by the next wavefront");
             copy4_to_lds(raw_rsrc(a.rows + 2 * (tok * Nq + head), (uint32_t)((n - 1) * Nq + heads) * 8), R,
                          r < span ? (x * Nq + g) * 8 + 4 * h : kOutside);
         } else if (w == 1) {
